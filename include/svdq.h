@@ -515,6 +515,139 @@ size_t svdq_fp4_linear_workspace_size(int b, int m, int n, int rank);
 int svdq_fp4_linear(const uint16_t* x, const svdq_fp4_layer* layer, int b, void* y, int y_dtype,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ===========================================================================
+ * The product with an epilogue: the element-wise work that follows a linear
+ * layer in a transformer block, done on the fp32 result before its one
+ * rounding to y's type instead of in passes over y:
+ *     v = (the product, the low-rank branch and bias[j], as above)
+ *     a = act(v) for columns j >= act_begin, v for the others
+ *     y[i,j] = residual[i,j] + gate[i / gate_rows, j] * a
+ * A fused projection (QKV columns, then MLP columns) activates only the columns
+ * from act_begin; a block's output projection is gated per sample and added to
+ * the residual stream.
+ *
+ * act (SVDQ_ACT_*):
+ *   NONE       v
+ *   GELU_TANH  0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))
+ *   GELU_ERF   v Phi(v) (absolute error at most 1e-7 |v| before rounding)
+ *   SILU       v / (1 + exp(-v))
+ *   RELU       max(v, 0)
+ * NaN stays NaN in all of them; GELU and SiLU of -inf are NaN.
+ * ========================================================================= */
+enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1, SVDQ_ACT_GELU_ERF = 2, SVDQ_ACT_SILU = 3, SVDQ_ACT_RELU = 4 };
+
+/*   act, act_begin  0 <= act_begin <= n.
+ *   gate            bf16 [ceil(b / gate_rows)][n] or NULL (= 1); any alignment.
+ *   gate_rows       rows that share a gate row; 0 = all b rows share one.
+ *   residual        y's type, row i at residual + i * ldr, or NULL (= 0); element
+ *                   alignment.  It may be y itself (same address and stride);
+ *                   any other overlap with y's elements is refused.
+ *   ldr, ldy        row strides in elements, n .. SVDQ_MAX_DIM, or 0 for n (a
+ *                   column slice of a wider tensor).  Nothing is written
+ *                   between the rows. */
+typedef struct svdq_epilogue {
+  int32_t act, act_begin, gate_rows, ldr, ldy;
+  const uint16_t* gate;
+  const void* residual;
+} svdq_epilogue;
+
+/* Bytes of device workspace svdq_gemm_w4a4_lowrank_up_epi needs (0 for few
+ * rows). */
+size_t svdq_gemm_epi_workspace_size(int b, int n, int m);
+
+/* DEVICE: svdq_gemm_w4a4_lowrank_up with an epilogue (epi NULL: none).  The
+ * integer sums per group are the same exact ones; the groups' fp32 sum may be
+ * taken in another order, so results differ from svdq_gemm_w4a4_lowrank_up's by
+ * rounding.  The order depends only on the shape and the device's CU count.
+ * The 8-bit and NVFP4 forms below are the same for their settings, with the
+ * workspaces of svdq_w8a8_gemm_lowrank_up and svdq_fp4_gemm_lowrank_up. */
+int svdq_gemm_w4a4_lowrank_up_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer* layer,
+                                  const svdq_epilogue* epi, int b, void* y, int y_dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+int svdq_w8a8_gemm_lowrank_up_epi(const int8_t* qx, const uint16_t* ascale, const float* z,
+                                  const svdq_w8a8_layer* layer, const svdq_epilogue* epi, int b, void* y, int y_dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+int svdq_fp4_gemm_lowrank_up_epi(const uint8_t* qx, const uint8_t* ascale, const float* z, const svdq_fp4_layer* layer,
+                                 const svdq_epilogue* epi, int b, void* y, int y_dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* DEVICE: the whole layer with an epilogue: the activation kernels of
+ * svdq_linear (svdq_w8a8_linear, svdq_fp4_linear), then the product above.
+ * Workspace as svdq_linear (svdq_w8a8_linear, svdq_fp4_linear). */
+int svdq_linear_epi(const uint16_t* x, const svdq_layer* layer, const svdq_epilogue* epi, int b, void* y, int y_dtype,
+                    void* workspace, size_t workspace_bytes, void* stream);
+int svdq_w8a8_linear_epi(const uint16_t* x, const svdq_w8a8_layer* layer, const svdq_epilogue* epi, int b, void* y,
+                         int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int svdq_fp4_linear_epi(const uint16_t* x, const svdq_fp4_layer* layer, const svdq_epilogue* epi, int b, void* y,
+                        int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ===========================================================================
+ * INT4 layers grouped by expert: b rows sorted by expert, each expert a layer of
+ * its own with the same m, n and rank, in one pair of launches whose row counts
+ * stay on the device.
+ *   offsets  device int32 [experts + 1], non-decreasing: rows offsets[e] ..
+ *            offsets[e+1]-1 are expert e's (possibly none).  Rows before
+ *            offsets[0] and from offsets[experts] on belong to no expert: no
+ *            output of theirs is written.  Values are clamped to [0, b], so no
+ *            offsets lead outside the b rows; where they decrease, which
+ *            expert's result a row gets is undefined.
+ * ========================================================================= */
+#define SVDQ_MAX_EXPERTS 1024
+
+/* The experts' layers on the device, every tensor of svdq_layer with a leading
+ * expert dimension: smooth_inv fp32 [experts][m] or NULL, qw
+ * [experts][m/64][n][32], wscale fp16 [experts][m/64][n], l1 bf16
+ * [experts][rank][m], l2 bf16 [experts][n][rank] (NULL iff rank == 0), bias bf16
+ * [experts][n] or NULL.  Alignments as svdq_layer. */
+typedef struct svdq_grouped_layer {
+  int32_t experts, m, n, rank, group;
+  const float* smooth_inv;
+  const uint8_t* qw;
+  const uint16_t* wscale;
+  const uint16_t* l1;
+  const uint16_t* l2;
+  const uint16_t* bias;
+} svdq_grouped_layer;
+
+/* DEVICE: svdq_quantize_act_lowrank_down for rows sorted by expert, gathering
+ * them: row i of expert e is x[row_index[i]] with smooth_inv[e] and l1[e].
+ *   x bf16 [x_rows][m]; row_index device int32 [b], or NULL (row i is x[i],
+ *   x_rows >= b); an index outside [0, x_rows) stands for a row of zeros.
+ *   Outputs as svdq_quantize_act_lowrank_down for b rows (codes and scales bit
+ *   for bit its own; z up to the order of its fp32 sum); the entries of rows
+ *   without an expert are left as they were.  No workspace.  layer->qw, wscale,
+ *   l2 and bias are not used. */
+int svdq_grouped_quantize_act_lowrank_down(const uint16_t* x, int x_rows, const int32_t* row_index,
+                                           const int32_t* offsets, const svdq_grouped_layer* layer, int b, uint8_t* qx,
+                                           uint16_t* ascale, float* z, void* stream);
+
+/* DEVICE: the product of rows sorted by expert with their experts' layers, with
+ * the activation of an epilogue (epi NULL: none; its gate and residual must be
+ * NULL, svdq_combine_rows adds the residual).  qx, ascale, z for b rows as
+ * above.  Rows without an expert are neither used nor written.  No workspace.
+ * layer->smooth_inv and l1 are not used. */
+int svdq_grouped_gemm_w4a4_lowrank_up(const uint8_t* qx, const uint16_t* ascale, const float* z,
+                                      const int32_t* offsets, const svdq_grouped_layer* layer,
+                                      const svdq_epilogue* epi, int b, void* y, int y_dtype, void* stream);
+
+/* DEVICE: the two back to back, codes and z in the workspace (256-byte aligned,
+ * >= svdq_grouped_linear_workspace_size(...) bytes, not shared by calls that
+ * overlap in time; no part of it needs clearing). */
+size_t svdq_grouped_linear_workspace_size(int b, int experts, int m, int n, int rank);
+int svdq_grouped_linear(const uint16_t* x, int x_rows, const int32_t* row_index, const int32_t* offsets,
+                        const svdq_grouped_layer* layer, const svdq_epilogue* epi, int b, void* y, int y_dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* DEVICE: the rows of a token brought together again:
+ *     y[t,j] = residual[t,j] + sum_q weight[t,q] rows[index[t,q], j]
+ * summed in fp32 in the order of q and rounded once.
+ *   rows [R][n] in dtype (SVDQ_OUT_BF16 or SVDQ_OUT_F32); index device int32
+ *   [t][k], an index outside [0, R) adding nothing; weight fp32 [t][k] or NULL
+ *   (= 1); residual dtype [t][n] or NULL, may be y itself; y dtype [t][n], apart
+ *   from rows.  Element alignment.  1 <= k <= SVDQ_MAX_EXPERTS. */
+int svdq_combine_rows(const void* rows, int R, int n, int dtype, const int32_t* index, const float* weight, int t,
+                      int k, const void* residual, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,8 @@ SVDQ_GROUP = 64
 SVDQ_MAX_RANK = 256
 SVDQ_MAX_DIM = 1 << 22
 SVDQ_W8A8_MAX_M = 131072
+SVDQ_MAX_EXPERTS = 1024
+ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "gelu_erf": 2, "silu": 3, "relu": 4}  # SVDQ_ACT_*
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsvdq.so")
 
@@ -61,6 +63,19 @@ class svdq_fp4_layer(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("t_x", ctypes.c_float), ("t_w", ctypes.c_float), ("smooth_inv", _vp), ("qw", _vp),
                 ("wscale", _vp), ("l1", _vp), ("l2", _vp), ("bias", _vp)]
+
+
+class svdq_epilogue(ctypes.Structure):
+    """Mirror of ``struct svdq_epilogue`` (device addresses)."""
+    _fields_ = [("act", ctypes.c_int32), ("act_begin", ctypes.c_int32), ("gate_rows", ctypes.c_int32),
+                ("ldr", ctypes.c_int32), ("ldy", ctypes.c_int32), ("gate", _vp), ("residual", _vp)]
+
+
+class svdq_grouped_layer(ctypes.Structure):
+    """Mirror of ``struct svdq_grouped_layer`` (all pointers are device addresses)."""
+    _fields_ = [("experts", ctypes.c_int32), ("m", ctypes.c_int32), ("n", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("smooth_inv", _vp), ("qw", _vp), ("wscale", _vp), ("l1", _vp),
+                ("l2", _vp), ("bias", _vp)]
 
 
 # (name, restype, argtypes) for every exported symbol of include/svdq.h
@@ -118,6 +133,31 @@ SIGNATURES = [
     ("svdq_fp4_linear_workspace_size", _size, [_c_int, _c_int, _c_int, _c_int]),
     ("svdq_fp4_linear", _c_int,
      [_vp, ctypes.POINTER(svdq_fp4_layer), _c_int, _vp, _c_int, _vp, _size, _vp]),
+    ("svdq_gemm_epi_workspace_size", _size, [_c_int, _c_int, _c_int]),
+    ("svdq_gemm_w4a4_lowrank_up_epi", _c_int,
+     [_vp, _vp, _vp, ctypes.POINTER(svdq_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size, _vp]),
+    ("svdq_w8a8_gemm_lowrank_up_epi", _c_int,
+     [_vp, _vp, _vp, ctypes.POINTER(svdq_w8a8_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size,
+      _vp]),
+    ("svdq_fp4_gemm_lowrank_up_epi", _c_int,
+     [_vp, _vp, _vp, ctypes.POINTER(svdq_fp4_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size,
+      _vp]),
+    ("svdq_linear_epi", _c_int,
+     [_vp, ctypes.POINTER(svdq_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size, _vp]),
+    ("svdq_w8a8_linear_epi", _c_int,
+     [_vp, ctypes.POINTER(svdq_w8a8_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size, _vp]),
+    ("svdq_fp4_linear_epi", _c_int,
+     [_vp, ctypes.POINTER(svdq_fp4_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size, _vp]),
+    ("svdq_grouped_quantize_act_lowrank_down", _c_int,
+     [_vp, _c_int, _vp, _vp, ctypes.POINTER(svdq_grouped_layer), _c_int, _vp, _vp, _vp, _vp]),
+    ("svdq_grouped_gemm_w4a4_lowrank_up", _c_int,
+     [_vp, _vp, _vp, _vp, ctypes.POINTER(svdq_grouped_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp]),
+    ("svdq_grouped_linear_workspace_size", _size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    ("svdq_grouped_linear", _c_int,
+     [_vp, _c_int, _vp, _vp, ctypes.POINTER(svdq_grouped_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int,
+      _vp, _size, _vp]),
+    ("svdq_combine_rows", _c_int,
+     [_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp]),
 ]
 
 _lib = None
@@ -440,6 +480,15 @@ def _gemm_operands(qx, ascale, z, layer, b, per_group_scales: bool, record: int,
     return b
 
 
+def _branch_tensors(dev, m, n, rank, l1, l2, smooth_inv, bias):
+    """Checks the tensors every setting's layer has besides its codes and scales."""
+    import torch
+    _dev(l1, "l1", torch.bfloat16, (rank, m), dev)
+    _dev(l2, "l2", torch.bfloat16, (n, rank), dev)
+    _dev(smooth_inv, "smooth_inv", torch.float32, (m,), dev)
+    _dev(bias, "bias", torch.bfloat16, (n,), dev)
+
+
 class DeviceLayer:
     """A prepared layer resident in device memory plus its ``svdq_layer`` struct."""
 
@@ -603,6 +652,21 @@ class DeviceLayer8:
         self.struct = svdq_w8a8_layer(self.m, self.n, self.rank, _ptr(self.smooth_inv), _ptr(self.qw),
                                       _ptr(self.wscale), _ptr(self.l1), _ptr(self.l2), _ptr(self.bias))
 
+    @classmethod
+    def from_tensors(cls, m, n, rank, qw, wscale, l1=None, l2=None, smooth_inv=None, bias=None):
+        import torch
+        dev = qw.device
+        _dev(qw, "qw", torch.int8, (m // SVDQ_GROUP, n, 64), dev)
+        _dev(wscale, "wscale", torch.float16, (n,), dev)
+        _branch_tensors(dev, m, n, rank, l1, l2, smooth_inv, bias)
+        self = cls.__new__(cls)
+        self.m, self.n, self.rank = m, n, rank
+        self.qw, self.wscale, self.l1, self.l2 = qw, wscale, l1, l2
+        self.smooth_inv, self.bias = smooth_inv, bias
+        self.struct = svdq_w8a8_layer(m, n, rank, _ptr(smooth_inv), _ptr(qw), _ptr(wscale), _ptr(l1), _ptr(l2),
+                                      _ptr(bias))
+        return self
+
 
 def svdq_w8a8_act_workspace_size(b: int, m: int, rank: int) -> int:
     return int(lib().svdq_w8a8_act_workspace_size(b, m, rank))
@@ -717,6 +781,23 @@ class DeviceLayerFp4:
                                      _ptr(self.qw), _ptr(self.wscale), _ptr(self.l1), _ptr(self.l2),
                                      _ptr(self.bias))
 
+    @classmethod
+    def from_tensors(cls, m, n, rank, t_x, t_w, qw, wscale, l1=None, l2=None, smooth_inv=None, bias=None):
+        import torch
+        dev = qw.device
+        G = m // SVDQ_GROUP
+        _dev(qw, "qw", torch.uint8, (G, n, 32), dev)
+        _dev(wscale, "wscale", torch.uint8, (G, n, 4), dev)
+        _branch_tensors(dev, m, n, rank, l1, l2, smooth_inv, bias)
+        self = cls.__new__(cls)
+        self.m, self.n, self.rank = m, n, rank
+        self.t_x, self.t_w = float(t_x), float(t_w)
+        self.qw, self.wscale, self.l1, self.l2 = qw, wscale, l1, l2
+        self.smooth_inv, self.bias = smooth_inv, bias
+        self.struct = svdq_fp4_layer(m, n, rank, self.t_x, self.t_w, _ptr(smooth_inv), _ptr(qw), _ptr(wscale),
+                                     _ptr(l1), _ptr(l2), _ptr(bias))
+        return self
+
 
 def svdq_fp4_act_workspace_size(b: int, m: int, rank: int) -> int:
     return int(lib().svdq_fp4_act_workspace_size(b, m, rank))
@@ -775,4 +856,340 @@ def svdq_fp4_linear(x, layer: DeviceLayerFp4, out_dtype=None, y=None, workspace=
     workspace, wsb = _workspace(workspace, svdq_fp4_linear_workspace_size(b, m, layer.n, layer.rank), x.device)
     _check(lib().svdq_fp4_linear(_ptr(x), ctypes.byref(layer.struct), b, _ptr(y), code, _ptr(workspace),
                                  wsb, _stream(stream)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# products with an epilogue: activation, gate and residual before y's one rounding
+# ---------------------------------------------------------------------------
+
+class _On:
+    """Makes a tensor's device current and, with a stream given, that stream, so
+    that tensors allocated inside belong to the stream that uses them.  Enters
+    to the stream's handle."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.contexts = []
+        if torch.cuda.current_device() != device.index:
+            self.contexts.append(torch.cuda.device(device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = (torch.cuda.default_stream(device) if stream == 0
+                          else torch.cuda.ExternalStream(stream, device=device))
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, expected {device}")
+            self.handle = stream.cuda_stream
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+        return False
+
+
+def _rows(t, name: str, dtype, shape, device) -> int:
+    """A GPU matrix whose rows are contiguous, possibly a column slice of a wider
+    one; returns its row stride."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if shape[0] == 0:
+        return shape[1]
+    ld, step = t.stride()
+    if shape[1] > 1 and step != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    if shape[0] == 1:
+        return shape[1]
+    if not shape[1] <= ld <= SVDQ_MAX_DIM:
+        raise ValueError(f"the row stride of {name} must be in [{shape[1]}, {SVDQ_MAX_DIM}], got {ld}")
+    return ld
+
+
+def _epilogue(b: int, n: int, device, y, out_dtype, act, act_begin, gate=None, gate_rows=None, residual=None):
+    """(y, its C-ABI dtype code, the svdq_epilogue struct)."""
+    import torch
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, not {act!r}")
+    if not 0 <= act_begin <= n:
+        raise ValueError(f"act_begin must be in [0, {n}], got {act_begin}")
+    if y is not None and out_dtype is None:
+        out_dtype = y.dtype
+    out = _out_code(out_dtype)
+    dtype = torch.bfloat16 if out == SVDQ_OUT_BF16 else torch.float32
+    if y is None:
+        y, ldy = torch.empty((b, n), dtype=dtype, device=device), n
+    else:
+        ldy = _rows(y, "y", dtype, (b, n), device)
+    ldr = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", dtype, (b, n), device)
+    if gate is not None:
+        if gate_rows is not None and gate_rows < 0:
+            raise ValueError(f"gate_rows must be >= 0, got {gate_rows}")
+        gate_rows = min(gate_rows or b, b)
+        _dev(gate, "gate", torch.bfloat16, (-(-b // gate_rows) if b else 0, n), device)
+    epi = svdq_epilogue(code, act_begin, gate_rows or 0, ldr, ldy, None if gate is None else gate.data_ptr(),
+                        None if residual is None else residual.data_ptr())
+    return y, out, epi
+
+
+def svdq_gemm_epi_workspace_size(b: int, n: int, m: int) -> int:
+    return int(lib().svdq_gemm_epi_workspace_size(b, n, m))
+
+
+def _gemm_epi(fn, size, operands, qx, ascale, z, layer, act, act_begin, gate, gate_rows, residual, b, out_dtype, y,
+              workspace, stream):
+    b = _gemm_operands(qx, ascale, z, layer, b, *operands)
+    device = qx.device
+    with _On(device, stream) as handle:
+        y, code, epi = _epilogue(b, layer.n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
+        workspace, wsb = _workspace(workspace, size(b, layer.n, layer.m), device)
+        _check(fn(_ptr(qx), _ptr(ascale), _ptr(z), ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code,
+                  workspace.data_ptr(), wsb, handle))
+    return y
+
+
+def svdq_gemm_w4a4_lowrank_up_epi(qx, ascale, z, layer: DeviceLayer, act: str = "none", act_begin: int = 0, gate=None,
+                                  gate_rows: Optional[int] = None, residual=None, b: Optional[int] = None,
+                                  out_dtype=None, y=None, workspace=None, stream=None):
+    """y = residual + gate * act(product + bias), the activation in the columns
+    from ``act_begin`` on.
+
+    act: "none", "gelu_tanh", "gelu_erf", "silu" or "relu".  gate: bf16
+    [ceil(b / gate_rows)][n] (gate_rows None: all rows share its one row).
+    residual: [b][n] of y's dtype, possibly ``y`` itself.  y and residual may be
+    column slices of wider tensors."""
+    import torch
+    return _gemm_epi(lib().svdq_gemm_w4a4_lowrank_up_epi, svdq_gemm_epi_workspace_size,
+                     (True, 32, torch.uint8, torch.float16), qx, ascale, z, layer, act, act_begin, gate, gate_rows,
+                     residual, b, out_dtype, y, workspace, stream)
+
+
+def svdq_w8a8_gemm_lowrank_up_epi(qx, ascale, z, layer: DeviceLayer8, act: str = "none", act_begin: int = 0, gate=None,
+                                  gate_rows: Optional[int] = None, residual=None, b: Optional[int] = None,
+                                  out_dtype=None, y=None, workspace=None, stream=None):
+    """The 8-bit setting's product with the epilogue of svdq_gemm_w4a4_lowrank_up_epi."""
+    import torch
+    return _gemm_epi(lib().svdq_w8a8_gemm_lowrank_up_epi, svdq_w8a8_gemm_workspace_size,
+                     (False, 64, torch.int8, torch.float16), qx, ascale, z, layer, act, act_begin, gate, gate_rows,
+                     residual, b, out_dtype, y, workspace, stream)
+
+
+def svdq_fp4_gemm_lowrank_up_epi(qx, ascale, z, layer: DeviceLayerFp4, act: str = "none", act_begin: int = 0, gate=None,
+                                 gate_rows: Optional[int] = None, residual=None, b: Optional[int] = None,
+                                 out_dtype=None, y=None, workspace=None, stream=None):
+    """The NVFP4 setting's product with the epilogue of svdq_gemm_w4a4_lowrank_up_epi."""
+    import torch
+    return _gemm_epi(lib().svdq_fp4_gemm_lowrank_up_epi, svdq_fp4_gemm_workspace_size,
+                     (True, 32, torch.uint8, torch.uint8, (4,)), qx, ascale, z, layer, act, act_begin, gate, gate_rows,
+                     residual, b, out_dtype, y, workspace, stream)
+
+
+def _linear_epi(fn, size, x, layer, act, act_begin, gate, gate_rows, residual, out_dtype, y, workspace, stream):
+    b, m = _input(x)
+    device = layer.qw.device
+    _dev(x, "x", device=device)
+    if m != layer.m:
+        raise ValueError(f"x has {m} channels, the layer {layer.m}")
+    with _On(device, stream) as handle:
+        y, code, epi = _epilogue(b, layer.n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
+        workspace, wsb = _workspace(workspace, size(b, m, layer.n, layer.rank), device)
+        _check(fn(_ptr(x), ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code, workspace.data_ptr(),
+                  wsb, handle))
+    return y
+
+
+def svdq_linear_epi(x, layer: DeviceLayer, act: str = "none", act_begin: int = 0, gate=None,
+                    gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None,
+                    stream=None):
+    """svdq_linear with the epilogue of svdq_gemm_w4a4_lowrank_up_epi (workspace:
+    svdq_linear_workspace_size bytes)."""
+    return _linear_epi(lib().svdq_linear_epi, svdq_linear_workspace_size, x, layer, act, act_begin, gate, gate_rows,
+                       residual, out_dtype, y, workspace, stream)
+
+
+def svdq_w8a8_linear_epi(x, layer: DeviceLayer8, act: str = "none", act_begin: int = 0, gate=None,
+                         gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None,
+                         stream=None):
+    return _linear_epi(lib().svdq_w8a8_linear_epi, svdq_w8a8_linear_workspace_size, x, layer, act, act_begin, gate,
+                       gate_rows, residual, out_dtype, y, workspace, stream)
+
+
+def svdq_fp4_linear_epi(x, layer: DeviceLayerFp4, act: str = "none", act_begin: int = 0, gate=None,
+                        gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None,
+                        stream=None):
+    return _linear_epi(lib().svdq_fp4_linear_epi, svdq_fp4_linear_workspace_size, x, layer, act, act_begin, gate,
+                       gate_rows, residual, out_dtype, y, workspace, stream)
+
+
+# ---------------------------------------------------------------------------
+# INT4 layers grouped by expert
+# ---------------------------------------------------------------------------
+
+class GroupedDeviceLayer:
+    """One prepared INT4 layer per expert, stacked in device memory, plus its
+    ``svdq_grouped_layer`` struct.  hosts: the host dicts of the experts' layers
+    (equal m, n and rank)."""
+
+    def __init__(self, hosts, device="cuda", biases=None, smoothing: bool = True):
+        import torch
+        hosts = list(hosts)
+        if not hosts:
+            raise ValueError("at least one expert is needed")
+        dims = {(int(h["m"]), int(h["n"]), int(h["rank"])) for h in hosts}
+        if len(dims) != 1:
+            raise ValueError(f"the experts' layers have different (m, n, rank): {sorted(dims)}")
+        if biases is not None and len(biases) != len(hosts):
+            raise ValueError(f"{len(biases)} biases for {len(hosts)} experts")
+        m, n, rank = dims.pop()
+        t = lambda key, raw, dt: torch.from_numpy(
+            np.stack([np.ascontiguousarray(h[key]).view(raw) for h in hosts])).to(device=device).view(dt)
+        self._init(len(hosts), m, n, rank, t("qw", np.uint8, torch.uint8), t("wscale", np.int16, torch.float16),
+                   t("l1", np.int16, torch.bfloat16) if rank else None,
+                   t("l2", np.int16, torch.bfloat16) if rank else None,
+                   t("smooth_inv", np.float32, torch.float32) if smoothing else None,
+                   None if biases is None else torch.from_numpy(
+                       np.stack([np.asarray(v, np.uint16).view(np.int16) for v in biases])).to(device=device)
+                   .view(torch.bfloat16))
+
+    def _init(self, experts, m, n, rank, qw, wscale, l1, l2, smooth_inv, bias):
+        import torch
+        dev = qw.device
+        G = m // SVDQ_GROUP
+        _dev(qw, "qw", torch.uint8, (experts, G, n, 32), dev)
+        _dev(wscale, "wscale", torch.float16, (experts, G, n), dev)
+        _dev(l1, "l1", torch.bfloat16, (experts, rank, m), dev)
+        _dev(l2, "l2", torch.bfloat16, (experts, n, rank), dev)
+        _dev(smooth_inv, "smooth_inv", torch.float32, (experts, m), dev)
+        _dev(bias, "bias", torch.bfloat16, (experts, n), dev)
+        self.experts, self.m, self.n, self.rank = experts, m, n, rank
+        self.qw, self.wscale, self.l1, self.l2 = qw, wscale, l1, l2
+        self.smooth_inv, self.bias = smooth_inv, bias
+        self.struct = svdq_grouped_layer(experts, m, n, rank, SVDQ_GROUP, _ptr(smooth_inv), _ptr(qw), _ptr(wscale),
+                                         _ptr(l1), _ptr(l2), _ptr(bias))
+
+    @classmethod
+    def from_tensors(cls, experts, m, n, rank, qw, wscale, l1=None, l2=None, smooth_inv=None, bias=None):
+        self = cls.__new__(cls)
+        self._init(experts, m, n, rank, qw, wscale, l1, l2, smooth_inv, bias)
+        return self
+
+
+def _grouped_rows(x, offsets, layer, row_index):
+    """Checks a grouped layer's inputs; returns (b, x's rows)."""
+    import torch
+    x_rows, m = _input(x)
+    device = layer.qw.device
+    _dev(x, "x", device=device)
+    if m != layer.m:
+        raise ValueError(f"x has {m} channels, the layer {layer.m}")
+    _dev(offsets, "offsets", torch.int32, (layer.experts + 1,), device)
+    if row_index is None:
+        return x_rows, x_rows
+    if row_index.dim() != 1:
+        raise ValueError(f"row_index must be 1-D, got shape {tuple(row_index.shape)}")
+    _dev(row_index, "row_index", torch.int32, None, device)
+    return row_index.shape[0], x_rows
+
+
+def svdq_grouped_quantize_act_lowrank_down(x, offsets, layer: GroupedDeviceLayer, row_index=None, qx=None, ascale=None,
+                                           z=None, stream=None):
+    """Returns (qx uint8 [m/64][b][32], ascale fp16 [m/64][b], z fp32 [b][rank] or
+    None) of the rows x[row_index] (b of them, sorted by expert: offsets int32
+    [experts + 1]); rows without an expert are not written."""
+    import torch
+    b, x_rows = _grouped_rows(x, offsets, layer, row_index)
+    dev, G = x.device, layer.m // SVDQ_GROUP
+    with _On(dev, stream) as handle:
+        if qx is None:
+            qx = torch.empty((G, b, 32), dtype=torch.uint8, device=dev)
+        if ascale is None:
+            ascale = torch.empty((G, b), dtype=torch.float16, device=dev)
+        if z is None and layer.rank > 0:
+            z = torch.empty((b, layer.rank), dtype=torch.float32, device=dev)
+        _dev(qx, "qx", torch.uint8, (G, b, 32), dev)
+        _dev(ascale, "ascale", torch.float16, (G, b), dev)
+        _dev(z, "z", torch.float32, (b, layer.rank), dev)
+        _check(lib().svdq_grouped_quantize_act_lowrank_down(
+            _ptr(x), x_rows, _ptr(row_index), _ptr(offsets), ctypes.byref(layer.struct), b, _ptr(qx), _ptr(ascale),
+            _ptr(z), handle))
+    return qx, ascale, z
+
+
+def svdq_grouped_gemm_w4a4_lowrank_up(qx, ascale, z, offsets, layer: GroupedDeviceLayer, act: str = "none",
+                                      act_begin: int = 0, out_dtype=None, y=None, stream=None):
+    """The product of rows sorted by expert with their experts' layers and the
+    activation of svdq_gemm_w4a4_lowrank_up_epi; rows without an expert are not
+    written."""
+    import torch
+    b = _gemm_operands(qx, ascale, z, layer, None, True, 32, torch.uint8, torch.float16)
+    dev = qx.device
+    _dev(offsets, "offsets", torch.int32, (layer.experts + 1,), dev)
+    with _On(dev, stream) as handle:
+        y, code, epi = _epilogue(b, layer.n, dev, y, out_dtype, act, act_begin)
+        _check(lib().svdq_grouped_gemm_w4a4_lowrank_up(
+            _ptr(qx), _ptr(ascale), _ptr(z), _ptr(offsets), ctypes.byref(layer.struct), ctypes.byref(epi), b,
+            y.data_ptr(), code, handle))
+    return y
+
+
+def svdq_grouped_linear_workspace_size(b: int, experts: int, m: int, n: int, rank: int) -> int:
+    return int(lib().svdq_grouped_linear_workspace_size(b, experts, m, n, rank))
+
+
+def svdq_grouped_linear(x, offsets, layer: GroupedDeviceLayer, row_index=None, act: str = "none", act_begin: int = 0,
+                        out_dtype=None, y=None, workspace=None, stream=None):
+    """act(layer_e(x[row_index[i]])) for row i of expert e: rows offsets[e] ..
+    offsets[e+1]-1 of b = len(row_index) (all of x's without one).  The other rows
+    of y are not written (uninitialised in a y allocated here)."""
+    b, x_rows = _grouped_rows(x, offsets, layer, row_index)
+    dev = x.device
+    with _On(dev, stream) as handle:
+        y, code, epi = _epilogue(b, layer.n, dev, y, out_dtype, act, act_begin)
+        workspace, wsb = _workspace(
+            workspace, svdq_grouped_linear_workspace_size(b, layer.experts, layer.m, layer.n, layer.rank), dev)
+        _check(lib().svdq_grouped_linear(
+            _ptr(x), x_rows, _ptr(row_index), _ptr(offsets), ctypes.byref(layer.struct), ctypes.byref(epi), b,
+            y.data_ptr(), code, workspace.data_ptr(), wsb, handle))
+    return y
+
+
+def svdq_combine_rows(rows, index, weight=None, residual=None, out_dtype=None, y=None, stream=None):
+    """y[t] = residual[t] + sum_q weight[t, q] rows[index[t, q]]: rows [R][n]
+    (bf16 or fp32), index int32 [t][k] (outside [0, R): nothing is added), weight
+    fp32 [t][k] (None: ones), residual [t][n] of rows' dtype, possibly ``y``
+    itself."""
+    import torch
+    _dev(rows, "rows")
+    if rows.dim() != 2 or rows.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"rows must be a bf16 or fp32 matrix, got {rows.dtype} {tuple(rows.shape)}")
+    if out_dtype is not None and out_dtype != rows.dtype:
+        raise ValueError(f"y has the dtype of rows ({rows.dtype}), not {out_dtype}")
+    dev, (R, n) = rows.device, rows.shape
+    _dev(index, "index", torch.int32, None, dev)
+    if index.dim() != 2:
+        raise ValueError(f"index must be 2-D [t][k], got shape {tuple(index.shape)}")
+    t, k = index.shape
+    _dev(weight, "weight", torch.float32, (t, k), dev)
+    _dev(residual, "residual", rows.dtype, (t, n), dev)
+    with _On(dev, stream) as handle:
+        if y is None:
+            y = torch.empty((t, n), dtype=rows.dtype, device=dev)
+        _dev(y, "y", rows.dtype, (t, n), dev)
+        _check(lib().svdq_combine_rows(_ptr(rows), R, n, _out_code(rows.dtype), _ptr(index), _ptr(weight), t, k,
+                                       _ptr(residual), _ptr(y), handle))
     return y

@@ -11,6 +11,7 @@ import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,9 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsvdq.so")
 
-HOST_SOURCES = ["api.cpp", "prep.cpp", "bundle.cpp", "plan.cpp"]
-HIP_SOURCES = ["act_kernels.hip", "gemm_kernels.hip", "scratch.hip"]
-HEADERS = ["internal.h", "device_common.h"]
+HOST_SOURCES = ["api.cpp", "epi_api.cpp", "prep.cpp", "bundle.cpp", "plan.cpp"]
+HIP_SOURCES = ["act_kernels.hip", "gemm_kernels.hip", "epi_kernels.hip", "rows_kernels.hip", "group_kernels.hip",
+               "scratch.hip"]
+HEADERS = ["internal.h", "checks.h", "device_common.h", "quant.h", "epilogue.h", "grouped.h", "gemm_body.h", "launch.h"]
 
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
@@ -99,15 +101,18 @@ def build(verbose: bool = False) -> str:
     if not os.path.exists(HIPCC):
         raise RuntimeError(f"hipcc not found at {HIPCC}")
     os.makedirs(BUILD, exist_ok=True)
-    objs = []
-    for src in HOST_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
-        objs.append(obj)
-    for src in HIP_SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        _compile_kernels(src, obj, verbose)
-        objs.append(obj)
+    jobs = [(src, os.path.join(BUILD, src + ".o")) for src in HIP_SOURCES + HOST_SOURCES]
+
+    def one(job):
+        src, obj = job
+        if src in HIP_SOURCES:
+            _compile_kernels(src, obj, verbose)
+        else:
+            _run(["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
+
+    with ThreadPoolExecutor(max_workers=4) as pool:
+        list(pool.map(one, jobs))
+    objs = [obj for _, obj in jobs]
     tmp = LIB + ".tmp"
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs, "-lpthread"], verbose)
     os.replace(tmp, LIB)

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <vector>
 
+#include "checks.h"
 #include "internal.h"
 
 namespace svdq {
@@ -63,30 +64,7 @@ ActPlan act_plan(int b, int m, int rank) {
   return p;
 }
 
-}  // namespace svdq
-
-using namespace svdq;
-
-namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-#define REQUIRE(cond, code, ...)  \
-  do {                            \
-    if (!(cond)) {                \
-      set_error(__VA_ARGS__);     \
-      return (code);              \
-    }                             \
-  } while (0)
-
-bool all_finite(const float* p, size_t count) {
-  for (size_t i = 0; i < count; ++i)
-    if (!std::isfinite(p[i])) return false;
-  return true;
-}
+// ---- checks and workspace layouts shared by the entry points (checks.h) --------
 
 int check_group(int m, int group) {
   REQUIRE(group == SVDQ_GROUP, SVDQ_ERR_UNSUPPORTED, "group must be %d (got %d)", SVDQ_GROUP, group);
@@ -94,45 +72,6 @@ int check_group(int m, int group) {
           "m must be a positive multiple of %d (got %d)", SVDQ_GROUP, m);
   REQUIRE(m <= SVDQ_MAX_DIM, SVDQ_ERR_UNSUPPORTED, "m must be <= %d (got %d)", SVDQ_MAX_DIM, m);
   return SVDQ_OK;
-}
-
-// Arguments shared by the preparation entry points.
-int check_prepare(const float* W, const float* act_amax, int m, int n, int rank, int group, const uint8_t* qw,
-                  const uint16_t* wscale, const uint16_t* l1, const uint16_t* l2, const float* lambda,
-                  const float* smooth_inv) {
-  int st = check_group(m, group);
-  if (st) return st;
-  REQUIRE(n >= 1, SVDQ_ERR_INVALID_ARG, "n must be >= 1 (got %d)", n);
-  REQUIRE(n <= SVDQ_MAX_DIM, SVDQ_ERR_UNSUPPORTED, "n must be <= %d (got %d)", SVDQ_MAX_DIM, n);
-  REQUIRE(W && qw && wscale && lambda && smooth_inv, SVDQ_ERR_INVALID_ARG,
-          "W, qw, wscale, lambda and smooth_inv must not be NULL");
-  REQUIRE(rank >= 0 && rank <= SVDQ_MAX_RANK, SVDQ_ERR_UNSUPPORTED, "rank must be in [0, %d] (got %d)",
-          SVDQ_MAX_RANK, rank);
-  REQUIRE(rank <= std::min(m, n), SVDQ_ERR_INVALID_ARG, "rank %d exceeds min(m, n) = %d", rank, std::min(m, n));
-  REQUIRE(rank == 0 || (l1 && l2), SVDQ_ERR_INVALID_ARG, "l1 / l2 must not be NULL when rank > 0");
-  REQUIRE(all_finite(W, (size_t)m * n), SVDQ_ERR_NONFINITE, "W holds NaN or Inf");
-  if (act_amax) {
-    REQUIRE(all_finite(act_amax, (size_t)m), SVDQ_ERR_NONFINITE, "act_amax holds NaN or Inf");
-    for (int k = 0; k < m; ++k) REQUIRE(act_amax[k] >= 0.0f, SVDQ_ERR_INVALID_ARG, "act_amax[%d] is negative", k);
-  }
-  return SVDQ_OK;
-}
-
-// Copy a host candidate to the caller's buffers (l1 transposed [rank][m], l2
-// transposed [n][rank]).
-void export_layer(const HostLayer& L, int m, int n, int rank, uint8_t* qw, uint16_t* wscale, uint16_t* l1,
-                  uint16_t* l2, float* lambda, float* smooth_inv, float* residual) {
-  std::memcpy(qw, L.qw.data(), L.qw.size());
-  std::memcpy(wscale, L.wscale.data(), sizeof(uint16_t) * L.wscale.size());
-  std::memcpy(lambda, L.lam32.data(), sizeof(float) * m);
-  std::memcpy(smooth_inv, L.inv32.data(), sizeof(float) * m);
-  if (rank > 0) {
-    for (int i = 0; i < m; ++i)
-      for (int t = 0; t < rank; ++t) l1[(size_t)t * m + i] = L.l1b[(size_t)i * rank + t];
-    for (int t = 0; t < rank; ++t)
-      for (int j = 0; j < n; ++j) l2[(size_t)j * rank + t] = L.l2b[(size_t)t * n + j];
-  }
-  if (residual) std::memcpy(residual, L.r32.data(), sizeof(float) * L.r32.size());
 }
 
 int hip_status(int err, const char* what) {
@@ -144,10 +83,6 @@ int hip_status(int err, const char* what) {
   set_error("%s: HIP error %d (%s)", what, err, hip_error_name(err));
   return SVDQ_ERR_HIP;
 }
-
-struct LinearWorkspace {
-  size_t qx_off, as_off, z_off, zpart_off, gemm_off, total;
-};
 
 // device-independent upper bound of the GEMM kernel's workspace
 size_t gemm_ws_bytes(int b, int n, int m) {
@@ -309,6 +244,81 @@ int check_y(void* y, int y_dtype, int b) {
   return SVDQ_OK;
 }
 
+// Checks shared by svdq_linear and svdq_linear_noalloc (everything but the
+// workspace).  Sets *done when there is nothing to launch (b == 0).
+int check_linear(const uint16_t* x, const svdq_layer* layer, int b, void* y, int y_dtype, bool* done) {
+  *done = false;
+  int st = check_layer(layer);
+  if (st) return st;
+  REQUIRE(b >= 0, SVDQ_ERR_INVALID_ARG, "b must be >= 0 (got %d)", b);
+  REQUIRE(b <= SVDQ_MAX_DIM, SVDQ_ERR_UNSUPPORTED, "b must be <= %d (got %d)", SVDQ_MAX_DIM, b);
+  st = check_y(y, y_dtype, b);
+  if (st) return st;
+  if (b == 0) {
+    *done = true;
+    return SVDQ_OK;
+  }
+  REQUIRE(x != nullptr, SVDQ_ERR_INVALID_ARG, "x must not be NULL");
+  REQUIRE(aligned16(x), SVDQ_ERR_ALIGNMENT, "x must be 16-byte aligned");
+  if (layer->smooth_inv)
+    REQUIRE(aligned16(layer->smooth_inv), SVDQ_ERR_ALIGNMENT, "smooth_inv must be 16-byte aligned");
+  if (layer->rank > 0) {
+    REQUIRE(layer->l1 != nullptr, SVDQ_ERR_INVALID_ARG, "layer l1 must not be NULL when rank > 0");
+    REQUIRE(aligned16(layer->l1), SVDQ_ERR_ALIGNMENT, "layer l1 must be 16-byte aligned");
+  }
+  return SVDQ_OK;
+}
+
+}  // namespace svdq
+
+using namespace svdq;
+
+namespace {
+
+bool all_finite(const float* p, size_t count) {
+  for (size_t i = 0; i < count; ++i)
+    if (!std::isfinite(p[i])) return false;
+  return true;
+}
+
+// Arguments shared by the preparation entry points.
+int check_prepare(const float* W, const float* act_amax, int m, int n, int rank, int group, const uint8_t* qw,
+                  const uint16_t* wscale, const uint16_t* l1, const uint16_t* l2, const float* lambda,
+                  const float* smooth_inv) {
+  int st = check_group(m, group);
+  if (st) return st;
+  REQUIRE(n >= 1, SVDQ_ERR_INVALID_ARG, "n must be >= 1 (got %d)", n);
+  REQUIRE(n <= SVDQ_MAX_DIM, SVDQ_ERR_UNSUPPORTED, "n must be <= %d (got %d)", SVDQ_MAX_DIM, n);
+  REQUIRE(W && qw && wscale && lambda && smooth_inv, SVDQ_ERR_INVALID_ARG,
+          "W, qw, wscale, lambda and smooth_inv must not be NULL");
+  REQUIRE(rank >= 0 && rank <= SVDQ_MAX_RANK, SVDQ_ERR_UNSUPPORTED, "rank must be in [0, %d] (got %d)",
+          SVDQ_MAX_RANK, rank);
+  REQUIRE(rank <= std::min(m, n), SVDQ_ERR_INVALID_ARG, "rank %d exceeds min(m, n) = %d", rank, std::min(m, n));
+  REQUIRE(rank == 0 || (l1 && l2), SVDQ_ERR_INVALID_ARG, "l1 / l2 must not be NULL when rank > 0");
+  REQUIRE(all_finite(W, (size_t)m * n), SVDQ_ERR_NONFINITE, "W holds NaN or Inf");
+  if (act_amax) {
+    REQUIRE(all_finite(act_amax, (size_t)m), SVDQ_ERR_NONFINITE, "act_amax holds NaN or Inf");
+    for (int k = 0; k < m; ++k) REQUIRE(act_amax[k] >= 0.0f, SVDQ_ERR_INVALID_ARG, "act_amax[%d] is negative", k);
+  }
+  return SVDQ_OK;
+}
+
+// Copy a host candidate to the caller's buffers (l1 transposed [rank][m], l2
+// transposed [n][rank]).
+void export_layer(const HostLayer& L, int m, int n, int rank, uint8_t* qw, uint16_t* wscale, uint16_t* l1,
+                  uint16_t* l2, float* lambda, float* smooth_inv, float* residual) {
+  std::memcpy(qw, L.qw.data(), L.qw.size());
+  std::memcpy(wscale, L.wscale.data(), sizeof(uint16_t) * L.wscale.size());
+  std::memcpy(lambda, L.lam32.data(), sizeof(float) * m);
+  std::memcpy(smooth_inv, L.inv32.data(), sizeof(float) * m);
+  if (rank > 0) {
+    for (int i = 0; i < m; ++i)
+      for (int t = 0; t < rank; ++t) l1[(size_t)t * m + i] = L.l1b[(size_t)i * rank + t];
+    for (int t = 0; t < rank; ++t)
+      for (int j = 0; j < n; ++j) l2[(size_t)j * rank + t] = L.l2b[(size_t)t * n + j];
+  }
+  if (residual) std::memcpy(residual, L.r32.data(), sizeof(float) * L.r32.size());
+}
 
 }  // namespace
 
@@ -598,31 +608,6 @@ static int run_linear(const uint16_t* x, const svdq_layer* layer, int b, void* y
   }
   return hip_status(launch_gemm_up(qx, as, z, *layer, b, y, y_dtype, ws + w.gemm_off, stream),
                     "gemm_w4a4_lowrank_up");
-}
-
-// Checks shared by svdq_linear and svdq_linear_noalloc (everything but the
-// workspace).  Sets *done when there is nothing to launch (b == 0).
-static int check_linear(const uint16_t* x, const svdq_layer* layer, int b, void* y, int y_dtype, bool* done) {
-  *done = false;
-  int st = check_layer(layer);
-  if (st) return st;
-  REQUIRE(b >= 0, SVDQ_ERR_INVALID_ARG, "b must be >= 0 (got %d)", b);
-  REQUIRE(b <= SVDQ_MAX_DIM, SVDQ_ERR_UNSUPPORTED, "b must be <= %d (got %d)", SVDQ_MAX_DIM, b);
-  st = check_y(y, y_dtype, b);
-  if (st) return st;
-  if (b == 0) {
-    *done = true;
-    return SVDQ_OK;
-  }
-  REQUIRE(x != nullptr, SVDQ_ERR_INVALID_ARG, "x must not be NULL");
-  REQUIRE(aligned16(x), SVDQ_ERR_ALIGNMENT, "x must be 16-byte aligned");
-  if (layer->smooth_inv)
-    REQUIRE(aligned16(layer->smooth_inv), SVDQ_ERR_ALIGNMENT, "smooth_inv must be 16-byte aligned");
-  if (layer->rank > 0) {
-    REQUIRE(layer->l1 != nullptr, SVDQ_ERR_INVALID_ARG, "layer l1 must not be NULL when rank > 0");
-    REQUIRE(aligned16(layer->l1), SVDQ_ERR_ALIGNMENT, "layer l1 must be 16-byte aligned");
-  }
-  return SVDQ_OK;
 }
 
 int svdq_linear(const uint16_t* x, const svdq_layer* layer, int b, void* y, int y_dtype,

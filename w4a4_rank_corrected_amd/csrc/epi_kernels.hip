@@ -1,0 +1,135 @@
+// The tiled product (gemm_body.h) with the epilogue of epilogue.h, for one
+// layer in the INT4, 8-bit and NVFP4 settings, and for INT4 layers grouped by
+// expert; and the choice between it and the row kernel.
+#include <hip/hip_runtime.h>
+
+#include "gemm_body.h"
+#include "launch.h"
+
+#pragma clang fp contract(off)
+
+namespace svdq {
+namespace {
+
+using namespace dev;
+
+template <class C, bool OUT_BF16, int FMT, bool SK>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE))) void gemm_epi_kernel(
+    const uint8_t* __restrict__ qx, const uint16_t* __restrict__ ascale, const float* __restrict__ z, Operands L, int b,
+    int G, int tiles_m, int tiles_n, SplitK sk, float txw, EpiArgs ep) {
+  gemm_up_body<C, OUT_BF16, FMT, SK, kTileEpi>(qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, G, L.rank, tiles_m,
+                                               tiles_n, nullptr, sk, txw, ep);
+}
+
+// One tile of one expert per workgroup; the workgroups past the last tile end.
+template <class C, bool OUT_BF16>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE))) void gemm_grouped_kernel(
+    const uint8_t* __restrict__ qx, const uint16_t* __restrict__ ascale, const float* __restrict__ z, Operands L, int b,
+    int G, int tiles_n, Groups groups, EpiArgs ep) {
+  const GroupTile g = find_tile<C::TM>(groups.offsets, groups.experts, b, tiles_n, (int)blockIdx.x,
+                                       [](int d, int T) { return xcd_range(d, T); });
+  if (!g.live) return;
+  const size_t e = (size_t)g.expert;
+  gemm_up_body<C, OUT_BF16, kFmtInt4, false, kTileGrouped>(
+      qx, ascale, z, L.qw + e * G * L.n * 32, L.wscale + e * G * L.n, L.rank > 0 ? L.l2 + e * L.n * L.rank : nullptr,
+      L.bias ? L.bias + e * L.n : nullptr, b, L.n, G, L.rank, 0, tiles_n, nullptr, SplitK{0, 0, 1, 0, nullptr}, 1.0f, ep,
+      g);
+}
+
+template <bool OUT_BF16, int FMT>
+int launch_tiles(const uint8_t* qx, const uint16_t* ascale, const float* z, const Operands& L, int b,
+                 const GemmPlan& plan, const EpiArgs& ep, void* ws, hipStream_t st, float txw) {
+  SplitK sk{0, 0, 1, 0, nullptr};
+  if (plan.split) {
+    sk.P = plan.split_grid;
+    sk.T = plan.split_tiles;
+    sk.k = plan.pieces;
+    sk.lr = L.rank > 0 ? kLowRankPieceGroups : 0;
+    sk.partials = reinterpret_cast<float*>(ws);
+  }
+  auto run = [&](auto cfg) {
+    using C = decltype(cfg);
+    auto gemm = [&](auto kernel) {
+      return launch_checked(kernel, plan.grid, C::NT, st, qx, ascale, z, L, b, plan.G, plan.tiles_m, plan.tiles_n, sk,
+                            txw, ep);
+    };
+    if constexpr (FMT == kFmtFp4) {
+      if (plan.split) return (int)hipErrorInvalidValue;  // NVFP4 tiles are never split
+      return gemm(gemm_epi_kernel<C, OUT_BF16, FMT, false>);
+    } else {
+      if (!plan.split) return gemm(gemm_epi_kernel<C, OUT_BF16, FMT, false>);
+      const int status = gemm(gemm_epi_kernel<C, OUT_BF16, FMT, true>);
+      if (status != 0) return status;
+      constexpr int UNITS = C::TM * C::TN / 4;
+      return launch_checked(splitk_reduce_kernel<C, FMT, OUT_BF16, true>,
+                            (int)(((long long)sk.T * UNITS + 255) / 256), 256, st, (const float*)sk.partials, sk.T, sk.k,
+                            plan.tiles_m, plan.tiles_n, b, L.n, ascale, L.wscale,
+                            FMT == kFmtInt8 && L.rank > 0 ? 1 : 0, L.bias, (void*)nullptr, ep);
+    }
+  };
+  if constexpr (FMT == kFmtInt8) return run(Cfg8{});
+  if constexpr (FMT == kFmtFp4) return run(CfgF4{});
+  if constexpr (FMT == kFmtInt4) return plan.tile_n == CfgN::TN ? run(CfgN{}) : run(Cfg{});
+}
+
+template <int FMT>
+int launch_tiles_typed(const uint8_t* qx, const uint16_t* ascale, const float* z, const Operands& L, int m, int b,
+                       int y_dtype, const EpiArgs& ep, void* ws, void* stream, float txw) {
+  const GemmPlan plan = gemm_plan(b, L.n, m, device_cus(), FMT);
+  hipStream_t st = (hipStream_t)stream;
+  return y_dtype == SVDQ_OUT_BF16 ? launch_tiles<true, FMT>(qx, ascale, z, L, b, plan, ep, ws, st, txw)
+                                  : launch_tiles<false, FMT>(qx, ascale, z, L, b, plan, ep, ws, st, txw);
+}
+
+template <class C>
+int launch_grouped_tiles(const uint8_t* qx, const uint16_t* ascale, const float* z, const Operands& L, int G,
+                         const Groups& groups, int b, int y_dtype, const EpiArgs& ep, hipStream_t st) {
+  const long long tiles_n = (L.n + C::TN - 1) / C::TN;
+  const long long grid = grouped_row_blocks(b, groups.experts, C::TM) * tiles_n;
+  if (grid > 0x7FFFFFFF) return (int)hipErrorInvalidValue;
+  auto go = [&](auto kernel) {
+    return launch_checked(kernel, (int)grid, C::NT, st, qx, ascale, z, L, b, G, (int)tiles_n, groups, ep);
+  };
+  return y_dtype == SVDQ_OUT_BF16 ? go(gemm_grouped_kernel<C, true>) : go(gemm_grouped_kernel<C, false>);
+}
+
+}  // namespace
+
+int launch_gemm_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer& L, int b, int y_dtype,
+                    const EpiArgs& ep, void* ws, void* stream) {
+  if (b <= kRowsMax) {
+    const RowsArgs a{qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, L.m / SVDQ_GROUP, L.rank, Groups{nullptr, 0}, ep};
+    return launch_gemm_rows(a, b <= 16 ? 1 : (b <= 32 ? 2 : 4), y_dtype, stream);
+  }
+  const Operands o{L.qw, L.wscale, L.l2, L.bias, L.n, L.rank};
+  return launch_tiles_typed<kFmtInt4>(qx, ascale, z, o, L.m, b, y_dtype, ep, ws, stream, 1.0f);
+}
+
+int launch_gemm8_epi(const int8_t* qx, const uint16_t* ascale, const float* z, const svdq_w8a8_layer& L, int b,
+                     int y_dtype, const EpiArgs& ep, void* ws, void* stream) {
+  const Operands o{reinterpret_cast<const uint8_t*>(L.qw), L.wscale, L.l2, L.bias, L.n, L.rank};
+  return launch_tiles_typed<kFmtInt8>(reinterpret_cast<const uint8_t*>(qx), ascale, z, o, L.m, b, y_dtype, ep, ws,
+                                      stream, 1.0f);
+}
+
+int launch_gemm_fp4_epi(const uint8_t* qx, const uint8_t* ascale, const float* z, const svdq_fp4_layer& L, int b,
+                        int y_dtype, const EpiArgs& ep, void* ws, void* stream) {
+  const Operands o{L.qw, reinterpret_cast<const uint16_t*>(L.wscale), L.l2, L.bias, L.n, L.rank};
+  return launch_tiles_typed<kFmtFp4>(qx, reinterpret_cast<const uint16_t*>(ascale), z, o, L.m, b, y_dtype, ep, ws,
+                                     stream, L.t_x * L.t_w);
+}
+
+int launch_grouped_gemm(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_grouped_layer& L,
+                        const int32_t* offsets, int b, int y_dtype, const EpiArgs& ep, void* stream) {
+  const Groups groups{offsets, L.experts};
+  const int G = L.m / SVDQ_GROUP;
+  const int mean = (b + L.experts - 1) / L.experts;  // rows an expert gets on average
+  if (mean <= kRowsMax) {
+    const RowsArgs a{qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, G, L.rank, groups, ep};
+    return launch_gemm_rows(a, mean <= 16 ? 1 : (mean <= 32 ? 2 : 4), y_dtype, stream);
+  }
+  const Operands o{L.qw, L.wscale, L.l2, L.bias, L.n, L.rank};
+  return launch_grouped_tiles<Cfg>(qx, ascale, z, o, G, groups, b, y_dtype, ep, (hipStream_t)stream);
+}
+
+}  // namespace svdq

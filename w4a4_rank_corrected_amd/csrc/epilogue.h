@@ -1,0 +1,164 @@
+// The epilogue of the products with an epilogue (device code): activation,
+// gate and residual applied to the fp32 result (bias already added), then one
+// rounding to y's type.
+//
+//   a = act(v) in columns j >= act_begin, v in the others
+//   y = residual[i][j] + gate[i / gate_rows][j] * a
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "device_common.h"
+#include "internal.h"
+
+#pragma clang fp contract(off)
+
+namespace svdq {
+namespace dev {
+
+// exp(x) as 2^(x log2 e): one rounding of the argument (an absolute error of
+// |x| 2^-24 in x, the relative error of the result) and v_exp_f32.  Results
+// below 2^-126 are flushed to zero.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
+// 1/x to one ulp (v_rcp_f32); 1/inf = 0.
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// GELU in its tanh form, 0.5 v (1 + tanh(u)), u = sqrt(2/pi) (v + 0.044715 v^3),
+// as v / (1 + exp(-2 u)): no cancellation where tanh(u) nears -1.
+__device__ __forceinline__ float gelu_tanh(float v) {
+  const float v2 = v * v;
+  const float u2 = v * __builtin_fmaf(v2, -2.0f * 0.7978845608028654f * 0.044715f, -2.0f * 0.7978845608028654f);  // -2 u
+  return v * fast_rcp(1.0f + fast_exp(u2));
+}
+
+// GELU with the normal distribution's integral, v Phi(v), Phi(v) = erfc(-v / sqrt 2) / 2,
+// from Hastings' approximation (Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26): erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x)
+// for x >= 0, absolute error at most 1.5e-7 (an error of 0.75e-7 |v| in the result).
+__device__ __forceinline__ float gelu_erf(float v) {
+  const float x = fabsf(v) * 0.70710678118654752f;
+  const float t = fast_rcp(__builtin_fmaf(0.3275911f, x, 1.0f));
+  float p = 0.5f * 1.061405429f;
+  p = __builtin_fmaf(p, t, 0.5f * -1.453152027f);
+  p = __builtin_fmaf(p, t, 0.5f * 1.421413741f);
+  p = __builtin_fmaf(p, t, 0.5f * -0.284496736f);
+  p = __builtin_fmaf(p, t, 0.5f * 0.254829592f);
+  const float h = p * t * __builtin_amdgcn_exp2f(x * x * -1.44269504088896341f);  // Phi(-|v|)
+  return v * (v < 0.0f ? h : 1.0f - h);
+}
+
+__device__ __forceinline__ float silu(float v) { return v * fast_rcp(1.0f + fast_exp(-v)); }
+
+// NaN stays NaN
+__device__ __forceinline__ float relu(float v) { return v < 0.0f ? 0.0f : v; }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float v) {
+  if constexpr (ACT == SVDQ_ACT_GELU_TANH) return gelu_tanh(v);
+  if constexpr (ACT == SVDQ_ACT_GELU_ERF) return gelu_erf(v);
+  if constexpr (ACT == SVDQ_ACT_SILU) return silu(v);
+  if constexpr (ACT == SVDQ_ACT_RELU) return relu(v);
+  return v;
+}
+
+// f(integral_constant<int, ACT>) for the epilogue's activation (a wave-uniform
+// choice made once, outside the loops over elements); nothing for none.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == SVDQ_ACT_GELU_TANH)
+    f(std::integral_constant<int, SVDQ_ACT_GELU_TANH>{});
+  else if (act == SVDQ_ACT_GELU_ERF)
+    f(std::integral_constant<int, SVDQ_ACT_GELU_ERF>{});
+  else if (act == SVDQ_ACT_SILU)
+    f(std::integral_constant<int, SVDQ_ACT_SILU>{});
+  else if (act == SVDQ_ACT_RELU)
+    f(std::integral_constant<int, SVDQ_ACT_RELU>{});
+}
+
+// Four consecutive columns j .. j+3 of a bf16 or fp32 row as floats.  `vec`:
+// the row's vectors are aligned; columns >= n read as zero.
+template <bool BF16>
+__device__ __forceinline__ f32x4 load4(const void* row, int j, int n, bool vec) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (BF16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + j;
+    if (vec && j + 3 < n) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      v = f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < n) v[e] = __uint_as_float((uint32_t)p[e] << 16);
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(row) + j;
+    if (vec && j + 3 < n) {
+      v = *reinterpret_cast<const f32x4*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < n) v[e] = p[e];
+    }
+  }
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store4(void* row, int j, int n, bool vec, const f32x4& o) {
+  if constexpr (BF16) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(row) + j;
+    if (vec && j + 3 < n) {
+      *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < n) p[e] = bf16_bits(o[e]);
+    }
+  } else {
+    float* p = reinterpret_cast<float*>(row) + j;
+    if (vec && j + 3 < n) {
+      *reinterpret_cast<f32x4*>(p) = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < n) p[e] = o[e];
+    }
+  }
+}
+
+// Row `i` of a matrix of `BF16 ? bf16 : fp32` with row stride ld.
+template <bool BF16>
+__device__ __forceinline__ const void* row_of(const void* base, int i, int ld) {
+  return reinterpret_cast<const uint8_t*>(base) + (size_t)i * (size_t)ld * (BF16 ? 2 : 4);
+}
+template <bool BF16>
+__device__ __forceinline__ void* row_of(void* base, int i, int ld) {
+  return reinterpret_cast<uint8_t*>(base) + (size_t)i * (size_t)ld * (BF16 ? 2 : 4);
+}
+
+// The whole epilogue of four consecutive outputs of row i (v without the bias).
+template <bool OUT_BF16>
+__device__ __forceinline__ void finish_unit(f32x4 v, int i, int j, int n, const uint16_t* bias, const EpiArgs& ep) {
+  // all loads first, then the arithmetic
+  f32x4 bv = {0.f, 0.f, 0.f, 0.f}, gv = {1.f, 1.f, 1.f, 1.f}, rv = {0.f, 0.f, 0.f, 0.f};
+  if (bias) bv = load4<true>(bias, j, n, ep.b_vec);
+  if (ep.gate) gv = load4<true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, ep.g_vec);
+  if (ep.residual) rv = load4<OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, ep.r_vec);
+  v += bv;
+  with_act(ep.act, [&](auto A) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = act_value<decltype(A)::value>(v[e]);
+      v[e] = j + e >= ep.act_begin ? a : v[e];
+    }
+  });
+  if (ep.gate) v *= gv;
+  if (ep.residual) v = rv + v;
+  store4<OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, ep.y_vec, v);
+}
+
+}  // namespace dev
+}  // namespace svdq

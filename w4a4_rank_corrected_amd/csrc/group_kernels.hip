@@ -1,0 +1,304 @@
+// Grouped by expert: the activation quantization + low-rank down-projection of
+// rows sorted by expert, and the combination of a token's rows afterwards.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "device_common.h"
+#include "epilogue.h"
+#include "grouped.h"
+#include "internal.h"
+#include "launch.h"
+#include "quant.h"
+
+#pragma clang fp contract(off)
+
+namespace svdq {
+namespace {
+
+using namespace dev;
+
+// ---------------------------------------------------------------------------
+// Row i of expert e: x~ = bf16(fl32(x[row_index[i]] * smooth_inv[e])), its INT4
+// codes and scales, z = x~ L1[e] (fp32).  A workgroup of 8 waves owns 16 rows of
+// one expert (grouped.h) and its waves split the channel groups, so each row's
+// Z is complete in the workgroup: the waves' partial sums are added in LDS in
+// wave order.  The arithmetic per element is quant_store's; the lane layout that
+// of the act-quant kernels (lane (r, c): row r, channels 8c .. 8c+7 and
+// 32+8c .. 32+8c+7 of a group).  Z is summed over groups in a fixed order.
+// A row index outside [0, x_rows) reads as a row of zeros.
+// Q = kActQuantNone: Z alone, of ranks rank0 .. rank0 + 16 TB - 1 (further ranks
+// of layers with more than 64).
+// ---------------------------------------------------------------------------
+constexpr int kGroupWaves = 8;
+template <int TB, bool SMOOTH, int Q>
+__global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
+    const uint16_t* __restrict__ x, int x_rows, const int32_t* __restrict__ row_index, Groups groups, int b, int m,
+    int G, const float* __restrict__ inv_all, const uint16_t* __restrict__ l1_all, int rank, int rank0,
+    uint8_t* __restrict__ qx, uint16_t* __restrict__ ascale, float* __restrict__ zout) {
+  constexpr int NW = kGroupWaves;
+  constexpr int NB = TB > 0 ? TB : 1;
+  constexpr int D = 2;
+  __shared__ __align__(16) float s_inv[NW][64];
+  __shared__ __align__(16) float s_z[TB > 0 ? NW * 16 * 16 * TB : 1];
+  const int tid = (int)threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, c = lane >> 4;
+  const GroupTile gt = find_tile<16>(groups.offsets, groups.experts, b, 1, (int)blockIdx.x, [](int d, int) { return d; });
+  if (!gt.live) return;  // the whole workgroup
+  const int row0 = gt.lo + gt.u * 16;
+  const int row = row0 + r;
+  const bool mine = row < gt.hi;
+  const float* inv = SMOOTH ? inv_all + (size_t)gt.expert * m : nullptr;
+  const uint16_t* l1t = TB > 0 ? l1_all + ((size_t)gt.expert * rank + rank0) * m : nullptr;
+  const int ranks = min(rank - rank0, 16 * TB);  // of this launch
+  int src = mine ? (row_index ? row_index[row] : row) : -1;
+  const bool read = src >= 0 && src < x_rows;
+  const uint16_t* xr = x + (size_t)(read ? src : 0) * m + 8 * c;
+  const uint32_t l1_bytes = TB > 0 ? (uint32_t)((ranks - 1) * m + 64) * 2u : 0u;
+  const int nj = wave < G ? (G - wave + NW - 1) / NW : 0;  // groups of this wave
+
+  struct Stage {
+    u32x4 xa, xb;
+    u32x4 la[NB], lb[NB];  // L1 rows tb*16 + r, channels 8c.. and 32 + 8c..
+    uint32_t iv;           // 1/lambda of channel `lane` of the group
+  };
+  auto load = [&](int j, Stage& st) {
+    const bool live = j < nj;
+    const int g = live ? wave + NW * j : 0;
+    st.xa = st.xb = u32x4{0u, 0u, 0u, 0u};
+    if (read && live) {
+      st.xa = ldg16(xr + (size_t)g * 64);
+      st.xb = ldg16(xr + (size_t)g * 64 + 32);
+    }
+    if constexpr (TB > 0) {
+      const __amdgpu_buffer_rsrc_t rl = make_rsrc(l1t + (size_t)g * 64, live ? l1_bytes : 0u);
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) {
+        const int t = tb * 16 + r;
+        const uint32_t off = t < ranks ? (uint32_t)(t * m + 8 * c) * 2u : 0x7FFFFFF0u;
+        st.la[tb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rl, off, 0, 0));
+        st.lb[tb] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rl, off + 64u, 0, 0));
+      }
+    }
+    if constexpr (SMOOTH) {
+      const __amdgpu_buffer_rsrc_t ri = make_rsrc(inv + (size_t)g * 64, live ? 256u : 0u);
+      st.iv = __builtin_amdgcn_raw_buffer_load_b32(ri, (uint32_t)lane * 4u, 0, 0);
+    }
+  };
+
+  f32x4 acc[NB];
+#pragma unroll
+  for (int t = 0; t < NB; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // rows of another expert (or past the last) drop their stores: offsets past
+  // the end of the group's records
+  const uint32_t q_off = mine ? (uint32_t)row * 32u + 4u * c : 0x7FFFFFE0u;
+  const uint32_t s_off = mine && c == 0 ? (uint32_t)row * 2u : 0x7FFFFFE0u;
+
+  auto process = [&](int j, const Stage& st) {
+    const int g = wave + NW * j;
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = bf16_lo(st.xa[e]);
+      v[2 * e + 1] = bf16_hi(st.xa[e]);
+      v[8 + 2 * e] = bf16_lo(st.xb[e]);
+      v[8 + 2 * e + 1] = bf16_hi(st.xb[e]);
+    }
+    if constexpr (SMOOTH) {
+      // the wave's own slot: LDS accesses of one wave complete in order, so
+      // the previous group's reads finish before this write lands
+      s_inv[wave][lane] = __uint_as_float(st.iv);
+      const float* iv = s_inv[wave];
+      const f32x4 i0 = *reinterpret_cast<const f32x4*>(iv + 8 * c);
+      const f32x4 i1 = *reinterpret_cast<const f32x4*>(iv + 8 * c + 4);
+      const f32x4 i2 = *reinterpret_cast<const f32x4*>(iv + 32 + 8 * c);
+      const f32x4 i3 = *reinterpret_cast<const f32x4*>(iv + 36 + 8 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] *= i0[e];
+        v[4 + e] *= i1[e];
+        v[8 + e] *= i2[e];
+        v[12 + e] *= i3[e];
+      }
+    }
+    uint32_t xt[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      xt[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+      v[2 * q] = bf16_lo(xt[q]);
+      v[2 * q + 1] = bf16_hi(xt[q]);
+    }
+    quant_store<Q>(v, g, b, row, c, q_off, s_off, qx, ascale, 1.0f);
+    if constexpr (TB > 0) {
+      const bf16x8 a0 = __builtin_bit_cast(bf16x8, u32x4{xt[0], xt[1], xt[2], xt[3]});
+      const bf16x8 a1 = __builtin_bit_cast(bf16x8, u32x4{xt[4], xt[5], xt[6], xt[7]});
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) {
+        acc[tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, st.la[tb]), acc[tb], 0, 0, 0);
+        acc[tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, st.lb[tb]), acc[tb], 0, 0, 0);
+      }
+    }
+  };
+
+  Stage st[D];
+#pragma unroll
+  for (int u = 0; u < D; ++u) load(u, st[u]);
+  int j = 0;
+  for (; j + D <= nj; j += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      process(j + u, st[u]);
+      load(j + u + D, st[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u + 1 < D; ++u)
+    if (j + u < nj) process(j + u, st[u]);
+
+  if constexpr (TB > 0) {
+    // partial Z of each wave (MFMA D layout: row 4c + v, column 16 tb + r),
+    // then Z[row0 + i][rank0 + t] = sum over waves in order
+    constexpr int ZC = 16 * TB;
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int vv = 0; vv < 4; ++vv) s_z[(wave * 16 + 4 * c + vv) * ZC + tb * 16 + r] = acc[tb][vv];
+    __syncthreads();
+    for (int e = tid; e < 16 * ZC; e += 64 * NW) {
+      const int i = e / ZC, t = e - i * ZC;
+      float zsum = s_z[i * ZC + t];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) zsum += s_z[(w * 16 + i) * ZC + t];
+      if (row0 + i < gt.hi && t < ranks) zout[(size_t)(row0 + i) * rank + rank0 + t] = zsum;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// y[t] = residual[t] + sum_k weight[t][k] rows[index[t][k]], in fp32 in the
+// order of k, rounded once.  A thread takes VEC consecutive columns of a token
+// and issues the loads of up to kCombineBatch rows together.  An index outside
+// [0, R) adds nothing.
+// ---------------------------------------------------------------------------
+constexpr int kCombineBatch = 8;
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ rows, int R, int n,
+                                                      const int32_t* __restrict__ index,
+                                                      const float* __restrict__ weight, int t_count, int k,
+                                                      const void* residual, void* y, int units) {
+  constexpr int W = VEC ? (BF16 ? 8 : 4) : 1;  // columns per thread
+  const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long t = u / units;
+  if (t >= t_count) return;
+  const int j = (int)(u - t * units) * W;
+  auto get = [&](const void* base, long long row, float (&v)[W]) {
+    const size_t at = (size_t)row * n + j;
+    if constexpr (!VEC) {
+      v[0] = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[at] << 16)
+                  : reinterpret_cast<const float*>(base)[at];
+    } else if constexpr (BF16) {
+      const u32x4 w = ldg16(reinterpret_cast<const uint16_t*>(base) + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+    } else {
+      const f32x4 w = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(base) + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = w[e];
+    }
+  };
+  float sum[W], res[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) sum[e] = res[e] = 0.0f;
+  if (residual) get(residual, t, res);
+  for (int q0 = 0; q0 < k; q0 += kCombineBatch) {
+    float v[kCombineBatch][W], w[kCombineBatch];
+#pragma unroll
+    for (int q = 0; q < kCombineBatch; ++q) {
+      w[q] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[q][e] = 0.0f;
+      if (q0 + q < k) {
+        const int i = index[t * k + q0 + q];
+        if (i >= 0 && i < R) {
+          w[q] = weight ? weight[t * k + q0 + q] : 1.0f;
+          get(rows, i, v[q]);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kCombineBatch; ++q)
+#pragma unroll
+      for (int e = 0; e < W; ++e) sum[e] = __builtin_fmaf(w[q], v[q][e], sum[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < W; ++e) sum[e] = res[e] + sum[e];
+  const size_t at = (size_t)t * n + j;
+  if constexpr (!VEC) {
+    if (BF16)
+      reinterpret_cast<uint16_t*>(y)[at] = bf16_bits(sum[0]);
+    else
+      reinterpret_cast<float*>(y)[at] = sum[0];
+  } else if constexpr (BF16) {
+    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(y) + at) =
+        u32x4{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]), pack_bf16x2(sum[4], sum[5]),
+              pack_bf16x2(sum[6], sum[7])};
+  } else {
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(y) + at) = f32x4{sum[0], sum[1], sum[2], sum[3]};
+  }
+}
+
+}  // namespace
+
+int launch_grouped_act(const uint16_t* x, int x_rows, const int32_t* row_index, const int32_t* offsets,
+                       const svdq_grouped_layer& L, int b, uint8_t* qx, uint16_t* ascale, float* z, void* stream) {
+  const Groups groups{offsets, L.experts};
+  const int G = L.m / SVDQ_GROUP;
+  const int grid = (int)grouped_row_blocks(b, L.experts, 16);
+  auto go = [&](auto kernel, int rank0) {
+    return launch_checked(kernel, grid, 64 * kGroupWaves, (hipStream_t)stream, x, x_rows, row_index, groups, b, L.m, G,
+                          L.smooth_inv, L.l1, L.rank, rank0, qx, ascale, z);
+  };
+  auto pass = [&](auto TB, auto Q, int rank0) {
+    constexpr int tb = decltype(TB)::value, q = decltype(Q)::value;
+    return L.smooth_inv ? go(grouped_act_kernel<tb, true, q>, rank0) : go(grouped_act_kernel<tb, false, q>, rank0);
+  };
+  // codes and scales with the first 64 ranks, then 64 further ranks a launch
+  for (int rank0 = 0; rank0 == 0 || rank0 < L.rank; rank0 += 64) {
+    const int tb = (std::min(L.rank - rank0, 64) + 15) / 16;
+    auto sized = [&](auto Q) {
+      switch (tb) {
+        case 1: return pass(std::integral_constant<int, 1>{}, Q, rank0);
+        case 2: return pass(std::integral_constant<int, 2>{}, Q, rank0);
+        case 3: return pass(std::integral_constant<int, 3>{}, Q, rank0);
+        default: return pass(std::integral_constant<int, 4>{}, Q, rank0);
+      }
+    };
+    const std::integral_constant<int, kActQuantInt4> codes;
+    const int status = tb == 0 ? pass(std::integral_constant<int, 0>{}, codes, 0)
+                       : rank0 == 0 ? sized(codes)
+                                    : sized(std::integral_constant<int, kActQuantNone>{});
+    if (status != 0) return status;
+  }
+  return 0;
+}
+
+int launch_combine(const void* rows, int R, int n, int dtype, const int32_t* index, const float* weight, int t, int k,
+                   const void* residual, void* y, void* stream) {
+  const bool bf = dtype == SVDQ_OUT_BF16;
+  const int w = bf ? 8 : 4;
+  const bool vec = n % w == 0 && (((uintptr_t)rows | (uintptr_t)residual | (uintptr_t)y) & 15u) == 0;
+  const int units = vec ? n / w : n;
+  const long long grid = ((long long)t * units + 255) / 256;
+  if (grid > 0x7FFFFFFF) return (int)hipErrorInvalidValue;
+  auto go = [&](auto kernel) {
+    return launch_checked(kernel, (int)grid, 256, (hipStream_t)stream, rows, R, n, index, weight, t, k, residual, y,
+                          units);
+  };
+  if (bf) return vec ? go(combine_kernel<true, true>) : go(combine_kernel<true, false>);
+  return vec ? go(combine_kernel<false, true>) : go(combine_kernel<false, false>);
+}
+
+}  // namespace svdq

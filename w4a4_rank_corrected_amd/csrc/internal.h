@@ -169,6 +169,58 @@ int launch_gemm8_up(const int8_t* qx, const uint16_t* ascale, const float* z, co
 int launch_gemm_fp4_up(const uint8_t* qx, const uint8_t* ascale, const float* z, const svdq_fp4_layer& L, int b,
                        void* y, int y_dtype, void* ws, void* stream);
 const char* hip_error_name(int err);
+
+// ---- products with an epilogue, and grouped by expert --------------------------
+// What the epilogue of a product needs, as the kernels take it: svdq_epilogue
+// with its strides filled in, and which rows allow vector accesses of four
+// consecutive elements (all rows of the tensor start aligned).
+struct EpiArgs {
+  const uint16_t* gate;  // bf16 [ceil(b / gate_rows)][n] or NULL
+  const void* residual;  // y's type, row stride ldr, or NULL
+  void* y;               // row stride ldy
+  int act, act_begin, gate_rows, ldr, ldy;
+  bool b_vec, g_vec, r_vec, y_vec;
+};
+// The experts' rows of a grouped product.
+struct Groups {
+  const int32_t* offsets;  // device, [experts + 1]
+  int experts;
+};
+// The most row blocks of `rows` rows that b rows sorted into `experts` experts
+// can make: sum_e ceil(c_e / rows) with sum_e c_e <= b.
+constexpr long long grouped_row_blocks(long long b, long long experts, long long rows) {
+  const long long full = (b + experts * (rows - 1)) / rows;
+  return full < b ? full : b;
+}
+// Rows up to which the INT4 product with an epilogue uses the row kernel.
+constexpr int kRowsMax = 64;
+int launch_gemm_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer& L, int b,
+                    int y_dtype, const EpiArgs& ep, void* ws, void* stream);
+int launch_gemm8_epi(const int8_t* qx, const uint16_t* ascale, const float* z, const svdq_w8a8_layer& L, int b,
+                     int y_dtype, const EpiArgs& ep, void* ws, void* stream);
+int launch_gemm_fp4_epi(const uint8_t* qx, const uint8_t* ascale, const float* z, const svdq_fp4_layer& L, int b,
+                        int y_dtype, const EpiArgs& ep, void* ws, void* stream);
+int launch_grouped_gemm(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_grouped_layer& L,
+                        const int32_t* offsets, int b, int y_dtype, const EpiArgs& ep, void* stream);
+// The row kernel (rows_kernels.hip), for one layer (groups.offsets NULL) or
+// grouped by expert; rb = 16-row blocks per workgroup (1, 2 or 4).
+struct RowsArgs {
+  const uint8_t* qx;
+  const uint16_t* ascale;
+  const float* z;
+  const uint8_t* qw;
+  const uint16_t* wscale;
+  const uint16_t* l2;
+  const uint16_t* bias;
+  int b, n, G, rank;
+  Groups groups;
+  EpiArgs ep;
+};
+int launch_gemm_rows(const RowsArgs& a, int rb, int y_dtype, void* stream);
+int launch_grouped_act(const uint16_t* x, int x_rows, const int32_t* row_index, const int32_t* offsets,
+                       const svdq_grouped_layer& L, int b, uint8_t* qx, uint16_t* ascale, float* z, void* stream);
+int launch_combine(const void* rows, int R, int n, int dtype, const int32_t* index, const float* weight, int t, int k,
+                   const void* residual, void* y, void* stream);
 // Launcher status (not a hipError_t) of a kernel that would use scratch memory.
 constexpr int kErrKernelScratch = -1000;
 
