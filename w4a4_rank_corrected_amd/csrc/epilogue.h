@@ -139,15 +139,24 @@ __device__ __forceinline__ void* row_of(void* base, int i, int ld) {
   return reinterpret_cast<uint8_t*>(base) + (size_t)i * (size_t)ld * (BF16 ? 2 : 4);
 }
 
+// What the epilogue of four consecutive outputs of row i reads (all zero, and
+// the gate one, where there is none).
+struct EpiLoads {
+  f32x4 bias, gate, residual;
+};
+template <bool OUT_BF16>
+__device__ __forceinline__ EpiLoads load_unit(int i, int j, int n, const uint16_t* bias, const EpiArgs& ep) {
+  EpiLoads l{{0.f, 0.f, 0.f, 0.f}, {1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
+  if (bias) l.bias = load4<true>(bias, j, n, ep.b_vec);
+  if (ep.gate) l.gate = load4<true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, ep.g_vec);
+  if (ep.residual) l.residual = load4<OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, ep.r_vec);
+  return l;
+}
+
 // The whole epilogue of four consecutive outputs of row i (v without the bias).
 template <bool OUT_BF16>
-__device__ __forceinline__ void finish_unit(f32x4 v, int i, int j, int n, const uint16_t* bias, const EpiArgs& ep) {
-  // all loads first, then the arithmetic
-  f32x4 bv = {0.f, 0.f, 0.f, 0.f}, gv = {1.f, 1.f, 1.f, 1.f}, rv = {0.f, 0.f, 0.f, 0.f};
-  if (bias) bv = load4<true>(bias, j, n, ep.b_vec);
-  if (ep.gate) gv = load4<true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, ep.g_vec);
-  if (ep.residual) rv = load4<OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, ep.r_vec);
-  v += bv;
+__device__ __forceinline__ void finish_unit(f32x4 v, const EpiLoads& l, int i, int j, int n, const EpiArgs& ep) {
+  v += l.bias;
   with_act(ep.act, [&](auto A) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -155,8 +164,8 @@ __device__ __forceinline__ void finish_unit(f32x4 v, int i, int j, int n, const 
       v[e] = j + e >= ep.act_begin ? a : v[e];
     }
   });
-  if (ep.gate) v *= gv;
-  if (ep.residual) v = rv + v;
+  if (ep.gate) v *= l.gate;
+  if (ep.residual) v = l.residual + v;
   store4<OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, ep.y_vec, v);
 }
 

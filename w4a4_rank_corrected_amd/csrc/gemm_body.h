@@ -876,7 +876,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(
   }
   if (lowrank_slot) o += slots[base + (size_t)k * stride];
   if constexpr (EPI) {
-    finish_unit<OUT_BF16>(o, i, j, n, bias, ep);
+    finish_unit<OUT_BF16>(o, load_unit<OUT_BF16>(i, j, n, bias, ep), i, j, n, ep);
     return;
   }
   float bv[4] = {0.f, 0.f, 0.f, 0.f};

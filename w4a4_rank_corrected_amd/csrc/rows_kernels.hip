@@ -5,9 +5,10 @@
 // with the exact per-group integer sums and the two FMAs per element and group
 // of the tiled kernel (gemm_body.h).
 //
-// A workgroup computes 16 columns of RB blocks of 16 rows; its waves split the
-// channel groups (wave w takes groups w, w + NW, ...), and their sums are added
-// in LDS in wave order.  Nothing is staged in LDS before that: a lane's
+// A wave computes 16 columns of RB blocks of 16 rows.  Of a workgroup's waves,
+// nwk split the channel groups of the same columns (wave k takes groups k,
+// k + nwk, ...; their sums are added in LDS in wave order) and nwc take
+// neighbouring columns.  Nothing is staged in LDS before that: a lane's
 // MFMA operand (16 codes of one row or column) is 8 bytes of its packed record,
 // so weights and activations go from memory to registers to the MFMA, D groups
 // ahead.  Any channel order serves, as both operands unpack alike.
@@ -30,21 +31,21 @@ constexpr int rows_depth(int rb) { return rb == 1 ? 6 : (rb == 2 ? 4 : 3); }
 
 // SWV: the four scales of a lane's columns are one aligned 8-byte load.
 template <int RB, bool OUT_BF16, bool GROUPED, bool SWV>
-__global__ __launch_bounds__(1024) void gemm_w4a4_rows_kernel(RowsArgs a) {
+__global__ __launch_bounds__(RB == 4 ? 512 : 1024) void gemm_w4a4_rows_kernel(RowsArgs a, int nwk, int nwc) {
   extern __shared__ __align__(16) uint8_t rows_lds[];
   f32x4* part = reinterpret_cast<f32x4*>(rows_lds);  // [wave][row block][lane]
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nw = (int)(blockDim.x >> 6);
+  const int ct = wave / nwk, wk = wave - ct * nwk;  // this wave's column block and share of the groups
   const int r = lane & 15, c = lane >> 4;
   const int b = a.b, n = a.n, G = a.G, rank = a.rank;
-  const int tiles_n = (n + 15) / 16;
+  const int tiles_n = (n + 16 * nwc - 1) / (16 * nwc);
 
   const uint8_t* qw = a.qw;
   const uint16_t* wscale = a.wscale;
   const uint16_t* l2 = a.l2;
   const uint16_t* bias = a.bias;
-  int i0, j0, row_end;
+  int i0, j00, row_end;  // first row, the workgroup's first column, end of the rows
   if constexpr (GROUPED) {
     const GroupTile g = find_tile<16 * RB>(a.groups.offsets, a.groups.experts, b, tiles_n, (int)blockIdx.x,
                                            [](int d, int T) { return xcd_range(d, T); });
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(1024) void gemm_w4a4_rows_kernel(RowsArgs a) {
     // an expert's row blocks of one column block are neighbours: they share its weights in L2
     const int tj = g.u / g.blocks;
     i0 = g.lo + (g.u - tj * g.blocks) * 16 * RB;
-    j0 = tj * 16;
+    j00 = tj * 16 * nwc;
     row_end = g.hi;
     const size_t e = (size_t)g.expert;
     qw += e * G * n * 32;
@@ -61,21 +62,22 @@ __global__ __launch_bounds__(1024) void gemm_w4a4_rows_kernel(RowsArgs a) {
     if (bias) bias += e * n;
   } else {
     i0 = 0;
-    j0 = (int)blockIdx.x * 16;
+    j00 = (int)blockIdx.x * 16 * nwc;
     row_end = b;
   }
+  const int j0 = j00 + 16 * ct;
 
   struct Stage {
     uint2 w, a[RB];   // packed codes: this lane's 8 bytes of its column's and rows' records
     uint2 sw;         // fp16 scales of columns 4c .. 4c+3
     uint32_t sx[RB];  // fp16 scales of the rows
   };
-  const int nk = wave < G ? (G - wave + nw - 1) / nw : 0;  // groups of this wave
+  const int nk = wk < G ? (G - wk + nwk - 1) / nwk : 0;  // groups of this wave
   const uint32_t w_off = (uint32_t)(j0 + r) * 32u + 8u * c;
   const uint32_t s_off = (uint32_t)(j0 + 4 * c) * 2u;
   auto load = [&](int k, Stage& st) {
     const bool live = k < nk;
-    const int g = live ? wave + nw * k : 0;
+    const int g = live ? wk + nwk * k : 0;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(qw + (size_t)g * n * 32, live ? (uint32_t)n * 32u : 0u);
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.qx + (size_t)g * b * 32, live ? (uint32_t)b * 32u : 0u);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(wscale + (size_t)g * n, live ? (uint32_t)n * 2u : 0u);
@@ -122,40 +124,66 @@ __global__ __launch_bounds__(1024) void gemm_w4a4_rows_kernel(RowsArgs a) {
     }
   };
 
-  // low-rank branch: chunk q of 32 ranks belongs to wave q % NW
+  // low-rank branch: chunk q of 32 ranks belongs to wave nwk - 1 - q % nwk (the
+  // last ones: the first ones fetch the epilogue's operands)
+  const bool l2_vec = rank % 8 == 0 && ((uintptr_t)l2 & 15u) == 0, z_vec = rank % 4 == 0 && ((uintptr_t)a.z & 15u) == 0;
   auto lowrank = [&]() {
-    for (int kc = 32 * wave; kc < rank; kc += 32 * nw) {
+    for (int kc = 32 * (nwk - 1 - wk); kc < rank; kc += 32 * nwk) {
       const int t0 = kc + 8 * c;
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      u32x4 w = {0u, 0u, 0u, 0u};
       const int j = j0 + r;
       if (j < n) {
         const uint16_t* p = l2 + (size_t)j * rank + t0;
+        if (l2_vec) {
+          if (t0 < rank) w = ldg16(p);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (t0 + e < rank) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+          for (int e = 0; e < 8; ++e)
+            if (t0 + e < rank) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        }
       }
-      const bf16x8 P = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+      const bf16x8 P = __builtin_bit_cast(bf16x8, w);
 #pragma unroll
       for (int q = 0; q < RB; ++q) {
         const int i = i0 + 16 * q + r;
-        float zv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        f32x4 z0 = {0.f, 0.f, 0.f, 0.f}, z1 = {0.f, 0.f, 0.f, 0.f};
         if (i < row_end) {
           const float* zr = a.z + (size_t)i * rank + t0;
+          if (z_vec) {
+            if (t0 < rank) z0 = *reinterpret_cast<const f32x4*>(zr);
+            if (t0 + 4 < rank) z1 = *reinterpret_cast<const f32x4*>(zr + 4);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (t0 + e < rank) zv[e] = zr[e];
+            for (int e = 0; e < 4; ++e) {
+              if (t0 + e < rank) z0[e] = zr[e];
+              if (t0 + 4 + e < rank) z1[e] = zr[4 + e];
+            }
+          }
         }
-        const bf16x8 Q = __builtin_bit_cast(bf16x8, u32x4{pack_bf16x2(zv[0], zv[1]), pack_bf16x2(zv[2], zv[3]),
-                                                          pack_bf16x2(zv[4], zv[5]), pack_bf16x2(zv[6], zv[7])});
+        const bf16x8 Q = __builtin_bit_cast(bf16x8, u32x4{pack_bf16x2(z0[0], z0[1]), pack_bf16x2(z0[2], z0[3]),
+                                                          pack_bf16x2(z1[0], z1[1]), pack_bf16x2(z1[2], z1[3])});
         acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(P, Q, acc[q], 0, 0, 0);
       }
     }
+  };
+
+  // A unit is four consecutive columns of a row (a lane's four results).  Unit
+  // u of the workgroup: column block u / (64 RB), row block, lane.
+  auto unit_at = [&](int u, int& i, int& j) {
+    i = i0 + 16 * ((u >> 6) % RB) + (u & 15);
+    j = j00 + 16 * (u / (64 * RB)) + 4 * ((u & 63) >> 4);
+    return i < row_end && j < n;
   };
 
   constexpr int D = rows_depth(RB);
   Stage st[D];
 #pragma unroll
   for (int u = 0; u < D; ++u) load(u, st[u]);
+  // the operands of this thread's first unit's epilogue, while the codes arrive
+  int ui, uj;
+  const bool mine = tid < nwc * RB * 64 && unit_at(tid, ui, uj);
+  EpiLoads el;
+  if (mine) el = load_unit<OUT_BF16>(ui, uj, n, bias, a.ep);
   lowrank();
   int k = 0;
   for (; k + D <= nk; k += D) {
@@ -169,31 +197,38 @@ __global__ __launch_bounds__(1024) void gemm_w4a4_rows_kernel(RowsArgs a) {
   for (int u = 0; u + 1 < D; ++u)
     if (k + u < nk) compute(st[u]);
 
-  // sums of the waves, in wave order, then the epilogue of four columns a thread
 #pragma unroll
   for (int q = 0; q < RB; ++q) part[(wave * RB + q) * 64 + lane] = acc[q];
   __syncthreads();
-  for (int u = tid; u < RB * 64; u += (int)blockDim.x) {
-    f32x4 v = part[u];
-    for (int w = 1; w < nw; ++w) v += part[w * RB * 64 + u];
-    const int i = i0 + 16 * (u >> 6) + (u & 15), j = j0 + 4 * ((u & 63) >> 4);
-    if (i < row_end && j < n) finish_unit<OUT_BF16>(v, i, j, n, bias, a.ep);
-  }
+  auto sum = [&](int u) {
+    const int at = u / (64 * RB) * nwk * RB * 64 + u % (64 * RB);
+    f32x4 v = part[at];
+    for (int w = 1; w < nwk; ++w) v += part[at + w * RB * 64];
+    return v;
+  };
+  if (mine) finish_unit<OUT_BF16>(sum(tid), el, ui, uj, n, a.ep);
+  for (int u = tid + (int)blockDim.x; u < nwc * RB * 64; u += (int)blockDim.x)
+    if (unit_at(u, ui, uj)) finish_unit<OUT_BF16>(sum(u), load_unit<OUT_BF16>(ui, uj, n, bias, a.ep), ui, uj, n, a.ep);
 }
 
 template <int RB, bool OUT_BF16, bool GROUPED>
 int launch_rows(const RowsArgs& a, hipStream_t st) {
-  const long long tiles_n = (a.n + 15) / 16;
-  const long long grid = GROUPED ? grouped_row_blocks(a.b, a.groups.experts, 16 * RB) * tiles_n : tiles_n;
+  // Waves to split the groups over: up to the 16 waves a CU that are resident
+  // together (more would wait for a second round), each with two groups at the
+  // least; then column blocks until a workgroup has four waves.
+  const long long blocks = GROUPED ? grouped_row_blocks(a.b, a.groups.experts, 16 * RB) : 1;
+  const long long tiles = blocks * ((a.n + 15) / 16);
+  int nwk = 1;
+  while (nwk < (RB == 4 ? 8 : 16) && tiles * nwk <= 2048 && a.G >= 4 * nwk) nwk *= 2;
+  const int nwc = nwk < 4 ? 4 / nwk : 1;
+  const long long grid = blocks * ((a.n + 16 * nwc - 1) / (16 * nwc));
   if (grid > 0x7FFFFFFF) return (int)hipErrorInvalidValue;
-  const int most = RB == 4 ? 8 : 16;
-  const int nw = a.G >= 32 ? most : (a.G >= 16 ? 8 : (a.G >= 8 ? 4 : 2));
-  const size_t lds = (size_t)nw * RB * 1024;
+  const size_t lds = (size_t)nwk * nwc * RB * 1024;
   const bool swv = a.n % 4 == 0 && ((uintptr_t)a.wscale & 7u) == 0;
   auto go = [&](auto kernel) {
     const int ok = scratch_free(reinterpret_cast<const void*>(kernel));
     if (ok != 0) return ok;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3((unsigned)(64 * nw)), lds, st, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3((unsigned)(64 * nwk * nwc)), lds, st, a, nwk, nwc);
     return (int)hipGetLastError();
   };
   return swv ? go(gemm_w4a4_rows_kernel<RB, OUT_BF16, GROUPED, true>)
