@@ -21,23 +21,31 @@ using namespace dev;
 
 // ---------------------------------------------------------------------------
 // Row i of expert e: x~ = bf16(fl32(x[row_index[i]] * smooth_inv[e])), its INT4
-// codes and scales, z = x~ L1[e] (fp32).  A workgroup of 8 waves owns 16 rows of
+// codes and scales, z = x~ L1[e] (fp32).  A workgroup of NW waves owns 16 rows of
 // one expert (grouped.h) and its waves split the channel groups, so each row's
 // Z is complete in the workgroup: the waves' partial sums are added in LDS in
-// wave order.  The arithmetic per element is quant_store's; the lane layout that
-// of the act-quant kernels (lane (r, c): row r, channels 8c .. 8c+7 and
-// 32+8c .. 32+8c+7 of a group).  Z is summed over groups in a fixed order.
+// wave order.  Z is summed over groups in a fixed order.
+//
+// Four neighbouring lanes hold a row's group (lane 4 r + c: channels 8c .. 8c+7
+// and 32+8c .. 32+8c+7), so each 16-byte load of a quad is 64 contiguous bytes;
+// an MFMA operand wants lane r + 16 c instead, and x~ and L1 get there by lane
+// permutes (ds_bpermute).  Loading in the MFMA's lane order, every quad on four
+// rows, kept the address path busy instead: 26.4 against 18.5 us for 18006 rows
+// of 2048 channels at rank 16, 43.6 against 26.8 us for 8192 of 4608 at rank 32.
+// What bounds it now is the gather: 94 MB of rows and codes in those 18.5 us,
+// 5.1 TB/s (a large copy reaches 5.1).
 // A row index outside [0, x_rows) reads as a row of zeros.
 // Q = kActQuantNone: Z alone, of ranks rank0 .. rank0 + 16 TB - 1 (further ranks
 // of layers with more than 64).
 // ---------------------------------------------------------------------------
-constexpr int kGroupWaves = 8;
-template <int TB, bool SMOOTH, int Q>
-__global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
+// Waves a SIMD the register budget must allow, by the number of Z blocks.
+constexpr int group_waves_per_simd(int tb) { return tb <= 1 ? 6 : (tb <= 3 ? 4 : 3); }
+template <int TB, bool SMOOTH, int Q, int NW>
+__global__ __launch_bounds__(64 * NW)
+__attribute__((amdgpu_waves_per_eu(group_waves_per_simd(TB)))) void grouped_act_kernel(
     const uint16_t* __restrict__ x, int x_rows, const int32_t* __restrict__ row_index, Groups groups, int b, int m,
     int G, const float* __restrict__ inv_all, const uint16_t* __restrict__ l1_all, int rank, int rank0,
     uint8_t* __restrict__ qx, uint16_t* __restrict__ ascale, float* __restrict__ zout) {
-  constexpr int NW = kGroupWaves;
   constexpr int NB = TB > 0 ? TB : 1;
   constexpr int D = 2;
   __shared__ __align__(16) float s_inv[NW][64];
@@ -45,8 +53,11 @@ __global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
   const int tid = (int)threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, c = lane >> 4;
-  const GroupTile gt = find_tile<16>(groups.offsets, groups.experts, b, 1, (int)blockIdx.x, [](int d, int) { return d; });
+  const int r = lane >> 2, c = lane & 3;     // this lane's row and channels
+  const int mr = lane & 15, mc = lane >> 4;  // its place in an MFMA operand
+  const int pull = 4 * (4 * mr + mc);        // the lane (times 4) that holds its operand
+  const GroupTile gt = find_tile<16>(groups.offsets, groups.experts, b, 1, (int)blockIdx.x,
+                                     [](int d, int T) { return xcd_range(d, T); });
   if (!gt.live) return;  // the whole workgroup
   const int row0 = gt.lo + gt.u * 16;
   const int row = row0 + r;
@@ -54,9 +65,7 @@ __global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
   const float* inv = SMOOTH ? inv_all + (size_t)gt.expert * m : nullptr;
   const uint16_t* l1t = TB > 0 ? l1_all + ((size_t)gt.expert * rank + rank0) * m : nullptr;
   const int ranks = min(rank - rank0, 16 * TB);  // of this launch
-  int src = mine ? (row_index ? row_index[row] : row) : -1;
-  const bool read = src >= 0 && src < x_rows;
-  const uint16_t* xr = x + (size_t)(read ? src : 0) * m + 8 * c;
+  const int src = mine ? (row_index ? row_index[row] : row) : -1;
   const uint32_t l1_bytes = TB > 0 ? (uint32_t)((ranks - 1) * m + 64) * 2u : 0u;
   const int nj = wave < G ? (G - wave + NW - 1) / NW : 0;  // groups of this wave
 
@@ -65,14 +74,11 @@ __global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
     u32x4 la[NB], lb[NB];  // L1 rows tb*16 + r, channels 8c.. and 32 + 8c..
     uint32_t iv;           // 1/lambda of channel `lane` of the group
   };
-  auto load = [&](int j, Stage& st) {
+  // the expert's operands and the row's activations are loaded apart: the first
+  // groups' L1 and 1/lambda go out before the row index arrives
+  auto load_layer = [&](int j, Stage& st) {
     const bool live = j < nj;
     const int g = live ? wave + NW * j : 0;
-    st.xa = st.xb = u32x4{0u, 0u, 0u, 0u};
-    if (read && live) {
-      st.xa = ldg16(xr + (size_t)g * 64);
-      st.xb = ldg16(xr + (size_t)g * 64 + 32);
-    }
     if constexpr (TB > 0) {
       const __amdgpu_buffer_rsrc_t rl = make_rsrc(l1t + (size_t)g * 64, live ? l1_bytes : 0u);
 #pragma unroll
@@ -88,7 +94,6 @@ __global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
       st.iv = __builtin_amdgcn_raw_buffer_load_b32(ri, (uint32_t)lane * 4u, 0, 0);
     }
   };
-
   f32x4 acc[NB];
 #pragma unroll
   for (int t = 0; t < NB; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -131,27 +136,47 @@ __global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
       v[2 * q] = bf16_lo(xt[q]);
       v[2 * q + 1] = bf16_hi(xt[q]);
     }
-    quant_store<Q>(v, g, b, row, c, q_off, s_off, qx, ascale, 1.0f);
+    if constexpr (Q == kActQuantInt4) quant_store_int4(v, g, b, q_off, s_off, qx, ascale);
     if constexpr (TB > 0) {
-      const bf16x8 a0 = __builtin_bit_cast(bf16x8, u32x4{xt[0], xt[1], xt[2], xt[3]});
-      const bf16x8 a1 = __builtin_bit_cast(bf16x8, u32x4{xt[4], xt[5], xt[6], xt[7]});
+      auto operand = [&](const u32x4& w) {
+        u32x4 o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = (uint32_t)__builtin_amdgcn_ds_bpermute(pull, (int)w[q]);
+        return __builtin_bit_cast(bf16x8, o);
+      };
+      const bf16x8 a0 = operand(u32x4{xt[0], xt[1], xt[2], xt[3]});
+      const bf16x8 a1 = operand(u32x4{xt[4], xt[5], xt[6], xt[7]});
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) {
-        acc[tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, __builtin_bit_cast(bf16x8, st.la[tb]), acc[tb], 0, 0, 0);
-        acc[tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, __builtin_bit_cast(bf16x8, st.lb[tb]), acc[tb], 0, 0, 0);
+        acc[tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, operand(st.la[tb]), acc[tb], 0, 0, 0);
+        acc[tb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, operand(st.lb[tb]), acc[tb], 0, 0, 0);
       }
     }
   };
 
   Stage st[D];
 #pragma unroll
-  for (int u = 0; u < D; ++u) load(u, st[u]);
+  for (int u = 0; u < D; ++u) load_layer(u, st[u]);
+  const bool read = src >= 0 && src < x_rows;
+  const uint16_t* xr = x + (size_t)(read ? src : 0) * m + 8 * c;
+  auto load_x = [&](int j, Stage& st) {
+    st.xa = st.xb = u32x4{0u, 0u, 0u, 0u};
+    if (read && j < nj) {
+      const uint16_t* xg = xr + (size_t)(wave + NW * j) * 64;
+      st.xa = ldg16(xg);
+      st.xb = ldg16(xg + 32);
+    }
+  };
+
+#pragma unroll
+  for (int u = 0; u < D; ++u) load_x(u, st[u]);
   int j = 0;
   for (; j + D <= nj; j += D) {
 #pragma unroll
     for (int u = 0; u < D; ++u) {
       process(j + u, st[u]);
-      load(j + u + D, st[u]);
+      load_layer(j + u + D, st[u]);
+      load_x(j + u + D, st[u]);
     }
   }
 #pragma unroll
@@ -159,13 +184,13 @@ __global__ __launch_bounds__(64 * kGroupWaves) void grouped_act_kernel(
     if (j + u < nj) process(j + u, st[u]);
 
   if constexpr (TB > 0) {
-    // partial Z of each wave (MFMA D layout: row 4c + v, column 16 tb + r),
+    // partial Z of each wave (MFMA D layout: row 4 mc + v, column 16 tb + mr),
     // then Z[row0 + i][rank0 + t] = sum over waves in order
     constexpr int ZC = 16 * TB;
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-      for (int vv = 0; vv < 4; ++vv) s_z[(wave * 16 + 4 * c + vv) * ZC + tb * 16 + r] = acc[tb][vv];
+      for (int vv = 0; vv < 4; ++vv) s_z[(wave * 16 + 4 * mc + vv) * ZC + tb * 16 + mr] = acc[tb][vv];
     __syncthreads();
     for (int e = tid; e < 16 * ZC; e += 64 * NW) {
       const int i = e / ZC, t = e - i * ZC;
@@ -257,13 +282,23 @@ int launch_grouped_act(const uint16_t* x, int x_rows, const int32_t* row_index, 
   const Groups groups{offsets, L.experts};
   const int G = L.m / SVDQ_GROUP;
   const int grid = (int)grouped_row_blocks(b, L.experts, 16);
+  // Waves of a row block: four leave room for more row blocks on a CU (30.3 us
+  // against 40.3 for 18006 rows of 2048 channels at rank 64, within 4 % of each
+  // other at ranks 16 and 32); with fewer row blocks than CUs, eight keep more
+  // loads in flight for the same rows.  (Sixteen: 25-40 % slower with many rows,
+  // no faster with few.)
+  const int nw = grid <= kMaxCUs ? 8 : 4;
   auto go = [&](auto kernel, int rank0) {
-    return launch_checked(kernel, grid, 64 * kGroupWaves, (hipStream_t)stream, x, x_rows, row_index, groups, b, L.m, G,
+    return launch_checked(kernel, grid, 64 * nw, (hipStream_t)stream, x, x_rows, row_index, groups, b, L.m, G,
                           L.smooth_inv, L.l1, L.rank, rank0, qx, ascale, z);
   };
   auto pass = [&](auto TB, auto Q, int rank0) {
     constexpr int tb = decltype(TB)::value, q = decltype(Q)::value;
-    return L.smooth_inv ? go(grouped_act_kernel<tb, true, q>, rank0) : go(grouped_act_kernel<tb, false, q>, rank0);
+    auto with_waves = [&](auto NW) {
+      constexpr int w = decltype(NW)::value;
+      return L.smooth_inv ? go(grouped_act_kernel<tb, true, q, w>, rank0) : go(grouped_act_kernel<tb, false, q, w>, rank0);
+    };
+    return nw == 8 ? with_waves(std::integral_constant<int, 8>{}) : with_waves(std::integral_constant<int, 4>{});
   };
   // codes and scales with the first 64 ranks, then 64 further ranks a launch
   for (int rank0 = 0; rank0 == 0 || rank0 < L.rank; rank0 += 64) {

@@ -37,15 +37,16 @@ __device__ __forceinline__ int xcd_range(int d, int T) {
   return xcd < extra ? xcd * (per + 1) + k : extra * (per + 1) + (xcd - extra) * per + k;
 }
 
-// Exclusive scan over the wave; `total` receives the sum.
+// Exclusive scan over the wave with DPP moves (shifts within rows of 16 lanes,
+// then broadcasts of the rows' last lanes); `total` receives the sum.
 __device__ __forceinline__ int wave_scan(int v, int& total) {
-  const int lane = (int)(threadIdx.x & 63);
   int s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(s, d);
-    if (lane >= d) s += o;
-  }
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, true);   // row_shr:1
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, true);   // row_shr:2
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, true);   // row_shr:4
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, true);   // row_shr:8
+  s += __builtin_amdgcn_update_dpp(0, s, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  s += __builtin_amdgcn_update_dpp(0, s, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
   total = __builtin_amdgcn_readlane(s, 63);
   return s - v;
 }
