@@ -214,6 +214,8 @@ def _dev(t, name: str, dtype=None, shape=None, device=None) -> None:
         return
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return  # the usual case, without the messages
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if dtype is not None and t.dtype != dtype:
@@ -863,26 +865,36 @@ def svdq_fp4_linear(x, layer: DeviceLayerFp4, out_dtype=None, y=None, workspace=
 # products with an epilogue: activation, gate and residual before y's one rounding
 # ---------------------------------------------------------------------------
 
+def _current_stream(index: int) -> int:
+    """The handle of a device's current stream (without building a Stream object
+    where this torch gives the handle itself: 2 us less per call)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+
+
 class _On:
     """Makes a tensor's device current and, with a stream given, that stream, so
     that tensors allocated inside belong to the stream that uses them.  Enters
     to the stream's handle."""
 
+    __slots__ = ("contexts", "handle")
+
     def __init__(self, device, stream):
         import torch
-        self.contexts = []
+        self.contexts = ()
         if torch.cuda.current_device() != device.index:
-            self.contexts.append(torch.cuda.device(device))
+            self.contexts = (torch.cuda.device(device),)
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if isinstance(stream, int):
-                stream = (torch.cuda.default_stream(device) if stream == 0
-                          else torch.cuda.ExternalStream(stream, device=device))
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, expected {device}")
-            self.handle = stream.cuda_stream
-            self.contexts.append(torch.cuda.stream(stream))
+            self.handle = _current_stream(device.index)
+            return
+        if isinstance(stream, int):
+            stream = (torch.cuda.default_stream(device) if stream == 0
+                      else torch.cuda.ExternalStream(stream, device=device))
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, expected {device}")
+        self.handle = stream.cuda_stream
+        self.contexts += (torch.cuda.stream(stream),)
 
     def __enter__(self):
         for c in self.contexts:
@@ -957,7 +969,7 @@ def _gemm_epi(fn, size, operands, qx, ascale, z, layer, act, act_begin, gate, ga
     device = qx.device
     with _On(device, stream) as handle:
         y, code, epi = _epilogue(b, layer.n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
-        workspace, wsb = _workspace(workspace, size(b, layer.n, layer.m), device)
+        workspace, wsb = _workspace(workspace, size(b, layer.n, layer.m) if workspace is None else 0, device)
         _check(fn(_ptr(qx), _ptr(ascale), _ptr(z), ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code,
                   workspace.data_ptr(), wsb, handle))
     return y
@@ -1007,7 +1019,7 @@ def _linear_epi(fn, size, x, layer, act, act_begin, gate, gate_rows, residual, o
         raise ValueError(f"x has {m} channels, the layer {layer.m}")
     with _On(device, stream) as handle:
         y, code, epi = _epilogue(b, layer.n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
-        workspace, wsb = _workspace(workspace, size(b, m, layer.n, layer.rank), device)
+        workspace, wsb = _workspace(workspace, size(b, m, layer.n, layer.rank) if workspace is None else 0, device)
         _check(fn(_ptr(x), ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code, workspace.data_ptr(),
                   wsb, handle))
     return y
@@ -1160,8 +1172,10 @@ def svdq_grouped_linear(x, offsets, layer: GroupedDeviceLayer, row_index=None, a
     dev = x.device
     with _On(dev, stream) as handle:
         y, code, epi = _epilogue(b, layer.n, dev, y, out_dtype, act, act_begin)
-        workspace, wsb = _workspace(
-            workspace, svdq_grouped_linear_workspace_size(b, layer.experts, layer.m, layer.n, layer.rank), dev)
+        need = 0
+        if workspace is None:
+            need = svdq_grouped_linear_workspace_size(b, layer.experts, layer.m, layer.n, layer.rank)
+        workspace, wsb = _workspace(workspace, need, dev)
         _check(lib().svdq_grouped_linear(
             _ptr(x), x_rows, _ptr(row_index), _ptr(offsets), ctypes.byref(layer.struct), ctypes.byref(epi), b,
             y.data_ptr(), code, workspace.data_ptr(), wsb, handle))
