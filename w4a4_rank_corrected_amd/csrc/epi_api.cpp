@@ -58,6 +58,11 @@ int check_epilogue(const svdq_epilogue* epi, const uint16_t* bias, bool bias_row
   out->g_vec = ((uintptr_t)e.gate & 7u) == 0 && n % 4 == 0;
   out->r_vec = ((uintptr_t)e.residual & mask) == 0 && ldr % 4 == 0;
   out->y_vec = ((uintptr_t)y & mask) == 0 && ldy % 4 == 0;
+  const int wide = 16 / size;  // elements of y in 16 bytes
+  out->b_vec16 = aligned16(bias) && (!bias_rows || n % 8 == 0);
+  out->g_vec16 = aligned16(e.gate) && n % 8 == 0;
+  out->r_vec16 = aligned16(e.residual) && ldr % wide == 0;
+  out->y_vec16 = aligned16(y) && ldy % wide == 0;
   return SVDQ_OK;
 }
 

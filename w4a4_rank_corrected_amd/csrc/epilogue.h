@@ -27,11 +27,12 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // GELU in its tanh form, 0.5 v (1 + tanh(u)), u = sqrt(2/pi) (v + 0.044715 v^3),
-// as v / (1 + exp(-2 u)): no cancellation where tanh(u) nears -1.
+// as v / (1 + exp(-2 u)): no cancellation where tanh(u) nears -1.  log2 e is in
+// the polynomial's constants.
 __device__ __forceinline__ float gelu_tanh(float v) {
-  const float v2 = v * v;
-  const float u2 = v * __builtin_fmaf(v2, -2.0f * 0.7978845608028654f * 0.044715f, -2.0f * 0.7978845608028654f);  // -2 u
-  return v * fast_rcp(1.0f + fast_exp(u2));
+  constexpr float c = -2.0f * 0.7978845608028654f * 1.44269504088896341f;
+  const float x = v * __builtin_fmaf(v * v, c * 0.044715f, c);  // -2 u log2 e
+  return v * fast_rcp(1.0f + __builtin_amdgcn_exp2f(x));
 }
 
 // GELU with the normal distribution's integral, v Phi(v), Phi(v) = erfc(-v / sqrt 2) / 2,
@@ -125,6 +126,48 @@ __device__ __forceinline__ void store4(void* row, int j, int n, bool vec, const 
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (j + e < n) p[e] = o[e];
+    }
+  }
+}
+
+// W (4 or 8) consecutive columns j .. j+W-1 as floats; `vec`: the row's
+// 16-byte vectors are aligned (8 bytes for four bf16).  Columns >= n read as
+// zero.
+template <int W, bool BF16>
+__device__ __forceinline__ void load_cols(const void* row, int j, int n, bool vec, float (&v)[W]) {
+  if constexpr (W == 4) {
+    const f32x4 x = load4<BF16>(row, j, n, vec);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = x[e];
+  } else {
+    static_assert(W == 8 && BF16, "eight bf16 columns");
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + j;
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (vec && j + 7 < n) {
+      w = ldg16(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e < n) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+  }
+}
+template <int W, bool BF16>
+__device__ __forceinline__ void store_cols(void* row, int j, int n, bool vec, const float (&v)[W]) {
+  if constexpr (W == 4) {
+    store4<BF16>(row, j, n, vec, f32x4{v[0], v[1], v[2], v[3]});
+  } else {
+    static_assert(W == 8 && BF16, "eight bf16 columns");
+    uint16_t* p = reinterpret_cast<uint16_t*>(row) + j;
+    if (vec && j + 7 < n) {
+      *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                           pack_bf16x2(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (j + e < n) p[e] = bf16_bits(v[e]);
     }
   }
 }

@@ -249,6 +249,7 @@ __device__ __forceinline__ void gemm_up_body(
     const uint16_t* __restrict__ bias, int b, int n, int G, int rank, int tiles_m, int tiles_n,
     void* __restrict__ yout, SplitK sk, float txw, const EpiArgs& ep = EpiArgs{},
     const GroupTile& grp = GroupTile{}) {
+  static_assert(MODE == kTilePlain || C::KG == 1, "the low-rank product's LDS space");
   static_assert(MODE != kTileGrouped || !SK, "experts' tiles are not split");
   // rows of this workgroup's tile end here
   const int row_end = MODE == kTileGrouped ? grp.hi : b;
@@ -345,6 +346,73 @@ __device__ __forceinline__ void gemm_up_body(
         const bf16x8 Q = __builtin_bit_cast(
             bf16x8, u32x4{pack_bf16x2(zv[0], zv[1]), pack_bf16x2(zv[2], zv[3]),
                           pack_bf16x2(zv[4], zv[5]), pack_bf16x2(zv[6], zv[7])});
+#pragma unroll
+        for (int bj = 0; bj < BJ; ++bj)
+          acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(P[bj], Q, acc[bi][bj], 0, 0, 0);
+      }
+    }
+  };
+
+  // The same through LDS (MODE != kTilePlain): Z and L2 of the tile are loaded
+  // once per workgroup, neighbouring lanes along a row, and staged as bf16 rows
+  // of 64 bytes (32 ranks) in the layout of the unpacked codes, so the operand
+  // reads are the codes' own.  lr_a, lr_b: LDS space of TM and TN such rows that
+  // nothing else uses meanwhile.  The caller synchronises before and after.
+  auto lowrank_lds = [&](int i0, int j0, uint8_t* lr_a, uint8_t* lr_b) {
+    for (int kc = 0; kc < rank; kc += 32) {
+      if (kc > 0) __syncthreads();
+      constexpr int ZP = TM * 8 / NT, LP = TN * 4 / NT;  // pieces a thread: four ranks of Z, eight of L2
+      f32x4 zv[ZP];
+      u32x4 lv[LP];
+#pragma unroll
+      for (int q = 0; q < ZP; ++q) {
+        const int k = tid + NT * q, i = i0 + (k >> 3), t = kc + 4 * (k & 7);
+        zv[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (i < row_end) {
+          const float* zr = z + (size_t)i * rank + t;
+          if (z_vec) {
+            if (t < rank) zv[q] = *reinterpret_cast<const f32x4*>(zr);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t + e < rank) zv[q][e] = zr[e];
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < LP; ++q) {
+        const int k = tid + NT * q, j = j0 + (k >> 2), t = kc + 8 * (k & 3);
+        lv[q] = u32x4{0u, 0u, 0u, 0u};
+        if (j < n) {
+          const uint16_t* lr = l2t + (size_t)j * rank + t;
+          if (l2_vec) {
+            if (t < rank) lv[q] = ldg16(lr);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (t + e < rank) lv[q][e >> 1] |= (uint32_t)lr[e] << (16 * (e & 1));
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < ZP; ++q) {
+        const int k = tid + NT * q, row = k >> 3, p = k & 7;
+        *reinterpret_cast<uint2*>(lr_a + row * 64 + 16 * ((p >> 1) ^ chunk_swz(row)) + 8 * (p & 1)) =
+            uint2{pack_bf16x2(zv[q][0], zv[q][1]), pack_bf16x2(zv[q][2], zv[q][3])};
+      }
+#pragma unroll
+      for (int q = 0; q < LP; ++q) {
+        const int k = tid + NT * q, row = k >> 2;
+        *reinterpret_cast<u32x4*>(lr_b + row * 64 + 16 * ((k & 3) ^ chunk_swz(row))) = lv[q];
+      }
+      __syncthreads();
+      bf16x8 P[BJ];
+#pragma unroll
+      for (int bj = 0; bj < BJ; ++bj)
+        P[bj] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(lr_b + (WN * wn + 16 * bj + r) * 64 + cs));
+#pragma unroll
+      for (int bi = 0; bi < BI; ++bi) {
+        const bf16x8 Q = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(lr_a + (WM * wm + 16 * bi + r) * 64 + cs));
 #pragma unroll
         for (int bj = 0; bj < BJ; ++bj)
           acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(P[bj], Q, acc[bi][bj], 0, 0, 0);
@@ -626,59 +694,89 @@ __device__ __forceinline__ void gemm_up_body(
   };
 
   // ---- epilogue with activation, gate and residual ---------------------------
-  // The activation is chosen once for the tile and applied to the accumulators
-  // in place.  y may be the residual itself, so the compiler cannot move the
-  // residual's loads over y's stores: a column block's loads are all issued
-  // before its first store.
+  // An MFMA result holds 16 rows in neighbouring lanes, four columns each; a
+  // store or load in that order touches 16 rows' lines with every quad of
+  // lanes.  Each 16-row block of a wave therefore goes through LDS (the wave's
+  // own space, no barrier; rows 4 words apart modulo the banks) and comes back
+  // as W neighbouring columns a lane, a row's lanes next to each other: 16-byte
+  // accesses that fill whole 128-byte lines.  y may be the residual itself, so
+  // the compiler cannot move the residual's loads over y's stores: a block's
+  // are issued before the block ahead of it is stored.
+  constexpr int W = OUT_BF16 ? 8 : 4;        // columns a lane
+  constexpr int LPR = WN / W;                // lanes a row
+  constexpr int RPP = 64 / LPR;              // rows a pass
+  constexpr int PASS = 16 / RPP;             // passes a 16-row block
+  constexpr int PITCH = WN + 4;              // floats a row in LDS
+  __shared__ __align__(16) float s_epi[MODE == kTilePlain ? 4 : (NT / 64) * 16 * PITCH];
   auto store_tile_epi = [&](int i0, int j0) {
-    const int jw = j0 + WN * wn;  // this wave's columns
-    int grow[BI];                 // gate rows
+    // the lane number anew, opaque to the compiler: it would otherwise compute the
+    // addresses below ahead of the main loop and keep them in registers across it
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    float* mine = s_epi + wave * 16 * PITCH;
+    const int er = l / LPR, ec = (l % LPR) * W;  // this lane's row of a pass and column
+    float* put = mine + (l & 15) * PITCH + 4 * (l >> 4);
+    const int j = j0 + WN * wn + ec;
+    const int ib = i0 + WM * wm + er;
+    float bv[W];
 #pragma unroll
-    for (int bi = 0; bi < BI; ++bi) grow[bi] = ep.gate ? (i0 + WM * wm + 16 * bi + r) / ep.gate_rows : 0;
+    for (int e = 0; e < W; ++e) bv[e] = 0.0f;
+    if (bias) load_cols<W, true>(bias, j, n, W == 8 ? ep.b_vec16 : ep.b_vec, bv);
+    auto residual = [&](int bi, float (&rv)[PASS][W]) {
 #pragma unroll
-    for (int bj = 0; bj < BJ; ++bj) {
-      const int j = jw + 16 * bj + 4 * c;
-      f32x4 gv[BI], rv[BI];
-      if (ep.gate) {
-#pragma unroll
-        for (int bi = 0; bi < BI; ++bi)
-          if (i0 + WM * wm + 16 * bi + r < row_end)
-            gv[bi] = load4<true>(row_of<true>(ep.gate, grow[bi], n), j, n, ep.g_vec);
+      for (int q = 0; q < PASS; ++q) {
+        const int i = ib + 16 * bi + RPP * q;
+        if (i < row_end && j < n) load_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, ep.r_vec16, rv[q]);
       }
-      if (ep.residual) {
+    };
+    const bool acts = j0 + WN * wn + WN > ep.act_begin;
+    // NVFP4: no block ahead (its registers are full)
+    constexpr int AHEAD = F4 ? 0 : 1;
+    float rv[1 + AHEAD][PASS][W];
+    if (AHEAD && ep.residual) residual(0, rv[0]);
 #pragma unroll
-        for (int bi = 0; bi < BI; ++bi) {
-          const int i = i0 + WM * wm + 16 * bi + r;
-          if (i < row_end) rv[bi] = load4<OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, ep.r_vec);
+    for (int bi = 0; bi < BI; ++bi) {
+#pragma unroll
+      for (int bj = 0; bj < BJ; ++bj) *reinterpret_cast<f32x4*>(put + 16 * bj) = acc[bi][bj];
+      // one wave's LDS accesses complete in order; the fences keep the compiler to it
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (ep.residual && bi + AHEAD < BI) residual(bi + AHEAD, rv[(bi + AHEAD) % (1 + AHEAD)]);
+#pragma unroll
+      for (int q = 0; q < PASS; ++q) {
+        const int i = ib + 16 * bi + RPP * q;
+        float v[W];
+#pragma unroll
+        for (int h = 0; h < W / 4; ++h) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(mine + (er + RPP * q) * PITCH + ec + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e] + bv[4 * h + e];
+        }
+        if (acts) {
+          with_act(ep.act, [&](auto A) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              const float a = act_value<decltype(A)::value>(v[e]);
+              v[e] = j + e >= ep.act_begin ? a : v[e];
+            }
+          });
+        }
+        if (i < row_end && j < n) {
+          if (ep.gate) {
+            float gv[W];
+            load_cols<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, W == 8 ? ep.g_vec16 : ep.g_vec, gv);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] *= gv[e];
+          }
+          if (ep.residual) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = rv[bi % (1 + AHEAD)][q][e] + v[e];
+          }
+          store_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, ep.y_vec16, v);
         }
       }
-      if (bias) {
-        const f32x4 bv = load4<true>(bias, j, n, ep.b_vec);
-#pragma unroll
-        for (int bi = 0; bi < BI; ++bi) acc[bi][bj] += bv;
-      }
-      if (jw + 16 * bj + 16 > ep.act_begin) {
-        with_act(ep.act, [&](auto A) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const bool on = j + v >= ep.act_begin;
-#pragma unroll
-            for (int bi = 0; bi < BI; ++bi) {
-              const float a = act_value<decltype(A)::value>(acc[bi][bj][v]);
-              acc[bi][bj][v] = on ? a : acc[bi][bj][v];
-            }
-          }
-        });
-      }
-#pragma unroll
-      for (int bi = 0; bi < BI; ++bi) {
-        const int i = i0 + WM * wm + 16 * bi + r;
-        if (i >= row_end) continue;
-        f32x4 o = acc[bi][bj];
-        if (ep.gate) o *= gv[bi];
-        if (ep.residual) o = rv[bi] + o;
-        store4<OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, ep.y_vec, o);
-      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
   };
 
@@ -760,8 +858,17 @@ __device__ __forceinline__ void gemm_up_body(
   zero_acc();
   main_branch(i0, j0, g0, g1, [&] {
     // the tile's last groups carry the low-rank branch
-    if constexpr (!POST)
-      if (g1 == G) lowrank(i0, j0);
+    if constexpr (!POST) {
+      if (g1 == G) {
+        if constexpr (MODE == kTilePlain) {
+          lowrank(i0, j0);
+        } else if (rank > 0) {
+          // in the buffer that step 1 will be the first to write
+          lowrank_lds(i0, j0, As[1], Bs[1]);
+          __syncthreads();
+        }
+      }
+    }
   });
   if constexpr (SK) {
     if (split) {
@@ -802,7 +909,13 @@ __device__ __forceinline__ void gemm_up_body(
   }
   if constexpr (POST) {
     if (!split) scale_sums(i0, j0);
-    lowrank(i0, j0);
+    if constexpr (MODE == kTilePlain) {
+      lowrank(i0, j0);
+    } else {
+      // both buffers are free: the main loop ended with a barrier
+      static_assert(sizeof(As) >= TM * 64 && sizeof(Bs) >= TN * 64, "space for 32 ranks");
+      lowrank_lds(i0, j0, As[0], Bs[0]);
+    }
     if constexpr (SK) {
       if (split) {
         const __amdgpu_buffer_rsrc_t rp =
