@@ -27,8 +27,7 @@ bool overlap(const void* a, int lda, const void* b, int ldb, int rows, int n, in
 }
 
 // Checks an epilogue for an output of b x n and fills the kernels' arguments.
-int check_epilogue(const svdq_epilogue* epi, const uint16_t* bias, bool bias_rows, int b, int n, void* y, int y_dtype,
-                   EpiArgs* out) {
+int check_epilogue(const svdq_epilogue* epi, int b, int n, void* y, int y_dtype, EpiArgs* out) {
   const svdq_epilogue e = epi ? *epi : svdq_epilogue{SVDQ_ACT_NONE, 0, 0, 0, 0, nullptr, nullptr};
   REQUIRE(e.act >= SVDQ_ACT_NONE && e.act <= SVDQ_ACT_RELU, SVDQ_ERR_INVALID_ARG, "unknown activation %d", e.act);
   REQUIRE(e.act_begin >= 0 && e.act_begin <= n, SVDQ_ERR_INVALID_ARG, "act_begin must be in [0, %d] (got %d)", n,
@@ -45,7 +44,6 @@ int check_epilogue(const svdq_epilogue* epi, const uint16_t* bias, bool bias_row
   if (e.residual && b > 0 && !(e.residual == y && (ldr == ldy || b == 1)))
     REQUIRE(!overlap(e.residual, ldr, y, ldy, b, n, size), SVDQ_ERR_INVALID_ARG,
             "residual overlaps y without being y itself");
-  const uintptr_t mask = y_dtype == SVDQ_OUT_F32 ? 15u : 7u;  // four elements
   out->gate = e.gate;
   out->residual = e.residual;
   out->y = y;
@@ -54,15 +52,6 @@ int check_epilogue(const svdq_epilogue* epi, const uint16_t* bias, bool bias_row
   out->gate_rows = e.gate_rows ? e.gate_rows : std::max(b, 1);
   out->ldr = ldr;
   out->ldy = ldy;
-  out->b_vec = ((uintptr_t)bias & 7u) == 0 && (!bias_rows || n % 4 == 0);
-  out->g_vec = ((uintptr_t)e.gate & 7u) == 0 && n % 4 == 0;
-  out->r_vec = ((uintptr_t)e.residual & mask) == 0 && ldr % 4 == 0;
-  out->y_vec = ((uintptr_t)y & mask) == 0 && ldy % 4 == 0;
-  const int wide = 16 / size;  // elements of y in 16 bytes
-  out->b_vec16 = aligned16(bias) && (!bias_rows || n % 8 == 0);
-  out->g_vec16 = aligned16(e.gate) && n % 8 == 0;
-  out->r_vec16 = aligned16(e.residual) && ldr % wide == 0;
-  out->y_vec16 = aligned16(y) && ldy % wide == 0;
   return SVDQ_OK;
 }
 
@@ -146,7 +135,7 @@ int check_grouped_gemm(const int32_t* offsets, const svdq_grouped_layer* L, cons
   // the kernels number their tiles (16 x 16 at the smallest) with 32-bit integers
   REQUIRE(grouped_row_blocks(b, L->experts, 16) * ((L->n + 15) / 16) <= 0x7FFFFFFF, SVDQ_ERR_UNSUPPORTED,
           "too many output tiles (b=%d, n=%d, experts=%d)", b, L->n, L->experts);
-  return check_epilogue(epi, L->bias, true, b, L->n, y, y_dtype, ep);
+  return check_epilogue(epi, b, L->n, y, y_dtype, ep);
 }
 
 struct GroupedWorkspace {
@@ -193,7 +182,7 @@ int svdq_gemm_w4a4_lowrank_up_epi(const uint8_t* qx, const uint16_t* ascale, con
   int st = check_layer(layer);
   if (!st) st = check_rows(b);
   if (!st) st = check_y(y, y_dtype, b);
-  if (!st) st = check_epilogue(epi, layer->bias, false, b, layer->n, y, y_dtype, &ep);
+  if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_operands(qx, ascale, z, layer->rank, 2);
   if (!st) st = check_workspace(workspace, workspace_bytes, gemm_epi_ws_bytes(b, layer->n, layer->m), 16);
@@ -209,7 +198,7 @@ int svdq_w8a8_gemm_lowrank_up_epi(const int8_t* qx, const uint16_t* ascale, cons
   int st = check_layer8(layer);
   if (!st) st = check_rows(b);
   if (!st) st = check_y(y, y_dtype, b);
-  if (!st) st = check_epilogue(epi, layer->bias, false, b, layer->n, y, y_dtype, &ep);
+  if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_operands(qx, ascale, z, layer->rank, 2);
   if (!st) st = check_workspace(workspace, workspace_bytes, gemm_ws_bytes(b, layer->n, layer->m), 16);
@@ -225,7 +214,7 @@ int svdq_fp4_gemm_lowrank_up_epi(const uint8_t* qx, const uint8_t* ascale, const
   int st = check_layer_fp4(layer);
   if (!st) st = check_rows(b);
   if (!st) st = check_y(y, y_dtype, b);
-  if (!st) st = check_epilogue(epi, layer->bias, false, b, layer->n, y, y_dtype, &ep);
+  if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_operands(qx, ascale, z, layer->rank, 2);
   if (!st) st = check_workspace(workspace, workspace_bytes, gemm_ws_bytes(b, layer->n, layer->m), 16);
@@ -239,7 +228,7 @@ int svdq_linear_epi(const uint16_t* x, const svdq_layer* layer, const svdq_epilo
   bool done = false;
   EpiArgs ep;
   int st = check_linear(x, layer, b, y, y_dtype, &done);
-  if (!st) st = check_epilogue(epi, layer->bias, false, b, layer->n, y, y_dtype, &ep);
+  if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || done) return st;
   const LinearWorkspace w = linear_ws_layout(b, layer->m, layer->n, layer->rank);
   st = check_workspace(workspace, workspace_bytes, w.total, kAlign);
@@ -260,7 +249,7 @@ int svdq_w8a8_linear_epi(const uint16_t* x, const svdq_w8a8_layer* layer, const 
   int st = check_layer8(layer);
   if (!st) st = check_rows(b);
   if (!st) st = check_y(y, y_dtype, b);
-  if (!st) st = check_epilogue(epi, layer->bias, false, b, layer->n, y, y_dtype, &ep);
+  if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_input(x, layer->smooth_inv, layer->l1, layer->rank);
   if (st) return st;
@@ -283,7 +272,7 @@ int svdq_fp4_linear_epi(const uint16_t* x, const svdq_fp4_layer* layer, const sv
   int st = check_layer_fp4(layer);
   if (!st) st = check_rows(b);
   if (!st) st = check_y(y, y_dtype, b);
-  if (!st) st = check_epilogue(epi, layer->bias, false, b, layer->n, y, y_dtype, &ep);
+  if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_input(x, layer->smooth_inv, layer->l1, layer->rank);
   if (st) return st;

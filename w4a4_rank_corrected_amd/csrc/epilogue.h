@@ -79,15 +79,21 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
     f(std::integral_constant<int, SVDQ_ACT_RELU>{});
 }
 
-// Four consecutive columns j .. j+3 of a bf16 or fp32 row as floats.  `vec`:
-// the row's vectors are aligned; columns >= n read as zero.
+// Vectors at any element's address: gfx950 loads and stores them unaligned, so
+// a row need not start 16-byte aligned to be read and written by vectors.
+typedef u32x4 u32x4_loose __attribute__((aligned(2)));
+typedef uint2 uint2_loose __attribute__((aligned(2)));
+typedef f32x4 f32x4_loose __attribute__((aligned(4)));
+
+// Four consecutive columns j .. j+3 of a bf16 or fp32 row as floats; columns
+// >= n read as zero.
 template <bool BF16>
-__device__ __forceinline__ f32x4 load4(const void* row, int j, int n, bool vec) {
+__device__ __forceinline__ f32x4 load4(const void* row, int j, int n) {
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   if constexpr (BF16) {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + j;
-    if (vec && j + 3 < n) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
+    if (j + 3 < n) {
+      const uint2 w = *reinterpret_cast<const uint2_loose*>(p);
       v = f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
     } else {
 #pragma unroll
@@ -96,8 +102,8 @@ __device__ __forceinline__ f32x4 load4(const void* row, int j, int n, bool vec) 
     }
   } else {
     const float* p = reinterpret_cast<const float*>(row) + j;
-    if (vec && j + 3 < n) {
-      v = *reinterpret_cast<const f32x4*>(p);
+    if (j + 3 < n) {
+      v = *reinterpret_cast<const f32x4_loose*>(p);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -108,11 +114,11 @@ __device__ __forceinline__ f32x4 load4(const void* row, int j, int n, bool vec) 
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store4(void* row, int j, int n, bool vec, const f32x4& o) {
+__device__ __forceinline__ void store4(void* row, int j, int n, const f32x4& o) {
   if constexpr (BF16) {
     uint16_t* p = reinterpret_cast<uint16_t*>(row) + j;
-    if (vec && j + 3 < n) {
-      *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+    if (j + 3 < n) {
+      *reinterpret_cast<uint2_loose*>(p) = uint2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -120,8 +126,8 @@ __device__ __forceinline__ void store4(void* row, int j, int n, bool vec, const 
     }
   } else {
     float* p = reinterpret_cast<float*>(row) + j;
-    if (vec && j + 3 < n) {
-      *reinterpret_cast<f32x4*>(p) = o;
+    if (j + 3 < n) {
+      *reinterpret_cast<f32x4_loose*>(p) = o;
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -130,21 +136,20 @@ __device__ __forceinline__ void store4(void* row, int j, int n, bool vec, const 
   }
 }
 
-// W (4 or 8) consecutive columns j .. j+W-1 as floats; `vec`: the row's
-// 16-byte vectors are aligned (8 bytes for four bf16).  Columns >= n read as
-// zero.
+// W (4, or 8 of bf16) consecutive columns j .. j+W-1 as floats; columns >= n
+// read as zero.
 template <int W, bool BF16>
-__device__ __forceinline__ void load_cols(const void* row, int j, int n, bool vec, float (&v)[W]) {
+__device__ __forceinline__ void load_cols(const void* row, int j, int n, float (&v)[W]) {
   if constexpr (W == 4) {
-    const f32x4 x = load4<BF16>(row, j, n, vec);
+    const f32x4 x = load4<BF16>(row, j, n);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = x[e];
   } else {
     static_assert(W == 8 && BF16, "eight bf16 columns");
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + j;
     u32x4 w = {0u, 0u, 0u, 0u};
-    if (vec && j + 7 < n) {
-      w = ldg16(p);
+    if (j + 7 < n) {
+      w = *reinterpret_cast<const u32x4_loose*>(p);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -155,15 +160,15 @@ __device__ __forceinline__ void load_cols(const void* row, int j, int n, bool ve
   }
 }
 template <int W, bool BF16>
-__device__ __forceinline__ void store_cols(void* row, int j, int n, bool vec, const float (&v)[W]) {
+__device__ __forceinline__ void store_cols(void* row, int j, int n, const float (&v)[W]) {
   if constexpr (W == 4) {
-    store4<BF16>(row, j, n, vec, f32x4{v[0], v[1], v[2], v[3]});
+    store4<BF16>(row, j, n, f32x4{v[0], v[1], v[2], v[3]});
   } else {
     static_assert(W == 8 && BF16, "eight bf16 columns");
     uint16_t* p = reinterpret_cast<uint16_t*>(row) + j;
-    if (vec && j + 7 < n) {
-      *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                           pack_bf16x2(v[6], v[7])};
+    if (j + 7 < n) {
+      *reinterpret_cast<u32x4_loose*>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -190,9 +195,9 @@ struct EpiLoads {
 template <bool OUT_BF16>
 __device__ __forceinline__ EpiLoads load_unit(int i, int j, int n, const uint16_t* bias, const EpiArgs& ep) {
   EpiLoads l{{0.f, 0.f, 0.f, 0.f}, {1.f, 1.f, 1.f, 1.f}, {0.f, 0.f, 0.f, 0.f}};
-  if (bias) l.bias = load4<true>(bias, j, n, ep.b_vec);
-  if (ep.gate) l.gate = load4<true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, ep.g_vec);
-  if (ep.residual) l.residual = load4<OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, ep.r_vec);
+  if (bias) l.bias = load4<true>(bias, j, n);
+  if (ep.gate) l.gate = load4<true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n);
+  if (ep.residual) l.residual = load4<OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n);
   return l;
 }
 
@@ -209,7 +214,7 @@ __device__ __forceinline__ void finish_unit(f32x4 v, const EpiLoads& l, int i, i
   });
   if (ep.gate) v *= l.gate;
   if (ep.residual) v = l.residual + v;
-  store4<OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, ep.y_vec, v);
+  store4<OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, v);
 }
 
 }  // namespace dev

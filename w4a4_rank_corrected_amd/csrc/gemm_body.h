@@ -721,12 +721,12 @@ __device__ __forceinline__ void gemm_up_body(
     float bv[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) bv[e] = 0.0f;
-    if (bias) load_cols<W, true>(bias, j, n, W == 8 ? ep.b_vec16 : ep.b_vec, bv);
+    if (bias) load_cols<W, true>(bias, j, n, bv);
     auto residual = [&](int bi, float (&rv)[PASS][W]) {
 #pragma unroll
       for (int q = 0; q < PASS; ++q) {
         const int i = ib + 16 * bi + RPP * q;
-        if (i < row_end && j < n) load_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, ep.r_vec16, rv[q]);
+        if (i < row_end && j < n) load_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, rv[q]);
       }
     };
     const bool acts = j0 + WN * wn + WN > ep.act_begin;
@@ -764,7 +764,7 @@ __device__ __forceinline__ void gemm_up_body(
         if (i < row_end && j < n) {
           if (ep.gate) {
             float gv[W];
-            load_cols<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, W == 8 ? ep.g_vec16 : ep.g_vec, gv);
+            load_cols<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, gv);
 #pragma unroll
             for (int e = 0; e < W; ++e) v[e] *= gv[e];
           }
@@ -772,7 +772,7 @@ __device__ __forceinline__ void gemm_up_body(
 #pragma unroll
             for (int e = 0; e < W; ++e) v[e] = rv[bi % (1 + AHEAD)][q][e] + v[e];
           }
-          store_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, ep.y_vec16, v);
+          store_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, v);
         }
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

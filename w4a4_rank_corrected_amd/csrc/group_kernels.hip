@@ -204,74 +204,92 @@ __attribute__((amdgpu_waves_per_eu(group_waves_per_simd(TB)))) void grouped_act_
 
 // ---------------------------------------------------------------------------
 // y[t] = residual[t] + sum_k weight[t][k] rows[index[t][k]], in fp32 in the
-// order of k, rounded once.  A thread takes VEC consecutive columns of a token
-// and issues the loads of up to kCombineBatch rows together.  An index outside
-// [0, R) adds nothing.
+// order of k, rounded once.  A thread takes W consecutive columns (16 bytes) of
+// a token and issues the loads of up to kCombineBatch rows together, keeping
+// them as they lie in memory until they are added (62 registers, so every wave
+// slot of a CU is used).  Rows that do not start 16-byte aligned go the same way
+// with element-aligned vectors (gfx950 loads and stores them at any address);
+// only the last columns of a row are taken one by one.  An index outside [0, R)
+// adds nothing.
+// Bound by memory: 4096 tokens x 6 rows of 2048 bf16 28.6 us, 4.7 TB/s (36 us
+// with the rows widened to fp32 on arrival: 100 registers).
 // ---------------------------------------------------------------------------
 constexpr int kCombineBatch = 8;
-template <bool BF16, bool VEC>
+template <bool BF16, bool ALIGNED>
 __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ rows, int R, int n,
                                                       const int32_t* __restrict__ index,
                                                       const float* __restrict__ weight, int t_count, int k,
                                                       const void* residual, void* y, int units) {
-  constexpr int W = VEC ? (BF16 ? 8 : 4) : 1;  // columns per thread
+  constexpr int W = BF16 ? 8 : 4;  // columns per thread
+  typedef typename std::conditional<BF16, uint16_t, uint32_t>::type Element;
+  typedef u32x4 Loose __attribute__((aligned(2)));
+  typedef typename std::conditional<ALIGNED, u32x4, Loose>::type Vector;
   const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long t = u / units;
   if (t >= t_count) return;
   const int j = (int)(u - t * units) * W;
-  auto get = [&](const void* base, long long row, float (&v)[W]) {
-    const size_t at = (size_t)row * n + j;
-    if constexpr (!VEC) {
-      v[0] = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[at] << 16)
-                  : reinterpret_cast<const float*>(base)[at];
-    } else if constexpr (BF16) {
-      const u32x4 w = ldg16(reinterpret_cast<const uint16_t*>(base) + at);
+  const int cols = min(n - j, W);
+  auto get = [&](const void* base, long long row) -> u32x4 {
+    const Element* p = reinterpret_cast<const Element*>(base) + (size_t)row * n + j;
+    if (ALIGNED || cols == W) return *reinterpret_cast<const Vector*>(p);
+    u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
-    } else {
-      const f32x4 w = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(base) + at);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = w[e];
-    }
+    for (int e = 0; e < W; ++e)
+      if (e < cols) {
+        if constexpr (BF16)
+          v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        else
+          v[e] = p[e];
+      }
+    return v;
   };
-  float sum[W], res[W];
+  auto value = [](const u32x4& w, int e) -> float {
+    if constexpr (BF16) return e & 1 ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+    return __uint_as_float(w[e]);
+  };
+  float sum[W];
 #pragma unroll
-  for (int e = 0; e < W; ++e) sum[e] = res[e] = 0.0f;
-  if (residual) get(residual, t, res);
+  for (int e = 0; e < W; ++e) sum[e] = 0.0f;
+  u32x4 res = {0u, 0u, 0u, 0u};
+  if (residual) res = get(residual, t);
   for (int q0 = 0; q0 < k; q0 += kCombineBatch) {
-    float v[kCombineBatch][W], w[kCombineBatch];
+    u32x4 v[kCombineBatch];
+    float w[kCombineBatch];
 #pragma unroll
     for (int q = 0; q < kCombineBatch; ++q) {
       w[q] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < W; ++e) v[q][e] = 0.0f;
+      v[q] = u32x4{0u, 0u, 0u, 0u};
       if (q0 + q < k) {
         const int i = index[t * k + q0 + q];
         if (i >= 0 && i < R) {
           w[q] = weight ? weight[t * k + q0 + q] : 1.0f;
-          get(rows, i, v[q]);
+          v[q] = get(rows, i);
         }
       }
     }
 #pragma unroll
     for (int q = 0; q < kCombineBatch; ++q)
 #pragma unroll
-      for (int e = 0; e < W; ++e) sum[e] = __builtin_fmaf(w[q], v[q][e], sum[e]);
+      for (int e = 0; e < W; ++e) sum[e] = __builtin_fmaf(w[q], value(v[q], e), sum[e]);
   }
+  if (residual)
 #pragma unroll
-  for (int e = 0; e < W; ++e) sum[e] = res[e] + sum[e];
-  const size_t at = (size_t)t * n + j;
-  if constexpr (!VEC) {
-    if (BF16)
-      reinterpret_cast<uint16_t*>(y)[at] = bf16_bits(sum[0]);
+    for (int e = 0; e < W; ++e) sum[e] = value(res, e) + sum[e];
+  Element* p = reinterpret_cast<Element*>(y) + (size_t)t * n + j;
+  u32x4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (BF16)
+      o[e] = pack_bf16x2(sum[2 * e], sum[2 * e + 1]);
     else
-      reinterpret_cast<float*>(y)[at] = sum[0];
-  } else if constexpr (BF16) {
-    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(y) + at) =
-        u32x4{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]), pack_bf16x2(sum[4], sum[5]),
-              pack_bf16x2(sum[6], sum[7])};
+      o[e] = __float_as_uint(sum[e]);
+  }
+  if (ALIGNED || cols == W) {
+    *reinterpret_cast<Vector*>(p) = o;
   } else {
-    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(y) + at) = f32x4{sum[0], sum[1], sum[2], sum[3]};
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+      if (e < cols) p[e] = BF16 ? (Element)(o[e >> (BF16 ? 1 : 0)] >> (BF16 ? 16 * (e & 1) : 0)) : (Element)o[e & 3];
   }
 }
 
@@ -324,16 +342,16 @@ int launch_combine(const void* rows, int R, int n, int dtype, const int32_t* ind
                    const void* residual, void* y, void* stream) {
   const bool bf = dtype == SVDQ_OUT_BF16;
   const int w = bf ? 8 : 4;
-  const bool vec = n % w == 0 && (((uintptr_t)rows | (uintptr_t)residual | (uintptr_t)y) & 15u) == 0;
-  const int units = vec ? n / w : n;
+  const bool aligned = n % w == 0 && (((uintptr_t)rows | (uintptr_t)residual | (uintptr_t)y) & 15u) == 0;
+  const int units = (n + w - 1) / w;
   const long long grid = ((long long)t * units + 255) / 256;
   if (grid > 0x7FFFFFFF) return (int)hipErrorInvalidValue;
   auto go = [&](auto kernel) {
     return launch_checked(kernel, (int)grid, 256, (hipStream_t)stream, rows, R, n, index, weight, t, k, residual, y,
                           units);
   };
-  if (bf) return vec ? go(combine_kernel<true, true>) : go(combine_kernel<true, false>);
-  return vec ? go(combine_kernel<false, true>) : go(combine_kernel<false, false>);
+  if (bf) return aligned ? go(combine_kernel<true, true>) : go(combine_kernel<true, false>);
+  return aligned ? go(combine_kernel<false, true>) : go(combine_kernel<false, false>);
 }
 
 }  // namespace svdq

@@ -172,15 +172,12 @@ const char* hip_error_name(int err);
 
 // ---- products with an epilogue, and grouped by expert --------------------------
 // What the epilogue of a product needs, as the kernels take it: svdq_epilogue
-// with its strides filled in, and whether all rows of a tensor allow vector
-// accesses of four elements (*_vec) and of 16 bytes (*_vec16).
+// with its strides filled in.
 struct EpiArgs {
   const uint16_t* gate;  // bf16 [ceil(b / gate_rows)][n] or NULL
   const void* residual;  // y's type, row stride ldr, or NULL
   void* y;               // row stride ldy
   int act, act_begin, gate_rows, ldr, ldy;
-  bool b_vec, g_vec, r_vec, y_vec;
-  bool b_vec16, g_vec16, r_vec16, y_vec16;
 };
 // The experts' rows of a grouped product.
 struct Groups {
