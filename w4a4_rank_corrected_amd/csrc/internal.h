@@ -201,7 +201,7 @@ int launch_gemm_fp4_epi(const uint8_t* qx, const uint8_t* ascale, const float* z
 int launch_grouped_gemm(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_grouped_layer& L,
                         const int32_t* offsets, int b, int y_dtype, const EpiArgs& ep, void* stream);
 // The row kernel (rows_kernels.hip), for one layer (groups.offsets NULL) or
-// grouped by expert; rb = 16-row blocks per workgroup (1, 2 or 4).
+// grouped by expert; rb = 16-row blocks per workgroup (1, 2, or 4 without groups).
 struct RowsArgs {
   const uint8_t* qx;
   const uint16_t* ascale;

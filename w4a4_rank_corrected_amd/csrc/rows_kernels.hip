@@ -1,5 +1,5 @@
-// INT4 product with an epilogue for few rows (up to 64, or up to 64 rows of one
-// expert at a time): the layer's weights are read once and bound it.
+// INT4 product with an epilogue for few rows (up to 64, or 16 or 32 rows of one
+// expert at a time): the layer's weights bound it.
 //
 // Y = epilogue(sum_g sx[g,i] sw[g,j] isum[i,j,g] + (bf16(Z) L2)[i,j] + bias[j]),
 // with the exact per-group integer sums and the two FMAs per element and group
@@ -238,7 +238,8 @@ int launch_rows(const RowsArgs& a, hipStream_t st) {
 template <int RB>
 int launch_rb(const RowsArgs& a, int y_dtype, hipStream_t st) {
   const bool bf = y_dtype == SVDQ_OUT_BF16;
-  if (a.groups.offsets) return bf ? launch_rows<RB, true, true>(a, st) : launch_rows<RB, false, true>(a, st);
+  if constexpr (RB <= 2)
+    if (a.groups.offsets) return bf ? launch_rows<RB, true, true>(a, st) : launch_rows<RB, false, true>(a, st);
   return bf ? launch_rows<RB, true, false>(a, st) : launch_rows<RB, false, false>(a, st);
 }
 
@@ -246,8 +247,8 @@ int launch_rb(const RowsArgs& a, int y_dtype, hipStream_t st) {
 
 int launch_gemm_rows(const RowsArgs& a, int rb, int y_dtype, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  // without groups one workgroup covers every row
-  if (!a.groups.offsets && a.b > 16 * rb) return (int)hipErrorInvalidValue;
+  // without groups one workgroup covers every row; experts' row blocks are 16 or 32 rows
+  if (a.groups.offsets ? rb > 2 : a.b > 16 * rb) return (int)hipErrorInvalidValue;
   if (rb == 1) return launch_rb<1>(a, y_dtype, st);
   if (rb == 2) return launch_rb<2>(a, y_dtype, st);
   if (rb == 4) return launch_rb<4>(a, y_dtype, st);
