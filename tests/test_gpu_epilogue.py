@@ -145,7 +145,9 @@ def test_int4_shapes(S, b, m, n, rank, out):
 
 
 @pytest.mark.parametrize("fmt", ["w8a8", "fp4"])
-@pytest.mark.parametrize("b,m,n,rank", [(1, 64, 1, 0), (5, 192, 70, 9), (256, 4096, 256, 16), (300, 2368, 201, 33)])
+# 8-bit: 64 x 64 tiles up to 384 wide ones, split tiles where those are few and long, whole wide tiles (the last)
+@pytest.mark.parametrize("b,m,n,rank", [(1, 64, 1, 0), (5, 192, 70, 9), (256, 4096, 256, 16), (300, 2368, 201, 33),
+                                        (300, 4352, 130, 40), (1100, 64, 5640, 20)])
 def test_other_settings_shapes(S, fmt, b, m, n, rank):
     _say(f"{fmt} b={b} m={m} n={n} rank={rank}")
     c = Case(S, fmt, b, m, n, rank, bias=n % 2 == 0)

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_body.h"
 #include "launch.h"
@@ -23,6 +24,9 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C
                                                tiles_n, nullptr, sk, txw, ep);
 }
 
+// 8-bit codes, few tiles: 64 x 64 tiles, 4 waves of 32 x 32, loads three groups
+// ahead (90 registers).
+using Cfg8S = GemmCfg<64, 64, 32, 32, 4, 3>;
 // Experts with few rows: 64 x 128 tiles, 4 waves of 64 x 32.
 using CfgG = GemmCfg<64, 128, 64, 32, 3, 2>;
 
@@ -58,11 +62,10 @@ int launch_tiles(const uint8_t* qx, const uint16_t* ascale, const float* z, cons
       return launch_checked(kernel, plan.grid, C::NT, st, qx, ascale, z, L, b, plan.G, plan.tiles_m, plan.tiles_n, sk,
                             txw, ep);
     };
-    if constexpr (FMT == kFmtFp4) {
-      if (plan.split) return (int)hipErrorInvalidValue;  // NVFP4 tiles are never split
-      return gemm(gemm_epi_kernel<C, OUT_BF16, FMT, false>);
+    if (!plan.split) return gemm(gemm_epi_kernel<C, OUT_BF16, FMT, false>);
+    if constexpr (FMT == kFmtFp4 || std::is_same_v<C, Cfg8S>) {
+      return (int)hipErrorInvalidValue;  // never split
     } else {
-      if (!plan.split) return gemm(gemm_epi_kernel<C, OUT_BF16, FMT, false>);
       const int status = gemm(gemm_epi_kernel<C, OUT_BF16, FMT, true>);
       if (status != 0) return status;
       constexpr int UNITS = C::TM * C::TN / 4;
@@ -72,22 +75,37 @@ int launch_tiles(const uint8_t* qx, const uint16_t* ascale, const float* z, cons
                             FMT == kFmtInt8 && L.rank > 0 ? 1 : 0, L.bias, (void*)nullptr, ep);
     }
   };
-  if constexpr (FMT == kFmtInt8) return run(Cfg8{});
+  if constexpr (FMT == kFmtInt8) return plan.tile_n == Cfg8S::TN ? run(Cfg8S{}) : run(Cfg8{});
   if constexpr (FMT == kFmtFp4) return run(CfgF4{});
   if constexpr (FMT == kFmtInt4) return plan.tile_n == CfgN::TN ? run(CfgN{}) : run(Cfg{});
 }
 
-// The plan of the plain product, except that in the 8-bit setting a launch of
-// less than one round of tiles is split into as many pieces as give every CU one
-// workgroup, not three: its tiles are bound by the matrix units, which further
-// pieces share, while every piece adds a 64 KB partial tile to write and read
-// (1000 x 4608 -> 1152, 72 tiles: 3 pieces 21.4 us, 2: 24.0, 4: 23.4, 10: 27.3).
+// The plan of the plain product, except in the 8-bit setting, whose tiles are
+// bound by the matrix units and whose split pieces each write and read back a
+// 64 KB partial tile:
+//   * up to 384 tiles (half a round) are cut into 64 x 64 tiles instead, unsplit
+//     (us, plain plan / 64 x 64, rank 16, residual: 500 x 2048 -> 2048 17.5 / 11.0;
+//     1000 x 1152 -> 4608 33.2 / 20.8; 1500 x 4608 -> 2048 36.4 / 29.1; 576 tiles,
+//     2000 x 4608 -> 4608: 64 / 76), unless they are fewer than CUs and long
+//     (256 x 4608 -> 1152: 14.1 / 16.3);
+//   * a launch that is split whole gets as many pieces as give every CU one
+//     workgroup, not three (1000 x 4608 -> 1152, 72 tiles: 3 pieces 21.4 us, 2:
+//     24.0, 4: 23.4, 10: 27.3).
 GemmPlan epi_plan(int b, int n, int m, int fmt) {
   GemmPlan p = gemm_plan(b, n, m, device_cus(), fmt);
-  const int T = p.tiles_m * p.tiles_n;
-  if (fmt == kFmtInt8 && p.split && p.split_tiles == T) {
-    p.pieces = std::max(2, std::min(p.pieces, device_cus() / T));
-    p.split_grid = p.grid = T * p.pieces;
+  if (fmt != kFmtInt8) return p;
+  const long long T = (long long)p.tiles_m * p.tiles_n;
+  const int sm = (b + Cfg8S::TM - 1) / Cfg8S::TM, sn = (n + Cfg8S::TN - 1) / Cfg8S::TN;
+  if (T <= 384 && (p.G < 64 || (long long)sm * sn >= device_cus())) {
+    p.tiles_m = sm;
+    p.tiles_n = sn;
+    p.tile_n = Cfg8S::TN;
+    p.grid = sm * sn;
+    p.split = p.split_tiles = p.split_grid = 0;
+    p.pieces = 1;
+  } else if (p.split && p.split_tiles == T) {
+    p.pieces = (int)std::max<long long>(2, std::min<long long>(p.pieces, device_cus() / T));
+    p.split_grid = p.grid = (int)T * p.pieces;
   }
   return p;
 }

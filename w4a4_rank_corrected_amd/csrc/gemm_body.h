@@ -97,10 +97,12 @@ __device__ __forceinline__ void unpack_piece(uint8_t* row, int rs, int w0, const
 
 // Copy a piece of an 8-bit record (64 codes, one byte each) starting at word w0
 // into the LDS row `row` (swizzle rs), chunk by chunk.
-__device__ __forceinline__ void copy_piece(uint8_t* row, int rs, int w0, const Piece<32>& p) {
+template <int BYTES>
+__device__ __forceinline__ void copy_piece(uint8_t* row, int rs, int w0, const Piece<BYTES>& p) {
   const int j = w0 >> 2;
-  *reinterpret_cast<u32x4*>(row + 16 * (j ^ rs)) = u32x4{p.w[0], p.w[1], p.w[2], p.w[3]};
-  *reinterpret_cast<u32x4*>(row + 16 * ((j + 1) ^ rs)) = u32x4{p.w[4], p.w[5], p.w[6], p.w[7]};
+#pragma unroll
+  for (int h = 0; h < BYTES / 16; ++h)
+    *reinterpret_cast<u32x4*>(row + 16 * ((j + h) ^ rs)) = u32x4{p.w[4 * h], p.w[4 * h + 1], p.w[4 * h + 2], p.w[4 * h + 3]};
 }
 
 // f(integral_constant<int, U>) for each U of the sequence, in order (compile-time
@@ -155,7 +157,7 @@ struct GemmCfg {
   static_assert(A_BYTES == 4 || A_BYTES == 8 || A_BYTES == 16, "activation staging piece");
   static_assert(B_BYTES == 4 || B_BYTES == 8 || B_BYTES == 16, "weight staging piece");
   static_assert(NT >= TM + TN && TM % 64 == 0 && TN % 64 == 0, "scale staging: at most one scale per thread");
-  static_assert(BI == 4 && BJ % 2 == 0, "scale reads: one 16-byte row-scale vector, whole fp16 column vectors");
+  static_assert(BJ % 2 == 0, "whole fp16 vectors of column scales");
 };
 
 // 128 x 128 tile, 4 waves of 64 x 64; three workgroups share a CU (168
@@ -257,7 +259,8 @@ __device__ __forceinline__ void gemm_up_body(
   // INT4 starts the accumulators from the low-rank product; the 8-bit and
   // NVFP4 settings apply their scales after the main loop and then add it.
   constexpr bool POST = W8 || F4;
-  static_assert(!W8 || (2 * C::A_BYTES == 32 && 2 * C::B_BYTES == 32), "8-bit records: 32-byte staging pieces");
+  static_assert(!W8 || (C::A_BYTES >= 8 && C::B_BYTES >= 8), "8-bit records: staging pieces of 16 or 32 bytes");
+  static_assert(FMT != kFmtInt4 || C::BI == 4, "scale reads: one 16-byte row-scale vector");
   static_assert(!F4 || (C::A_BYTES == 16 && C::B_BYTES == 16), "FP4 records: 16-byte staging pieces");
   constexpr int TM = C::TM, TN = C::TN, WM = C::WM, WN = C::WN, NT = C::NT;
   constexpr int BI = C::BI, BJ = C::BJ;
