@@ -196,10 +196,11 @@ class _Fake:
         import torch
         self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
         self.is_cuda = True
-        self._stride = stride or tuple(int(__import__("math").prod(shape[i + 1:])) for i in range(len(shape)))
+        self._dense = tuple(int(__import__("math").prod(shape[i + 1:])) for i in range(len(shape)))
+        self._stride = stride or self._dense
 
     def is_contiguous(self):
-        return True
+        return self._stride == self._dense
 
     def dim(self):
         return len(self.shape)

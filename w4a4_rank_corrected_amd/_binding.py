@@ -912,6 +912,8 @@ def _rows(t, name: str, dtype, shape, device) -> int:
     one; returns its row stride."""
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a GPU tensor")
+    if t.device == device and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return shape[1]
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
@@ -968,10 +970,13 @@ def _gemm_epi(fn, size, operands, qx, ascale, z, layer, act, act_begin, gate, ga
     b = _gemm_operands(qx, ascale, z, layer, b, *operands)
     device = qx.device
     with _On(device, stream) as handle:
-        y, code, epi = _epilogue(b, layer.n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
-        workspace, wsb = _workspace(workspace, size(b, layer.n, layer.m) if workspace is None else 0, device)
-        _check(fn(_ptr(qx), _ptr(ascale), _ptr(z), ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code,
-                  workspace.data_ptr(), wsb, handle))
+        n = layer.n
+        y, code, epi = _epilogue(b, n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
+        workspace, wsb = _workspace(workspace, size(b, n, layer.m) if workspace is None else 0, device)
+        status = fn(qx.data_ptr(), ascale.data_ptr(), None if z is None else z.data_ptr(), ctypes.byref(layer.struct),
+                    ctypes.byref(epi), b, y.data_ptr(), code, workspace.data_ptr(), wsb, handle)
+        if status != SVDQ_OK:
+            _check(status)
     return y
 
 

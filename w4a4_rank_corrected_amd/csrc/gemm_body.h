@@ -732,7 +732,9 @@ __device__ __forceinline__ void gemm_up_body(
         if (i < row_end && j < n) load_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, rv[q]);
       }
     };
-    const bool acts = j0 + WN * wn + WN > ep.act_begin;
+    // all, or some, of this wave's columns are activated (wave-uniform)
+    const int jw = j0 + WN * (wave_u % C::WAVES_N);
+    const bool whole = jw >= ep.act_begin, acts = jw + WN > ep.act_begin;
     // NVFP4: no block ahead (its registers are full)
     constexpr int AHEAD = F4 ? 0 : 1;
     float rv[1 + AHEAD][PASS][W];
@@ -755,7 +757,12 @@ __device__ __forceinline__ void gemm_up_body(
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e] + bv[4 * h + e];
         }
-        if (acts) {
+        if (whole) {
+          with_act(ep.act, [&](auto A) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = act_value<decltype(A)::value>(v[e]);
+          });
+        } else if (acts) {
           with_act(ep.act, [&](auto A) {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
