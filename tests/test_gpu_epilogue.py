@@ -131,11 +131,11 @@ def test_activations(S, fmt, b, act):
 
 
 # rows: the row kernel's block sizes and their borders, one narrow tile, a tile border, split tiles (m = 2368 and
-# 4096 at a few hundred rows, m = 12288 behind a full round)
+# 4096 at a few hundred rows), narrow tiles that would not pay as pieces (200 rows), whole wide tiles (1100 rows)
 @pytest.mark.parametrize("b,m,n,rank", [
     (1, 64, 1, 0), (1, 4608, 77, 32), (2, 128, 16, 1), (15, 192, 33, 7), (16, 1024, 256, 16), (17, 2048, 61, 33),
     (32, 512, 130, 64), (33, 576, 18, 100), (64, 2048, 100, 256), (65, 64, 5, 8), (129, 1152, 260, 32), (256, 4096, 256, 16),
-    (300, 2368, 203, 24), (4608, 640, 129, 8)])
+    (300, 2368, 203, 24), (4608, 640, 129, 8), (200, 1152, 4608, 16), (1100, 64, 5640, 40)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_int4_shapes(S, b, m, n, rank, out):
     _say(f"int4 b={b} m={m} n={n} rank={rank} {out}")

@@ -127,7 +127,7 @@ def test_quantize(S, E, b, m, rank, pad, gather):
 # the row kernel's block sizes, the 64-row tiles (many small experts; many channels), the 128-row tiles (the last two)
 @pytest.mark.parametrize("E,b,m,n,rank,pad", [
     (1, 1, 64, 1, 0, 0), (2, 3, 4608, 40, 32, 0), (16, 9, 512, 77, 16, 2), (7, 100, 192, 33, 7, 0), (3, 80, 1024, 130, 33, 10),
-    (4, 200, 256, 64, 100, 0), (64, 500, 128, 36, 16, 7), (100, 900, 64, 20, 3, 0), (3, 400, 640, 203, 24, 11),
+    (4, 200, 256, 64, 100, 0), (64, 500, 128, 36, 16, 7), (100, 900, 64, 20, 3, 0), (1024, 700, 64, 40, 8, 3), (3, 400, 640, 203, 24, 11),
     (5, 1500, 192, 300, 0, 0), (2, 300, 2048, 129, 256, 1), (64, 1500, 64, 1100, 20, 3), (130, 1400, 128, 1283, 0, 0),
     (3, 400, 4096, 3000, 33, 11), (2, 1100, 128, 11001, 16, 5), (1, 1100, 64, 11264, 40, 0)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])

@@ -80,32 +80,54 @@ int launch_tiles(const uint8_t* qx, const uint16_t* ascale, const float* z, cons
   if constexpr (FMT == kFmtInt4) return plan.tile_n == CfgN::TN ? run(CfgN{}) : run(Cfg{});
 }
 
-// The plan of the plain product, except in the 8-bit setting, whose tiles are
-// bound by the matrix units and whose split pieces each write and read back a
-// 64 KB partial tile:
-//   * up to 384 tiles (half a round) are cut into 64 x 64 tiles instead, unsplit
-//     (us, plain plan / 64 x 64, rank 16, residual: 500 x 2048 -> 2048 17.5 / 11.0;
-//     1000 x 1152 -> 4608 33.2 / 20.8; 1500 x 4608 -> 2048 36.4 / 29.1; 576 tiles,
-//     2000 x 4608 -> 4608: 64 / 76), unless they are fewer than CUs and long
-//     (256 x 4608 -> 1152: 14.1 / 16.3);
+// One tile of TM x TN per workgroup, none split.
+template <class C>
+void whole_tiles(GemmPlan& p, int b, int n) {
+  p.tiles_m = (b + C::TM - 1) / C::TM;
+  p.tiles_n = (n + C::TN - 1) / C::TN;
+  p.tile_n = C::TN;
+  p.grid = p.tiles_m * p.tiles_n;
+  p.split = p.split_tiles = p.split_grid = 0;
+  p.pieces = 1;
+}
+
+// The plan of the plain product, except for less than one round of tiles (768):
+// INT4, T = wide (128 x 128) tiles:
+//   * above half a round whole wide tiles, not narrow ones (rank 16, residual, us:
+//     1500 x 1152 -> 4608, T = 432, 32.0 narrow / 29.6 wide; 2500 rows, T = 720,
+//     42.3 / 37.0; 3000 x 2048 -> 2048, T = 384, 34.7 / 42.4);
+//   * pieces only where they pay.  A narrow tile takes about half a microsecond a
+//     group, so k pieces save G (1 - 1/k) / 2; they cost a launch and 64 KB of
+//     traffic a piece, about 1.5 us + 0.013 us a piece (split / whole, us:
+//     200 x 1152 -> 4608 16.4 / 14.5, 500 rows 22.4 / 19.5, 1000 x 2048 -> 2048
+//     24.4 / 21.9; 500 x 2048 -> 2048 17.5 / 20.6, 256 x 4096 -> 8000 31.9 / 36.6,
+//     1000 x 4608 -> 1152 24.7 / 39.9).
+// 8 bits, whose tiles are bound by the matrix units:
+//   * up to 384 tiles are cut into 64 x 64 tiles instead, unsplit (plain plan /
+//     64 x 64: 500 x 2048 -> 2048 17.5 / 11.0; 1000 x 1152 -> 4608 33.2 / 20.8;
+//     1500 x 4608 -> 2048 36.4 / 29.1; 576 tiles, 2000 x 4608 -> 4608: 64 / 76),
+//     unless they are fewer than CUs and long (256 x 4608 -> 1152: 14.1 / 16.3);
 //   * a launch that is split whole gets as many pieces as give every CU one
 //     workgroup, not three (1000 x 4608 -> 1152, 72 tiles: 3 pieces 21.4 us, 2:
 //     24.0, 4: 23.4, 10: 27.3).
 GemmPlan epi_plan(int b, int n, int m, int fmt) {
   GemmPlan p = gemm_plan(b, n, m, device_cus(), fmt);
-  if (fmt != kFmtInt8) return p;
-  const long long T = (long long)p.tiles_m * p.tiles_n;
-  const int sm = (b + Cfg8S::TM - 1) / Cfg8S::TM, sn = (n + Cfg8S::TN - 1) / Cfg8S::TN;
-  if (T <= 384 && (p.G < 64 || (long long)sm * sn >= device_cus())) {
-    p.tiles_m = sm;
-    p.tiles_n = sn;
-    p.tile_n = Cfg8S::TN;
-    p.grid = sm * sn;
-    p.split = p.split_tiles = p.split_grid = 0;
-    p.pieces = 1;
-  } else if (p.split && p.split_tiles == T) {
-    p.pieces = (int)std::max<long long>(2, std::min<long long>(p.pieces, device_cus() / T));
-    p.split_grid = p.grid = (int)T * p.pieces;
+  const long long T = (long long)p.tiles_m * p.tiles_n, slots = (long long)p.wg_per_cu * device_cus();
+  if (fmt == kFmtInt4 && T < 2 * slots && p.tile_n == CfgN::TN) {
+    const long long wide = (long long)p.tiles_m * ((n + Cfg::TN - 1) / Cfg::TN);
+    if (2 * wide > slots + 32)
+      whole_tiles<Cfg>(p, b, n);
+    else if (p.split && 0.5 * p.G * (1.0 - 1.0 / p.pieces) <= 1.5 + 0.013 * (double)p.split_grid)
+      whole_tiles<CfgN>(p, b, n);
+  }
+  if (fmt == kFmtInt8) {
+    const long long small = (long long)((b + Cfg8S::TM - 1) / Cfg8S::TM) * ((n + Cfg8S::TN - 1) / Cfg8S::TN);
+    if (T <= 384 && (p.G < 64 || small >= device_cus())) {
+      whole_tiles<Cfg8S>(p, b, n);
+    } else if (p.split && p.split_tiles == T) {
+      p.pieces = (int)std::max<long long>(2, std::min<long long>(p.pieces, device_cus() / T));
+      p.split_grid = p.grid = (int)T * p.pieces;
+    }
   }
   return p;
 }
