@@ -325,3 +325,43 @@ def test_graph_replay(S, b):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want), k
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_products(S, seed):
+    rng = np.random.default_rng([7, seed])
+    fmt = ["int4", "int4", "w8a8", "fp4"][rng.integers(4)]
+    b, n = int(np.exp(rng.uniform(0, np.log(700)))), int(np.exp(rng.uniform(0, np.log(900))))
+    m, rank = 64 * int(rng.integers(1, 40)), int(rng.choice([0, 1, 8, 20, 32, 50, 64, 129]))
+    kw = dict(act=ACTS[rng.integers(5)], act_begin=int(rng.integers(0, n + 1)), residual=bool(rng.integers(2)),
+              gate_rows=[None, int(rng.integers(1, b + 1))][rng.integers(2)], out=["f32", "bf16"][rng.integers(2)],
+              inplace=bool(rng.integers(2)))
+    _say(f"random {fmt} b={b} m={m} n={n} rank={rank} {kw}")
+    Case(S, fmt, b, m, n, rank, bias=bool(rng.integers(2)), seed=seed).run(**kw)
+
+
+def test_outputs_past_32_bit_offsets(S):
+    """More than 2^31 outputs: the first and last rows, in place on the residual."""
+    b, m, n = 66000, 64, 33000
+    rng = np.random.default_rng(3)
+    rows = np.array([0, 1, 127, 128, 65071, 65073, 65535, 65536, b - 129, b - 1])
+    cx, cw = np.zeros((b, m), np.int8), rng.integers(-7, 8, (n, m)).astype(np.int8)
+    cx[rows] = rng.integers(-7, 8, (len(rows), m))
+    sx, sw = np.full((1, b), 0.25), (0.05 * np.exp(0.4 * rng.standard_normal((1, n)))).astype(np.float16).astype(np.float64)
+    layer = S.DeviceLayer.from_tensors(m, n, 0, torch.from_numpy(LY.pack_codes(cw)).cuda(),
+                                       torch.from_numpy(sw.astype(np.float16)).cuda())
+    y = torch.full((b, n), 1.5, dtype=torch.bfloat16, device="cuda")
+    assert y.numel() > 2 ** 31
+    S.svdq_gemm_w4a4_lowrank_up_epi(torch.from_numpy(LY.pack_codes(cx)).cuda(), torch.from_numpy(sx.astype(np.float16)).cuda(),
+                                    None, layer, act="silu", act_begin=100, residual=y, y=y)
+    torch.cuda.synchronize()
+    got = to_np(y[torch.from_numpy(rows).cuda()])
+    v, dv = R.product_int4(cx[rows], sx[:, rows], cw, sw)
+    want, tol = R.epilogue(v, dv, "silu", 100, residual=np.full(v.shape, 1.5), out="bf16")
+    assert (np.abs(got - want) <= tol).all()
+    assert bool((y[2:127] == 1.5).all()) and bool((y[65537:65600] == 1.5).all())
+    # the same rows combined: the index reaches past 2^31 elements
+    out = S.svdq_combine_rows(y, torch.tensor([[0, b - 1]], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    both = got[0] + got[-1]
+    assert (np.abs(to_np(out)[0] - both) <= np.abs(both) * 2.0 ** -8 + 1e-30).all()

@@ -359,3 +359,65 @@ def test_a_whole_expert_block(S):
             # z may round to the other bf16 neighbour: one step of it through l2
             tol = tol + 1.13 * (np.abs(R.bf16(z)) * 2.0 ** -7) @ np.abs(X.l2[e]).T
             assert (np.abs(got[lo:hi] - ref) <= tol).all(), e
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_grouped_linears(S, seed):
+    rng = np.random.default_rng([11, seed])
+    E, n = int(np.exp(rng.uniform(0, np.log(80)))), int(np.exp(rng.uniform(np.log(8), np.log(700))))
+    tokens, k = int(np.exp(rng.uniform(0, np.log(300)))), int(rng.integers(1, min(E, 4) + 1))
+    m, rank = 64 * int(rng.integers(1, 20)), int(rng.choice([0, 4, 16, 40, 65]))
+    act, pad = ["none", "gelu_erf", "silu", "relu"][rng.integers(4)], int(rng.integers(0, 3)) * 7
+    _say(f"random grouped E={E} tokens={tokens} k={k} m={m} n={n} rank={rank} {act} pad={pad}")
+    X = Experts(S, E, m, n, rank, bias=bool(rng.integers(2)), smooth=bool(rng.integers(2)), seed=seed)
+    x = R.bf16(rng.standard_normal((tokens, m)))
+    chosen = np.stack([rng.choice(E, k, replace=False) for _ in range(tokens)]).reshape(-1)
+    order = np.argsort(chosen, kind="stable")
+    off = np.concatenate([[0], np.cumsum(np.bincount(chosen, minlength=E))])
+    src = np.concatenate([order // k, rng.integers(-3, tokens + 3, pad)])
+    b = len(src)
+    dx, do, ds = dev_bf16(x), i32(off), i32(src)
+    begin = int(rng.integers(0, n + 1))
+    y = torch.full((b, n), 99.0, device="cuda")
+    S.svdq_grouped_linear(dx, do, X.layer, ds, act=act, act_begin=begin, y=y)
+    _, _, z = S.svdq_grouped_quantize_act_lowrank_down(dx, do, X.layer, ds)
+    torch.cuda.synchronize()
+    got, zz = to_np(y), to_np(z) if rank else np.zeros((b, 0))
+    assert (got[off[-1]:] == 99).all()
+    for e in range(E):
+        lo, hi = off[e], off[e + 1]
+        codes, s, zr, dz = X.quantized(e, x[src[lo:hi]])
+        assert (np.abs(zz[lo:hi] - zr) <= dz + 1e-38).all()
+        v, dv = R.product_int4(codes, s, X.cw[e], X.sw[e], zz[lo:hi], X.l2[e], X.bias[e] if X.bias is not None else None)
+        want, tol = R.epilogue(v, dv, act, begin)
+        assert (np.abs(got[lo:hi] - want) <= tol).all(), e
+
+
+def test_operands_past_32_bit_offsets(S):
+    """Activations and weights of more than 4 GB: rows gathered from the end of x, the last expert's layer."""
+    E, m, n, rank = 66, 4096, 32768, 16
+    rng = np.random.default_rng(4)
+    qw = torch.zeros((E, m // 64, n, 32), dtype=torch.uint8, device="cuda")
+    assert qw.numel() > 2 ** 32
+    one = Experts(S, 1, m, n, rank, bias=False, smooth=False)
+    qw[-1] = one.layer.qw[0]
+    wide = lambda t: torch.cat([torch.zeros((E - 1,) + tuple(t.shape[1:]), dtype=t.dtype, device="cuda"), t])
+    layer = S.GroupedDeviceLayer.from_tensors(E, m, n, rank, qw, wide(one.layer.wscale), wide(one.layer.l1), wide(one.layer.l2))
+    rows = 530000
+    x = torch.zeros((rows, m), dtype=torch.bfloat16, device="cuda")
+    assert x.numel() * 2 > 2 ** 32
+    tail = R.bf16(rng.standard_normal((3, m)))
+    x[-3:] = dev_bf16(tail)
+    src, off = i32([rows - 3, rows - 1, rows - 2]), i32([0] * E + [3])
+    y = S.svdq_grouped_linear(x, off, layer, src, out_dtype=torch.float32)
+    _, _, z = S.svdq_grouped_quantize_act_lowrank_down(x, off, layer, src)
+    torch.cuda.synchronize()
+    codes, s, _, _ = one.quantized(0, tail[[0, 2, 1]])
+    v, dv = R.product_int4(codes, s, one.cw[0], one.sw[0], to_np(z), one.l2[0])
+    want, tol = R.epilogue(v, dv)
+    assert (np.abs(to_np(y) - want) <= tol).all()
+    # the same rows through the tiles: enough of them that the row kernel is not chosen
+    many = i32(np.repeat([rows - 3, rows - 1, rows - 2], 200))
+    y = S.svdq_grouped_linear(x, i32([0] * E + [600]), layer, many, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert (np.abs(to_np(y) - np.repeat(want, 200, 0)) <= np.repeat(tol, 200, 0)).all()
