@@ -559,6 +559,7 @@ size_t svdq_gemm_epi_workspace_size(int b, int n, int m);
  * integer sums per group are the same exact ones; the groups' fp32 sum may be
  * taken in another order, so results differ from svdq_gemm_w4a4_lowrank_up's by
  * rounding.  The order depends only on the shape and the device's CU count.
+ * svdq_gemm_schedule describes the plain product only.
  * The 8-bit and NVFP4 forms below are the same for their settings, with the
  * workspaces of svdq_w8a8_gemm_lowrank_up and svdq_fp4_gemm_lowrank_up. */
 int svdq_gemm_w4a4_lowrank_up_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer* layer,
@@ -590,7 +591,7 @@ int svdq_fp4_linear_epi(const uint16_t* x, const svdq_fp4_layer* layer, const sv
  *            offsets[0] and from offsets[experts] on belong to no expert: no
  *            output of theirs is written.  Values are clamped to [0, b], so no
  *            offsets lead outside the b rows; where they decrease, which
- *            expert's result a row gets is undefined.
+ *            expert's result a row gets, if any, is undefined.
  * ========================================================================= */
 #define SVDQ_MAX_EXPERTS 1024
 
@@ -613,9 +614,9 @@ typedef struct svdq_grouped_layer {
  * them: row i of expert e is x[row_index[i]] with smooth_inv[e] and l1[e].
  *   x bf16 [x_rows][m]; row_index device int32 [b], or NULL (row i is x[i],
  *   x_rows >= b); an index outside [0, x_rows) stands for a row of zeros.
- *   Outputs as svdq_quantize_act_lowrank_down for b rows (codes and scales bit
- *   for bit its own; z up to the order of its fp32 sum); the entries of rows
- *   without an expert are left as they were.  No workspace.  layer->qw, wscale,
+ *   Outputs as svdq_quantize_act_lowrank_down for b rows (for finite x * smooth_inv
+ *   codes and scales bit for bit its own; z up to the order of its fp32 sum); the
+ *   entries of rows without an expert are left as they were.  No workspace.  layer->qw, wscale,
  *   l2 and bias are not used. */
 int svdq_grouped_quantize_act_lowrank_down(const uint16_t* x, int x_rows, const int32_t* row_index,
                                            const int32_t* offsets, const svdq_grouped_layer* layer, int b, uint8_t* qx,

@@ -16,6 +16,13 @@ namespace {
 
 using namespace dev;
 
+// INT4 is bound by the two FMAs per output and channel group that apply the
+// scales (4096 x 1152 -> 4608 with GELU: 55 us, of which the 18 groups are 33 and
+// y's write, Z L2 and GELU the rest); 8 bits by the steps over the groups when
+// tiles are few (1000 x 4608 -> 1152: 72 steps in 21 us); NVFP4 by the
+// dequantization, which every wave does for its own operands (2304 x 1152 -> 4608
+// with GELU: 42.5 us, 128 vector instructions a group beside 32 MFMAs; 44.9 us
+// with 32 LDS reads a group instead of 10).
 template <class C, bool OUT_BF16, int FMT, bool SK>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE))) void gemm_epi_kernel(
     const uint8_t* __restrict__ qx, const uint16_t* __restrict__ ascale, const float* __restrict__ z, Operands L, int b,
@@ -31,6 +38,9 @@ using Cfg8S = GemmCfg<64, 64, 32, 32, 4, 3>;
 using CfgG = GemmCfg<64, 128, 64, 32, 3, 2>;
 
 // One tile of one expert per workgroup; the workgroups past the last tile end.
+// Bound as the dense INT4 product, plus the empty rows of each expert's last row
+// block: 8192 rows of 8 experts, 1152 -> 4608: 98 us; 18006 rows of 64 experts,
+// 2048 -> 1408: 117 us, 27 % more tile rows than rows.
 template <class C, bool OUT_BF16>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE))) void gemm_grouped_kernel(
     const uint8_t* __restrict__ qx, const uint16_t* __restrict__ ascale, const float* __restrict__ z, Operands L, int b,

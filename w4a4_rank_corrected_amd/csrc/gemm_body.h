@@ -493,10 +493,19 @@ __device__ __forceinline__ void gemm_up_body(
     // its row (swizzled as above), and its two E4M3 block scales (blocks
     // w0/2 and w0/2 + 1: bytes 0 and 1 of sc) go to the row's scale slots as
     // fp16, with one 32-bit store
+    auto slot = [](int row) { return MODE == kTilePlain ? row * 4 : (row & ~63) * 4 + 4 * (row & 15); };
     auto stage_fp4 = [&](uint8_t* row, int ridx, int w0, const Piece<16>& pc, uint32_t sc, uint16_t* srow) {
       *reinterpret_cast<u32x4*>(row + 4 * (w0 ^ (4 * ((ridx >> 3) & 1)))) = u32x4{pc.w[0], pc.w[1], pc.w[2], pc.w[3]};
-      reinterpret_cast<uint32_t*>(srow)[w0 >> 2] =
-          e4m3_to_f16_bits(sc & 0xFFu) | (e4m3_to_f16_bits((sc >> 8) & 0xFFu) << 16);
+      const uint32_t s0 = e4m3_to_f16_bits(sc & 0xFFu), s1 = e4m3_to_f16_bits((sc >> 8) & 0xFFu);
+      if constexpr (MODE == kTilePlain) {
+        reinterpret_cast<uint32_t*>(srow)[w0 >> 2] = s0 | (s1 << 16);
+      } else {
+        // 64 rows at a time, [block][row % 16][row / 16]: a lane's four row blocks
+        // are neighbours
+        uint16_t* p = srow + 64 * (w0 >> 1) + ((ridx >> 4) & 3);
+        p[0] = (uint16_t)s0;
+        p[64] = (uint16_t)s1;
+      }
     };
     auto store_stage = [&](int buf, const Stage& st) {
 #pragma unroll
@@ -505,8 +514,8 @@ __device__ __forceinline__ void gemm_up_body(
         uint8_t* bs = &Bs[buf][(q * TN + b_col) * ROWB];
         if constexpr (F4) {
           uint16_t* fs = &F4s[buf][q * (TM + TN) * 4];
-          stage_fp4(as, a_row, a_w0, st.a[q], st.s[q], fs + a_row * 4);
-          stage_fp4(bs, b_col, b_w0, st.w[q], st.s2[q], fs + (TM + b_col) * 4);
+          stage_fp4(as, a_row, a_w0, st.a[q], st.s[q], fs + slot(a_row));
+          stage_fp4(bs, b_col, b_w0, st.w[q], st.s2[q], fs + slot(TM + b_col));
         } else if constexpr (W8) {
           copy_piece(as, chunk_swz(a_row), a_w0, st.a[q]);
           copy_piece(bs, chunk_swz(b_col), b_w0, st.w[q]);
@@ -539,22 +548,51 @@ __device__ __forceinline__ void gemm_up_body(
         const uint32_t* aw = reinterpret_cast<const uint32_t*>(as);
         const uint32_t* bw = reinterpret_cast<const uint32_t*>(bs);
         const _Float16* fs = reinterpret_cast<const _Float16*>(&F4s[buf][q * (TM + TN) * 4]);
+        if constexpr (MODE == kTilePlain) {
 #pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {  // channels 0-31, then 32-63 of the group
-          const int wo = kh ? f4w1 : f4w0, blk = 2 * kh + (c >> 1);
-          f16x8 Pb[BJ];
+          for (int kh = 0; kh < 2; ++kh) {  // channels 0-31, then 32-63 of the group
+            const int wo = kh ? f4w1 : f4w0, blk = 2 * kh + (c >> 1);
+            f16x8 Pb[BJ];
 #pragma unroll
-          for (int bj = 0; bj < BJ; ++bj) {
-            const int row = WN * wn + 16 * bj + r;
-            Pb[bj] = fp4_operand(bw[row * 8 + wo], fs[(TM + row) * 4 + blk]);
+            for (int bj = 0; bj < BJ; ++bj) {
+              const int row = WN * wn + 16 * bj + r;
+              Pb[bj] = fp4_operand(bw[row * 8 + wo], fs[(TM + row) * 4 + blk]);
+            }
+#pragma unroll
+            for (int bi = 0; bi < BI; ++bi) {
+              const int row = WM * wm + 16 * bi + r;
+              const f16x8 Qa = fp4_operand(aw[row * 8 + wo], fs[row * 4 + blk]);
+#pragma unroll
+              for (int bj = 0; bj < BJ; ++bj)
+                acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Pb[bj], Qa, acc[bi][bj], 0, 0, 0);
+            }
           }
+        } else {
+          // the lane takes words 2c and 2c + 1 of a row, which are its block c (the
+          // sum over a group is the same in another order): one 8-byte read of
+          // codes a row and one of block scales for all its rows (columns)
+          static_assert(BI == 4 && BJ == 4, "scale slots: four row blocks a wave");
+          const int wo = (2 * c) ^ (4 * ((r >> 3) & 1));
+          typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+          const f16x4 sa = *reinterpret_cast<const f16x4*>(fs + (WM * wm) * 4 + 4 * lane);
+          const f16x4 sb = *reinterpret_cast<const f16x4*>(fs + (TM + WN * wn) * 4 + 4 * lane);
+          uint2 wa[BI], wb[BJ];
 #pragma unroll
-          for (int bi = 0; bi < BI; ++bi) {
-            const int row = WM * wm + 16 * bi + r;
-            const f16x8 Qa = fp4_operand(aw[row * 8 + wo], fs[row * 4 + blk]);
+          for (int bj = 0; bj < BJ; ++bj) wb[bj] = *reinterpret_cast<const uint2*>(bw + (WN * wn + 16 * bj + r) * 8 + wo);
 #pragma unroll
-            for (int bj = 0; bj < BJ; ++bj)
-              acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Pb[bj], Qa, acc[bi][bj], 0, 0, 0);
+          for (int bi = 0; bi < BI; ++bi) wa[bi] = *reinterpret_cast<const uint2*>(aw + (WM * wm + 16 * bi + r) * 8 + wo);
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            f16x8 Pb[BJ];
+#pragma unroll
+            for (int bj = 0; bj < BJ; ++bj) Pb[bj] = fp4_operand(kh ? wb[bj].y : wb[bj].x, sb[bj]);
+#pragma unroll
+            for (int bi = 0; bi < BI; ++bi) {
+              const f16x8 Qa = fp4_operand(kh ? wa[bi].y : wa[bi].x, sa[bi]);
+#pragma unroll
+              for (int bj = 0; bj < BJ; ++bj)
+                acc[bi][bj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Pb[bj], Qa, acc[bi][bj], 0, 0, 0);
+            }
           }
         }
       } else if constexpr (W8) {
