@@ -365,3 +365,26 @@ def test_outputs_past_32_bit_offsets(S):
     torch.cuda.synchronize()
     both = got[0] + got[-1]
     assert (np.abs(to_np(out)[0] - both) <= np.abs(both) * 2.0 ** -8 + 1e-30).all()
+
+
+@pytest.mark.parametrize("block", range(4))
+def test_every_block_scale(S, block):
+    """NVFP4: each finite E4M3 scale against each other, one block of the group at a time."""
+    rng = np.random.default_rng(block)
+    k = np.arange(127)
+    e4m3 = np.where(k < 8, k / 8 * 2.0 ** -6, (1 + (k & 7) / 8) * 2.0 ** ((k >> 3) - 7.0))
+    px, pw = np.zeros((127, 64), np.int64), rng.integers(0, 16, (127, 64))
+    s = slice(16 * block, 16 * block + 16)
+    px[:, s] = rng.integers(0, 16, (127, 16))
+    ex, ew = rng.integers(0, 127, (127, 4)), rng.integers(0, 127, (127, 4))
+    ex[:, block], ew[:, block] = k, rng.permutation(127)
+    value = lambda p: E2M1[p & 7] * np.where(p & 8, -1, 1)
+    x, w = value(px[:, s]) * e4m3[ex[:, block], None], value(pw[:, s]) * e4m3[ew[:, block], None]
+    v, dv = R.product_values(x, w, 64)
+    u8 = lambda t: torch.from_numpy(t).cuda()
+    layer = S.DeviceLayerFp4.from_tensors(64, 127, 0, 1.0, 1.0, u8(LY.pack_fp4_codes(pw)), u8(LY.pack_fp4_scales(ew)))
+    y = S.svdq_fp4_gemm_lowrank_up_epi(u8(LY.pack_fp4_codes(px)), u8(LY.pack_fp4_scales(ex)), None, layer,
+                                       out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want, tol = R.epilogue(v, dv)
+    assert (np.abs(to_np(y) - want) <= tol).all()

@@ -21,8 +21,9 @@ using namespace dev;
 // y's write, Z L2 and GELU the rest); 8 bits by the steps over the groups when
 // tiles are few (1000 x 4608 -> 1152: 72 steps in 21 us); NVFP4 by the
 // dequantization, which every wave does for its own operands (2304 x 1152 -> 4608
-// with GELU: 42.5 us, 128 vector instructions a group beside 32 MFMAs; 44.9 us
-// with 32 LDS reads a group instead of 10).
+// with GELU: 40.1 us, 128 vector instructions a group beside 32 MFMAs; 42.5 us
+// with the block scales widened bit by bit, 44.9 us with 32 LDS reads a group
+// instead of 10 as well).
 template <class C, bool OUT_BF16, int FMT, bool SK>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE))) void gemm_epi_kernel(
     const uint8_t* __restrict__ qx, const uint16_t* __restrict__ ascale, const float* __restrict__ z, Operands L, int b,

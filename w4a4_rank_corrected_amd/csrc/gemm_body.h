@@ -496,15 +496,16 @@ __device__ __forceinline__ void gemm_up_body(
     auto slot = [](int row) { return MODE == kTilePlain ? row * 4 : (row & ~63) * 4 + 4 * (row & 15); };
     auto stage_fp4 = [&](uint8_t* row, int ridx, int w0, const Piece<16>& pc, uint32_t sc, uint16_t* srow) {
       *reinterpret_cast<u32x4*>(row + 4 * (w0 ^ (4 * ((ridx >> 3) & 1)))) = u32x4{pc.w[0], pc.w[1], pc.w[2], pc.w[3]};
-      const uint32_t s0 = e4m3_to_f16_bits(sc & 0xFFu), s1 = e4m3_to_f16_bits((sc >> 8) & 0xFFu);
       if constexpr (MODE == kTilePlain) {
-        reinterpret_cast<uint32_t*>(srow)[w0 >> 2] = s0 | (s1 << 16);
+        reinterpret_cast<uint32_t*>(srow)[w0 >> 2] =
+            e4m3_to_f16_bits(sc & 0xFFu) | (e4m3_to_f16_bits((sc >> 8) & 0xFFu) << 16);
       } else {
         // 64 rows at a time, [block][row % 16][row / 16]: a lane's four row blocks
         // are neighbours
-        uint16_t* p = srow + 64 * (w0 >> 1) + ((ridx >> 4) & 3);
-        p[0] = (uint16_t)s0;
-        p[64] = (uint16_t)s1;
+        const f16x2 s2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sc, 1.0f, false);
+        _Float16* p = reinterpret_cast<_Float16*>(srow) + 64 * (w0 >> 1) + ((ridx >> 4) & 3);
+        p[0] = s2[0];
+        p[64] = s2[1];
       }
     };
     auto store_stage = [&](int buf, const Stage& st) {
