@@ -560,8 +560,10 @@ size_t svdq_gemm_epi_workspace_size(int b, int n, int m);
  * taken in another order, so results differ from svdq_gemm_w4a4_lowrank_up's by
  * rounding.  The order depends only on the shape and the device's CU count.
  * svdq_gemm_schedule describes the plain product only.
- * The 8-bit and NVFP4 forms below are the same for their settings, with the
- * workspaces of svdq_w8a8_gemm_lowrank_up and svdq_fp4_gemm_lowrank_up. */
+ * The 8-bit and NVFP4 forms below are the same for their settings, with
+ * workspaces of the sizes of svdq_w8a8_gemm_lowrank_up's and
+ * svdq_fp4_gemm_lowrank_up's; all three write theirs when they split tiles, so
+ * calls that overlap in time need one each. */
 int svdq_gemm_w4a4_lowrank_up_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer* layer,
                                   const svdq_epilogue* epi, int b, void* y, int y_dtype, void* workspace,
                                   size_t workspace_bytes, void* stream);

@@ -388,3 +388,12 @@ def test_every_block_scale(S, block):
     torch.cuda.synchronize()
     want, tol = R.epilogue(v, dv)
     assert (np.abs(to_np(y) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("rank", [0, 33])
+@pytest.mark.parametrize("b,m,n", [(1, 1024, 64), (130, 2112, 301), (256, 1088, 1000), (100, 8192, 130)])
+def test_fp4_pieces(S, b, m, n, rank):
+    """Few tiles, which are split over the channel groups: every part of the epilogue after the sum of the pieces."""
+    case = Case(S, "fp4", b, m, n, rank)
+    case.run(out="f32")
+    case.run(act="gelu_erf", act_begin=n // 3, gate_rows=7, residual=True, inplace=True, out="bf16")

@@ -35,6 +35,9 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C
 // 8-bit codes, few tiles: 64 x 64 tiles, 4 waves of 32 x 32, loads three groups
 // ahead (90 registers).
 using Cfg8S = GemmCfg<64, 64, 32, 32, 4, 3>;
+// NVFP4, split tiles: at most two workgroups a CU are launched, so two share its
+// registers and loads run two groups ahead.
+using CfgF4K = GemmCfg<128, 128, 64, 64, 2, 2>;
 // Experts with few rows: 64 x 128 tiles, 4 waves of 64 x 32.
 using CfgG = GemmCfg<64, 128, 64, 32, 3, 2>;
 
@@ -74,16 +77,18 @@ int launch_tiles(const uint8_t* qx, const uint16_t* ascale, const float* z, cons
                             txw, ep);
     };
     if (!plan.split) return gemm(gemm_epi_kernel<C, OUT_BF16, FMT, false>);
-    if constexpr (FMT == kFmtFp4 || std::is_same_v<C, Cfg8S>) {
+    if constexpr (std::is_same_v<C, Cfg8S>) {
       return (int)hipErrorInvalidValue;  // never split
     } else {
-      const int status = gemm(gemm_epi_kernel<C, OUT_BF16, FMT, true>);
+      using CS = std::conditional_t<FMT == kFmtFp4, CfgF4K, C>;
+      const int status = gemm(gemm_epi_kernel<CS, OUT_BF16, FMT, true>);
       if (status != 0) return status;
       constexpr int UNITS = C::TM * C::TN / 4;
-      return launch_checked(splitk_reduce_kernel<C, FMT, OUT_BF16, true>,
+      // NVFP4 pieces are scaled sums: they add up like INT4's
+      return launch_checked(splitk_reduce_kernel<C, FMT == kFmtFp4 ? kFmtInt4 : FMT, OUT_BF16, true>,
                             (int)(((long long)sk.T * UNITS + 255) / 256), 256, st, (const float*)sk.partials, sk.T, sk.k,
                             plan.tiles_m, plan.tiles_n, b, L.n, ascale, L.wscale,
-                            FMT == kFmtInt8 && L.rank > 0 ? 1 : 0, L.bias, (void*)nullptr, ep);
+                            FMT != kFmtInt4 && L.rank > 0 ? 1 : 0, L.bias, (void*)nullptr, ep);
     }
   };
   if constexpr (FMT == kFmtInt8) return plan.tile_n == Cfg8S::TN ? run(Cfg8S{}) : run(Cfg8{});
@@ -102,8 +107,8 @@ void whole_tiles(GemmPlan& p, int b, int n) {
   p.pieces = 1;
 }
 
-// The plan of the plain product, except for less than one round of tiles (768):
-// INT4, T = wide (128 x 128) tiles:
+// The plan of the plain product, except for few tiles.
+// INT4, less than one round of tiles (768), T = wide (128 x 128) tiles:
 //   * above half a round whole wide tiles, not narrow ones (rank 16, residual, us:
 //     1500 x 1152 -> 4608, T = 432, 32.0 narrow / 29.6 wide; 2500 rows, T = 720,
 //     42.3 / 37.0; 3000 x 2048 -> 2048, T = 384, 34.7 / 42.4);
@@ -121,6 +126,14 @@ void whole_tiles(GemmPlan& p, int b, int n) {
 //   * a launch that is split whole gets as many pieces as give every CU one
 //     workgroup, not three (1000 x 4608 -> 1152, 72 tiles: 3 pieces 21.4 us, 2:
 //     24.0, 4: 23.4, 10: 27.3).
+// NVFP4, which the plain product never splits: into as many pieces as two
+// workgroups a CU take, where the 0.62 us a group that they save pay for the
+// launch and for 0.03 us a piece (whole / split, us: 256 x 4608 -> 1152 51.6 /
+// 16.4; 500 x 2048 -> 2048 27.1 / 18.7; 128 x 8192 -> 8192 89 / 33; 65 x 12288 ->
+// 3000 128 / 25; 100 x 1152 -> 4608 17.9 / 16.0; not 256 x 1152 -> 4608, 18.2 /
+// 18.8).  Fewer pieces, where they cost least by that count, were up to 10 %
+// slower.  The pieces stay within the workspace: k T <= two a CU, k within the
+// limits it is sized for.
 GemmPlan epi_plan(int b, int n, int m, int fmt) {
   GemmPlan p = gemm_plan(b, n, m, device_cus(), fmt);
   const long long T = (long long)p.tiles_m * p.tiles_n, slots = (long long)p.wg_per_cu * device_cus();
@@ -130,6 +143,16 @@ GemmPlan epi_plan(int b, int n, int m, int fmt) {
       whole_tiles<Cfg>(p, b, n);
     else if (p.split && 0.5 * p.G * (1.0 - 1.0 / p.pieces) <= 1.5 + 0.013 * (double)p.split_grid)
       whole_tiles<CfgN>(p, b, n);
+  }
+  if (fmt == kFmtFp4) {
+    const long long two = CfgF4K::WG_PER_CU * (long long)device_cus();
+    const long long k = std::min<long long>({kMaxPiecesAll, p.G / kMinPieceGroups, two / T});
+    if (k >= 2 && 0.62 * p.G * (1.0 - 1.0 / (double)k) > 1.5 + 0.03 * (double)(T * k)) {
+      p.pieces = (int)k;
+      p.split = 1;
+      p.split_tiles = (int)T;
+      p.split_grid = p.grid = (int)(T * k);
+    }
   }
   if (fmt == kFmtInt8) {
     const long long small = (long long)((b + Cfg8S::TM - 1) / Cfg8S::TM) * ((n + Cfg8S::TN - 1) / Cfg8S::TN);

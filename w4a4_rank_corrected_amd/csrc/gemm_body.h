@@ -882,8 +882,9 @@ __device__ __forceinline__ void gemm_up_body(
   // before their loads, so no workgroup waits for or signals another, and the
   // result does not depend on dispatch order (deterministic for a shape and
   // CU count).  The piece with the tile's last groups carries the low-rank
-  // product in its sums (INT4), or, in the 8-bit setting (integer sums),
-  // stores it alone in slot k of the tile (NVFP4 tiles are never split).
+  // product in its sums (INT4), or, in the 8-bit setting (integer sums) and with
+  // NVFP4 (sums before their tensor scales; split with an epilogue only), stores
+  // it alone in slot k of the tile.
   const int T = MODE == kTileGrouped ? 0 : tiles_m * tiles_n;
   const bool split = SK && (int)blockIdx.x < sk.P;
   int t, g0 = 0, g1 = G;
@@ -943,6 +944,8 @@ __device__ __forceinline__ void gemm_up_body(
       const int piece = (int)blockIdx.x - t * sk.k;
       if constexpr (W8)
         store_slot(piece * sk.T + t, [&](int bi, int bj) { return __builtin_bit_cast(u32x4, iacc[bi][bj]); });
+      else if constexpr (F4)  // scaled here, so that the reduction only adds
+        store_slot(piece * sk.T + t, [&](int bi, int bj) { return __builtin_bit_cast(u32x4, acc[bi][bj] * txw); });
       else
         store_slot(piece * sk.T + t, [&](int bi, int bj) { return __builtin_bit_cast(u32x4, acc[bi][bj]); });
       if constexpr (!POST) {
@@ -992,8 +995,8 @@ __device__ __forceinline__ void gemm_up_body(
 // store), adds the k pieces' units in piece order (i32 in the 8-bit setting,
 // exact), applies the epilogue the whole tiles apply (8-bit: the per-row and
 // per-column scales, then the tile's low-rank slot), adds the bias and stores
-// Y.  All k loads are issued before the first add.  (NVFP4 tiles are never
-// split.)
+// Y.  All k loads are issued before the first add.  NVFP4 pieces come already
+// scaled and are reduced as INT4's, plus the low-rank slot.
 // (EPI: with the epilogue of epilogue.h.)
 template <class C, int FMT, bool OUT_BF16, bool EPI = false>
 __global__ __launch_bounds__(256) void splitk_reduce_kernel(
@@ -1002,7 +1005,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(
     const uint16_t* __restrict__ bias, void* __restrict__ yout, EpiArgs ep = EpiArgs{}) {
   static_assert(C::NT == 256 && kMaxPiecesAll <= 16, "unit layout of the slots");
   constexpr int WU = C::BI * C::BJ * 64;    // units per wave
-  static_assert(FMT == kFmtInt4 || FMT == kFmtInt8, "INT4 and 8-bit tiles only");
+  static_assert(FMT == kFmtInt4 || FMT == kFmtInt8, "fp32 or integer sums");
   constexpr int UNITS = C::TM * C::TN / 4;  // 16-byte units per slot
   const int u = (int)blockIdx.x * 256 + (int)threadIdx.x;
   const int t = u / UNITS, w = u - t * UNITS;
