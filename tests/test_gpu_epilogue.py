@@ -397,3 +397,11 @@ def test_fp4_pieces(S, b, m, n, rank):
     case = Case(S, "fp4", b, m, n, rank)
     case.run(out="f32")
     case.run(act="gelu_erf", act_begin=n // 3, gate_rows=7, residual=True, inplace=True, out="bf16")
+
+
+@pytest.mark.parametrize("rank", [0, 5, 40])
+@pytest.mark.parametrize("b,m,n", [(1, 64, 1), (1, 4608, 70), (15, 192, 33), (17, 1152, 130), (33, 448, 999), (64, 2048, 50)])
+def test_fp4_few_rows(S, b, m, n, rank):
+    case = Case(S, "fp4", b, m, n, rank, bias=rank != 5)
+    case.run(out="f32")
+    case.run(act="silu", act_begin=n // 2, gate_rows=4, residual=True, inplace=True, out="bf16")

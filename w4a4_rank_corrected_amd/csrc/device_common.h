@@ -51,5 +51,21 @@ __device__ __forceinline__ float max4_rows(float v) {
   return fmaxf(__uint_as_float(pr[0]), __uint_as_float(pr[1]));
 }
 
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Eight FP4 codes (one 32-bit word, the even channel in each byte's low
+// nibble) -> the f16 operand code * s, in channel order.  The conversion at
+// unit scale is exact, and so is the product: an E2M1 value times an E4M3
+// scale has at most 6 significant bits and lies in 2^-10 .. 2688.
+__device__ __forceinline__ f16x8 fp4_operand(uint32_t w, _Float16 s) {
+  const f16x2 ss = {s, s};
+  const f16x2 h0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * ss;
+  const f16x2 h1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * ss;
+  const f16x2 h2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * ss;
+  const f16x2 h3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * ss;
+  return f16x8{h0[0], h0[1], h1[0], h1[1], h2[0], h2[1], h3[0], h3[1]};
+}
+
 }  // namespace dev
 }  // namespace svdq

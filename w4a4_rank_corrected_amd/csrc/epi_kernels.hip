@@ -131,7 +131,7 @@ void whole_tiles(GemmPlan& p, int b, int n) {
 // launch and for 0.03 us a piece (whole / split, us: 256 x 4608 -> 1152 51.6 /
 // 16.4; 500 x 2048 -> 2048 27.1 / 18.7; 128 x 8192 -> 8192 89 / 33; 65 x 12288 ->
 // 3000 128 / 25; 100 x 1152 -> 4608 17.9 / 16.0; not 256 x 1152 -> 4608, 18.2 /
-// 18.8).  Fewer pieces, where they cost least by that count, were up to 10 %
+// 18.8; up to 64 rows are the row kernel's).  Fewer pieces, where they cost least by that count, were up to 10 %
 // slower.  The pieces stay within the workspace: k T <= two a CU, k within the
 // limits it is sized for.
 GemmPlan epi_plan(int b, int n, int m, int fmt) {
@@ -192,8 +192,8 @@ int launch_grouped_tiles(const uint8_t* qx, const uint16_t* ascale, const float*
 int launch_gemm_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer& L, int b, int y_dtype,
                     const EpiArgs& ep, void* ws, void* stream) {
   if (b <= kRowsMax) {
-    const RowsArgs a{qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, L.m / SVDQ_GROUP, L.rank, Groups{nullptr, 0}, ep};
-    return launch_gemm_rows(a, b <= 16 ? 1 : (b <= 32 ? 2 : 4), y_dtype, stream);
+    const RowsArgs a{qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, L.m / SVDQ_GROUP, L.rank, Groups{nullptr, 0}, ep, 1.0f};
+    return launch_gemm_rows(a, b <= 16 ? 1 : (b <= 32 ? 2 : 4), y_dtype, kFmtInt4, stream);
   }
   const Operands o{L.qw, L.wscale, L.l2, L.bias, L.n, L.rank};
   return launch_tiles_typed<kFmtInt4>(qx, ascale, z, o, L.m, b, y_dtype, ep, ws, stream, 1.0f);
@@ -209,6 +209,11 @@ int launch_gemm8_epi(const int8_t* qx, const uint16_t* ascale, const float* z, c
 int launch_gemm_fp4_epi(const uint8_t* qx, const uint8_t* ascale, const float* z, const svdq_fp4_layer& L, int b,
                         int y_dtype, const EpiArgs& ep, void* ws, void* stream) {
   const Operands o{L.qw, reinterpret_cast<const uint16_t*>(L.wscale), L.l2, L.bias, L.n, L.rank};
+  if (b <= kRowsMax) {
+    const RowsArgs a{qx, reinterpret_cast<const uint16_t*>(ascale), z, L.qw, o.wscale, L.l2, L.bias, b, L.n,
+                     L.m / SVDQ_GROUP, L.rank, Groups{nullptr, 0}, ep, L.t_x * L.t_w};
+    return launch_gemm_rows(a, b <= 16 ? 1 : (b <= 32 ? 2 : 4), y_dtype, kFmtFp4, stream);
+  }
   return launch_tiles_typed<kFmtFp4>(qx, reinterpret_cast<const uint16_t*>(ascale), z, o, L.m, b, y_dtype, ep, ws,
                                      stream, L.t_x * L.t_w);
 }
@@ -229,8 +234,8 @@ int launch_grouped_gemm(const uint8_t* qx, const uint16_t* ascale, const float* 
   const long long steps = grouped_row_blocks(b, L.experts, 16 * rb) * ((L.n + 15) / 16) * G;
   const long long tiles = grouped_row_blocks(b, L.experts, 64) * ((L.n + 127) / 128);
   if (mean <= 8 || (tiles <= 384 && steps <= 160000)) {
-    const RowsArgs a{qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, G, L.rank, groups, ep};
-    return launch_gemm_rows(a, rb, y_dtype, stream);
+    const RowsArgs a{qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, G, L.rank, groups, ep, 1.0f};
+    return launch_gemm_rows(a, rb, y_dtype, kFmtInt4, stream);
   }
   // 128 x 128 tiles do the most work per staged record, 64 x 128 tiles leave less
   // of an expert's last row block empty and fill the chip with fewer rows: mean

@@ -190,7 +190,7 @@ constexpr long long grouped_row_blocks(long long b, long long experts, long long
   const long long full = (b + experts * (rows - 1)) / rows;
   return full < b ? full : b;
 }
-// Rows up to which the INT4 product with an epilogue uses the row kernel.
+// Rows up to which the INT4 and NVFP4 products with an epilogue use the row kernel.
 constexpr int kRowsMax = 64;
 int launch_gemm_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer& L, int b,
                     int y_dtype, const EpiArgs& ep, void* ws, void* stream);
@@ -213,8 +213,9 @@ struct RowsArgs {
   int b, n, G, rank;
   Groups groups;
   EpiArgs ep;
+  float txw;  // NVFP4: the product of the tensor scales
 };
-int launch_gemm_rows(const RowsArgs& a, int rb, int y_dtype, void* stream);
+int launch_gemm_rows(const RowsArgs& a, int rb, int y_dtype, int fmt, void* stream);
 int launch_grouped_act(const uint16_t* x, int x_rows, const int32_t* row_index, const int32_t* offsets,
                        const svdq_grouped_layer& L, int b, uint8_t* qx, uint16_t* ascale, float* z, void* stream);
 int launch_combine(const void* rows, int R, int n, int dtype, const int32_t* index, const float* weight, int t, int k,
