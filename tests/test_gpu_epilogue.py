@@ -405,3 +405,35 @@ def test_fp4_few_rows(S, b, m, n, rank):
     case = Case(S, "fp4", b, m, n, rank, bias=rank != 5)
     case.run(out="f32")
     case.run(act="silu", act_begin=n // 2, gate_rows=4, residual=True, inplace=True, out="bf16")
+
+
+@pytest.mark.parametrize("b", [7, 130])
+def test_fp4_in_two_graphs_and_on_two_streams(S, b):
+    """Captured calls (row kernel, split tiles) of two layers, replayed together on two streams, each with its workspace."""
+    n, m = 203, 2368
+    runs = []
+    for seed in range(2):
+        c = Case(S, "fp4", b, m, n, 24, seed=seed)
+        y = torch.empty((b, n), device="cuda")
+        ws = torch.empty(max(1, S.svdq_fp4_gemm_workspace_size(b, n, m)), dtype=torch.uint8, device="cuda")
+        call = lambda c=c, y=y, ws=ws: c.call(c.qx, c.ascale, c.z, c.layer, act="gelu_tanh", out_dtype=torch.float32, y=y,
+                                              workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        runs.append((c, y, g, torch.cuda.Stream()))
+    for k in range(3):
+        for c, y, g, stream in runs:
+            y.zero_()
+            c.z.copy_(torch.randn_like(c.z))
+        torch.cuda.synchronize()
+        for c, y, g, stream in runs:
+            with torch.cuda.stream(stream):
+                g.replay()
+        torch.cuda.synchronize()
+        for c, y, g, stream in runs:
+            want = c.call(c.qx, c.ascale, c.z, c.layer, act="gelu_tanh", out_dtype=torch.float32)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want), (k, b)
