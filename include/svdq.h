@@ -529,7 +529,8 @@ int svdq_fp4_linear(const uint16_t* x, const svdq_fp4_layer* layer, int b, void*
  * act (SVDQ_ACT_*):
  *   NONE       v
  *   GELU_TANH  0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))
- *   GELU_ERF   v Phi(v) (absolute error at most 1e-7 |v| before rounding)
+ *   GELU_ERF   v Phi(v) (Phi to an absolute error of at most 1e-7; the product
+ *              with v rounds once more)
  *   SILU       v / (1 + exp(-v))
  *   RELU       max(v, 0)
  * NaN stays NaN in all of them; GELU and SiLU of -inf are NaN.
