@@ -954,8 +954,11 @@ def _epilogue(b: int, n: int, device, y, out_dtype, act, act_begin, gate=None, g
     if gate is not None:
         if gate_rows is not None and gate_rows < 0:
             raise ValueError(f"gate_rows must be >= 0, got {gate_rows}")
+        rows = -(-b // min(gate_rows or b, b)) if b else 0
+        if b == 0 and not gate_rows and tuple(gate.shape) == (1, n):
+            rows = 1  # the one row that all rows share, of which there are none
         gate_rows = min(gate_rows or b, b)
-        _dev(gate, "gate", torch.bfloat16, (-(-b // gate_rows) if b else 0, n), device)
+        _dev(gate, "gate", torch.bfloat16, (rows, n), device)
     epi = svdq_epilogue(code, act_begin, gate_rows or 0, ldr, ldy, None if gate is None else gate.data_ptr(),
                         None if residual is None else residual.data_ptr())
     return y, out, epi
