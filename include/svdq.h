@@ -552,8 +552,8 @@ typedef struct svdq_epilogue {
   const void* residual;
 } svdq_epilogue;
 
-/* Bytes of device workspace svdq_gemm_w4a4_lowrank_up_epi needs (0 for few
- * rows). */
+/* Bytes of device workspace svdq_gemm_w4a4_lowrank_up_epi and
+ * svdq_fp4_gemm_lowrank_up_epi need (0 for up to 64 rows). */
 size_t svdq_gemm_epi_workspace_size(int b, int n, int m);
 
 /* DEVICE: svdq_gemm_w4a4_lowrank_up with an epilogue (epi NULL: none).  The
@@ -561,10 +561,9 @@ size_t svdq_gemm_epi_workspace_size(int b, int n, int m);
  * taken in another order, so results differ from svdq_gemm_w4a4_lowrank_up's by
  * rounding.  The order depends only on the shape and the device's CU count.
  * svdq_gemm_schedule describes the plain product only.
- * The 8-bit and NVFP4 forms below are the same for their settings, with
- * workspaces of the sizes of svdq_w8a8_gemm_lowrank_up's and
- * svdq_fp4_gemm_lowrank_up's; all three write theirs when they split tiles, so
- * calls that overlap in time need one each. */
+ * The 8-bit and NVFP4 forms below are the same for their settings; the 8-bit
+ * one's workspace is of svdq_w8a8_gemm_workspace_size bytes.  All three write
+ * theirs when they split tiles, so calls that overlap in time need one each. */
 int svdq_gemm_w4a4_lowrank_up_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer* layer,
                                   const svdq_epilogue* epi, int b, void* y, int y_dtype, void* workspace,
                                   size_t workspace_bytes, void* stream);
@@ -577,7 +576,11 @@ int svdq_fp4_gemm_lowrank_up_epi(const uint8_t* qx, const uint8_t* ascale, const
 
 /* DEVICE: the whole layer with an epilogue: the activation kernels of
  * svdq_linear (svdq_w8a8_linear, svdq_fp4_linear), then the product above.
- * Workspace as svdq_linear (svdq_w8a8_linear, svdq_fp4_linear). */
+ * Workspace: 256-byte aligned, >= svdq_linear_epi_workspace_size (8 bits:
+ * svdq_w8a8_linear_workspace_size; NVFP4: svdq_fp4_linear_epi_workspace_size)
+ * bytes; up to 64 rows take less than svdq_linear's and svdq_fp4_linear's. */
+size_t svdq_linear_epi_workspace_size(int b, int m, int n, int rank);
+size_t svdq_fp4_linear_epi_workspace_size(int b, int m, int n, int rank);
 int svdq_linear_epi(const uint16_t* x, const svdq_layer* layer, const svdq_epilogue* epi, int b, void* y, int y_dtype,
                     void* workspace, size_t workspace_bytes, void* stream);
 int svdq_w8a8_linear_epi(const uint16_t* x, const svdq_w8a8_layer* layer, const svdq_epilogue* epi, int b, void* y,

@@ -1,0 +1,24 @@
+"""The workspaces that the products and layers with an epilogue ask for
+(tests/native/epi_workspace.cpp, host code with stubs for the launchers)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "w4a4_rank_corrected_amd", "csrc")
+NATIVE = os.path.join(ROOT, "tests", "native")
+
+
+def test_workspaces_are_what_the_size_functions_say(tmp_path):
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    exe = str(tmp_path / "epi_workspace")
+    sources = [os.path.join(CSRC, f) for f in ("api.cpp", "epi_api.cpp", "prep.cpp", "bundle.cpp", "plan.cpp")] + \
+              [os.path.join(NATIVE, f) for f in ("device_stubs.cpp", "epi_stubs.cpp", "epi_workspace.cpp")]
+    res = subprocess.run(["g++", "-std=c++17", "-O1", "-ffp-contract=off", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}",
+                          *sources, "-o", exe, "-pthread"], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-4000:]
+    run = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0 and "epi workspace ok" in run.stdout, (run.stdout + run.stderr)[-4000:]

@@ -18,8 +18,8 @@ from ._binding import (  # noqa: F401
     svdq_fp4_linear, svdq_fp4_linear_workspace_size, svdq_fp4_prepare_weights,
     svdq_fp4_quantize_act_lowrank_down,
     SVDQ_MAX_EXPERTS, ACTIVATIONS, svdq_gemm_epi_workspace_size, svdq_gemm_w4a4_lowrank_up_epi,
-    svdq_w8a8_gemm_lowrank_up_epi, svdq_fp4_gemm_lowrank_up_epi, svdq_linear_epi, svdq_w8a8_linear_epi,
-    svdq_fp4_linear_epi, GroupedDeviceLayer, svdq_grouped_quantize_act_lowrank_down,
+    svdq_w8a8_gemm_lowrank_up_epi, svdq_fp4_gemm_lowrank_up_epi, svdq_linear_epi_workspace_size, svdq_linear_epi,
+    svdq_w8a8_linear_epi, svdq_fp4_linear_epi_workspace_size, svdq_fp4_linear_epi, GroupedDeviceLayer, svdq_grouped_quantize_act_lowrank_down,
     svdq_grouped_gemm_w4a4_lowrank_up, svdq_grouped_linear_workspace_size, svdq_grouped_linear,
     svdq_combine_rows)
 
@@ -38,8 +38,8 @@ __all__ = [
     "svdq_fp4_linear", "svdq_fp4_linear_workspace_size", "svdq_fp4_prepare_weights",
     "svdq_fp4_quantize_act_lowrank_down",
     "SVDQ_MAX_EXPERTS", "ACTIVATIONS", "svdq_gemm_epi_workspace_size", "svdq_gemm_w4a4_lowrank_up_epi",
-    "svdq_w8a8_gemm_lowrank_up_epi", "svdq_fp4_gemm_lowrank_up_epi", "svdq_linear_epi", "svdq_w8a8_linear_epi",
-    "svdq_fp4_linear_epi", "GroupedDeviceLayer", "svdq_grouped_quantize_act_lowrank_down",
+    "svdq_w8a8_gemm_lowrank_up_epi", "svdq_fp4_gemm_lowrank_up_epi", "svdq_linear_epi_workspace_size",
+    "svdq_linear_epi", "svdq_w8a8_linear_epi", "svdq_fp4_linear_epi_workspace_size", "svdq_fp4_linear_epi", "GroupedDeviceLayer", "svdq_grouped_quantize_act_lowrank_down",
     "svdq_grouped_gemm_w4a4_lowrank_up", "svdq_grouped_linear_workspace_size", "svdq_grouped_linear",
     "svdq_combine_rows",
 ]

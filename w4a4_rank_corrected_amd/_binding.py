@@ -142,6 +142,8 @@ SIGNATURES = [
     ("svdq_fp4_gemm_lowrank_up_epi", _c_int,
      [_vp, _vp, _vp, ctypes.POINTER(svdq_fp4_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size,
       _vp]),
+    ("svdq_linear_epi_workspace_size", _size, [_c_int, _c_int, _c_int, _c_int]),
+    ("svdq_fp4_linear_epi_workspace_size", _size, [_c_int, _c_int, _c_int, _c_int]),
     ("svdq_linear_epi", _c_int,
      [_vp, ctypes.POINTER(svdq_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size, _vp]),
     ("svdq_w8a8_linear_epi", _c_int,
@@ -1014,7 +1016,7 @@ def svdq_fp4_gemm_lowrank_up_epi(qx, ascale, z, layer: DeviceLayerFp4, act: str 
                                  out_dtype=None, y=None, workspace=None, stream=None):
     """The NVFP4 setting's product with the epilogue of svdq_gemm_w4a4_lowrank_up_epi."""
     import torch
-    return _gemm_epi(lib().svdq_fp4_gemm_lowrank_up_epi, svdq_fp4_gemm_workspace_size,
+    return _gemm_epi(lib().svdq_fp4_gemm_lowrank_up_epi, svdq_gemm_epi_workspace_size,
                      (True, 32, torch.uint8, torch.uint8, (4,)), qx, ascale, z, layer, act, act_begin, gate, gate_rows,
                      residual, b, out_dtype, y, workspace, stream)
 
@@ -1033,12 +1035,20 @@ def _linear_epi(fn, size, x, layer, act, act_begin, gate, gate_rows, residual, o
     return y
 
 
+def svdq_linear_epi_workspace_size(b: int, m: int, n: int, rank: int) -> int:
+    return int(lib().svdq_linear_epi_workspace_size(b, m, n, rank))
+
+
+def svdq_fp4_linear_epi_workspace_size(b: int, m: int, n: int, rank: int) -> int:
+    return int(lib().svdq_fp4_linear_epi_workspace_size(b, m, n, rank))
+
+
 def svdq_linear_epi(x, layer: DeviceLayer, act: str = "none", act_begin: int = 0, gate=None,
                     gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None,
                     stream=None):
     """svdq_linear with the epilogue of svdq_gemm_w4a4_lowrank_up_epi (workspace:
-    svdq_linear_workspace_size bytes)."""
-    return _linear_epi(lib().svdq_linear_epi, svdq_linear_workspace_size, x, layer, act, act_begin, gate, gate_rows,
+    svdq_linear_epi_workspace_size bytes)."""
+    return _linear_epi(lib().svdq_linear_epi, svdq_linear_epi_workspace_size, x, layer, act, act_begin, gate, gate_rows,
                        residual, out_dtype, y, workspace, stream)
 
 
@@ -1052,7 +1062,7 @@ def svdq_w8a8_linear_epi(x, layer: DeviceLayer8, act: str = "none", act_begin: i
 def svdq_fp4_linear_epi(x, layer: DeviceLayerFp4, act: str = "none", act_begin: int = 0, gate=None,
                         gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None,
                         stream=None):
-    return _linear_epi(lib().svdq_fp4_linear_epi, svdq_fp4_linear_workspace_size, x, layer, act, act_begin, gate,
+    return _linear_epi(lib().svdq_fp4_linear_epi, svdq_fp4_linear_epi_workspace_size, x, layer, act, act_begin, gate,
                        gate_rows, residual, out_dtype, y, workspace, stream)
 
 

@@ -163,7 +163,14 @@ int run_act4(const uint16_t* x, const svdq_layer* layer, int b, char* ws, const 
   return hip_status(launch_z_reduce(zpart, p.splits, b, rank, z, stream), "z_reduce");
 }
 
+// INT4 and NVFP4: the row kernel takes no workspace.
 size_t gemm_epi_ws_bytes(int b, int n, int m) { return b <= kRowsMax ? 0 : gemm_ws_bytes(b, n, m); }
+size_t linear_epi_ws_bytes(const LinearWorkspace& w, int b) { return b <= kRowsMax ? w.gemm_off : w.total; }
+
+bool linear_dims_ok(int b, int m, int n, int rank) {
+  return b > 0 && b <= SVDQ_MAX_DIM && n > 0 && n <= SVDQ_MAX_DIM && m >= SVDQ_GROUP && m % SVDQ_GROUP == 0 &&
+         rank >= 0 && rank <= SVDQ_MAX_RANK;
+}
 
 }  // namespace
 
@@ -217,9 +224,17 @@ int svdq_fp4_gemm_lowrank_up_epi(const uint8_t* qx, const uint8_t* ascale, const
   if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_operands(qx, ascale, z, layer->rank, 2);
-  if (!st) st = check_workspace(workspace, workspace_bytes, gemm_ws_bytes(b, layer->n, layer->m), 16);
+  if (!st) st = check_workspace(workspace, workspace_bytes, gemm_epi_ws_bytes(b, layer->n, layer->m), 16);
   if (st) return st;
   return hip_status(launch_gemm_fp4_epi(qx, ascale, z, *layer, b, y_dtype, ep, workspace, stream), "gemm_fp4_epi");
+}
+
+size_t svdq_linear_epi_workspace_size(int b, int m, int n, int rank) {
+  return linear_dims_ok(b, m, n, rank) ? linear_epi_ws_bytes(linear_ws_layout(b, m, n, rank), b) : 0;
+}
+
+size_t svdq_fp4_linear_epi_workspace_size(int b, int m, int n, int rank) {
+  return linear_dims_ok(b, m, n, rank) ? linear_epi_ws_bytes(linear_fp4_ws_layout(b, m, n, rank), b) : 0;
 }
 
 int svdq_linear_epi(const uint16_t* x, const svdq_layer* layer, const svdq_epilogue* epi, int b, void* y, int y_dtype,
@@ -231,7 +246,7 @@ int svdq_linear_epi(const uint16_t* x, const svdq_layer* layer, const svdq_epilo
   if (!st) st = check_epilogue(epi, b, layer->n, y, y_dtype, &ep);
   if (st || done) return st;
   const LinearWorkspace w = linear_ws_layout(b, layer->m, layer->n, layer->rank);
-  st = check_workspace(workspace, workspace_bytes, w.total, kAlign);
+  st = check_workspace(workspace, workspace_bytes, linear_epi_ws_bytes(w, b), kAlign);
   if (st) return st;
   char* ws = (char*)workspace;
   st = run_act4(x, layer, b, ws, w, stream);
@@ -277,7 +292,7 @@ int svdq_fp4_linear_epi(const uint16_t* x, const svdq_fp4_layer* layer, const sv
   st = check_input(x, layer->smooth_inv, layer->l1, layer->rank);
   if (st) return st;
   const LinearWorkspace w = linear_fp4_ws_layout(b, layer->m, layer->n, layer->rank);
-  st = check_workspace(workspace, workspace_bytes, w.total, kAlign);
+  st = check_workspace(workspace, workspace_bytes, linear_epi_ws_bytes(w, b), kAlign);
   if (st) return st;
   char* ws = (char*)workspace;
   uint8_t* qx = (uint8_t*)(ws + w.qx_off);
