@@ -379,8 +379,8 @@ int svdq_combine_rows(const void* rows, int R, int n, int dtype, const int32_t* 
           "rows and residual must be element-aligned");
   REQUIRE((((uintptr_t)index | (uintptr_t)weight) & 3u) == 0, SVDQ_ERR_ALIGNMENT,
           "index and weight must be 4-byte aligned");
-  // one thread per element at the least
-  REQUIRE((long long)t * n <= 0x7FFFFFFFLL * 256, SVDQ_ERR_UNSUPPORTED, "t x n is too large (t=%d, n=%d)", t, n);
+  // 512 G elements: more than any device's memory
+  REQUIRE((long long)t * n <= 1LL << 39, SVDQ_ERR_UNSUPPORTED, "t x n is too large (t=%d, n=%d)", t, n);
   const int size = dtype == SVDQ_OUT_F32 ? 4 : 2;
   const uintptr_t row = (uintptr_t)n * size, py = (uintptr_t)y, pr = (uintptr_t)rows, ps = (uintptr_t)residual;
   const uintptr_t end = py + (uintptr_t)t * row;

@@ -344,11 +344,21 @@ int launch_combine(const void* rows, int R, int n, int dtype, const int32_t* ind
   const int w = bf ? 8 : 4;
   const bool aligned = n % w == 0 && (((uintptr_t)rows | (uintptr_t)residual | (uintptr_t)y) & 15u) == 0;
   const int units = (n + w - 1) / w;
-  const long long grid = ((long long)t * units + 255) / 256;
-  if (grid > 0x7FFFFFFF) return (int)hipErrorInvalidValue;
+  // A launch of 2^32 threads or more is cut short without an error, so outputs of
+  // more 16-byte units (64 GB) are taken some thousand tokens at a time.
+  const long long most = (0x100000000LL - 256) / units;
+  const size_t row = (size_t)n * (bf ? 2 : 4);
   auto go = [&](auto kernel) {
-    return launch_checked(kernel, (int)grid, 256, (hipStream_t)stream, rows, R, n, index, weight, t, k, residual, y,
-                          units);
+    for (long long t0 = 0; t0 < t; t0 += most) {
+      const int count = (int)std::min<long long>(t - t0, most);
+      const uint8_t* res = reinterpret_cast<const uint8_t*>(residual);
+      const int status = launch_checked(
+          kernel, (int)(((long long)count * units + 255) / 256), 256, (hipStream_t)stream, rows, R, n, index + t0 * k,
+          weight ? weight + t0 * k : nullptr, count, k, (const void*)(res ? res + t0 * row : nullptr),
+          (void*)(reinterpret_cast<uint8_t*>(y) + t0 * row), units);
+      if (status != 0) return status;
+    }
+    return 0;
   };
   if (bf) return aligned ? go(combine_kernel<true, true>) : go(combine_kernel<true, false>);
   return aligned ? go(combine_kernel<false, true>) : go(combine_kernel<false, false>);
