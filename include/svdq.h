@@ -632,6 +632,8 @@ int svdq_grouped_quantize_act_lowrank_down(const uint16_t* x, int x_rows, const 
  * the activation of an epilogue (epi NULL: none; its gate and residual must be
  * NULL, svdq_combine_rows adds the residual).  qx, ascale, z for b rows as
  * above.  Rows without an expert are neither used nor written.  No workspace.
+ * Products of more output tiles than one launch holds (2^32 threads: some 10^9
+ * columns times row blocks of 16) are refused with SVDQ_ERR_UNSUPPORTED.
  * layer->smooth_inv and l1 are not used. */
 int svdq_grouped_gemm_w4a4_lowrank_up(const uint8_t* qx, const uint16_t* ascale, const float* z,
                                       const int32_t* offsets, const svdq_grouped_layer* layer,

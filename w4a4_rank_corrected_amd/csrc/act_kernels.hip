@@ -741,6 +741,7 @@ __global__ void add_kernel(void* __restrict__ y, const void* __restrict__ t, siz
 
 int launch_add(void* y, const void* t, size_t count, int y_dtype, void* stream) {
   const unsigned blocks = (unsigned)((count + 8 * 256 - 1) / (8 * 256));
+  if (!launch_fits(blocks, 256)) return (int)hipErrorInvalidConfiguration;
   if (y_dtype == SVDQ_OUT_BF16)
     hipLaunchKernelGGL(add_kernel<true>, dim3(blocks), dim3(256), 0, (hipStream_t)stream, y, t, count);
   else

@@ -132,8 +132,9 @@ int check_grouped_gemm(const int32_t* offsets, const svdq_grouped_layer* L, cons
           "layer l2 and bias must be 2-byte aligned");
   REQUIRE(!epi || (!epi->gate && !epi->residual), SVDQ_ERR_UNSUPPORTED,
           "a grouped product takes no gate and no residual");
-  // the kernels number their tiles (16 x 16 at the smallest) with 32-bit integers
-  REQUIRE(grouped_row_blocks(b, L->experts, 16) * ((L->n + 15) / 16) <= 0x7FFFFFFF, SVDQ_ERR_UNSUPPORTED,
+  // (fewer than 2^32 threads are fewer than 2^26 tiles: 32-bit tile numbers serve)
+  const GroupedPlan plan = grouped_plan(b, L->n, L->m, L->experts);
+  REQUIRE(launch_fits(plan.grid, plan.threads), SVDQ_ERR_UNSUPPORTED,
           "too many output tiles (b=%d, n=%d, experts=%d)", b, L->n, L->experts);
   return check_epilogue(epi, b, L->n, y, y_dtype, ep);
 }

@@ -177,12 +177,11 @@ int launch_tiles_typed(const uint8_t* qx, const uint16_t* ascale, const float* z
 
 template <class C>
 int launch_grouped_tiles(const uint8_t* qx, const uint16_t* ascale, const float* z, const Operands& L, int G,
-                         const Groups& groups, int b, int y_dtype, const EpiArgs& ep, hipStream_t st) {
-  const long long tiles_n = (L.n + C::TN - 1) / C::TN;
-  const long long grid = grouped_row_blocks(b, groups.experts, C::TM) * tiles_n;
-  if (grid > 0x7FFFFFFF) return (int)hipErrorInvalidValue;
+                         const Groups& groups, int b, int y_dtype, const EpiArgs& ep, const GroupedPlan& plan,
+                         hipStream_t st) {
+  static_assert(C::TN == kGemmTileN && C::NT == 256, "the plan's tiles");
   auto go = [&](auto kernel) {
-    return launch_checked(kernel, (int)grid, C::NT, st, qx, ascale, z, L, b, G, (int)tiles_n, groups, ep);
+    return launch_checked(kernel, plan.grid, C::NT, st, qx, ascale, z, L, b, G, (L.n + C::TN - 1) / C::TN, groups, ep);
   };
   return y_dtype == SVDQ_OUT_BF16 ? go(gemm_grouped_kernel<C, true>) : go(gemm_grouped_kernel<C, false>);
 }
@@ -222,30 +221,15 @@ int launch_grouped_gemm(const uint8_t* qx, const uint16_t* ascale, const float* 
                         const int32_t* offsets, int b, int y_dtype, const EpiArgs& ep, void* stream) {
   const Groups groups{offsets, L.experts};
   const int G = L.m / SVDQ_GROUP;
-  const long long mean = (b + L.experts - 1) / L.experts;  // rows of an expert; the real counts are on the device
-  // The row kernel or tiles.  Its cost is the (16 RB rows) x (16 columns) x group
-  // steps it takes; a tile's waves share the weights, but each tile walks all
-  // groups at about half a microsecond a step, so too few tiles leave the chip
-  // waiting.  Product alone, us, row kernel against 64 x 128 tiles:
-  //   mean rows 4   of 64 experts, 2048 -> 1408: 21 / 26;  mean 16: 38 / 33;  mean 32: 53 / 43
-  //   mean rows 16  of 8 experts,  1152 -> 4608: 14 / 18 (324 tiles);  mean 64: 25 / 19 (540 tiles)
-  //   mean rows 150 of 4 experts,  4608 -> 1152: 21 / 39 (117 tiles)
-  const int rb = mean <= 16 ? 1 : 2;
-  const long long steps = grouped_row_blocks(b, L.experts, 16 * rb) * ((L.n + 15) / 16) * G;
-  const long long tiles = grouped_row_blocks(b, L.experts, 64) * ((L.n + 127) / 128);
-  if (mean <= 8 || (tiles <= 384 && steps <= 160000)) {
+  const GroupedPlan plan = grouped_plan(b, L.n, L.m, L.experts);
+  if (plan.rb > 0) {
     const RowsArgs a{qx, ascale, z, L.qw, L.wscale, L.l2, L.bias, b, L.n, G, L.rank, groups, ep, 1.0f};
-    return launch_gemm_rows(a, rb, y_dtype, kFmtInt4, stream);
+    return launch_gemm_rows(a, plan.rb, y_dtype, kFmtInt4, stream);
   }
-  // 128 x 128 tiles do the most work per staged record, 64 x 128 tiles leave less
-  // of an expert's last row block empty and fill the chip with fewer rows: mean
-  // rows 64 of 64 experts (2048 -> 1408) 66 / 51 us, 128: 80 / 73, 281: 133 / 140;
-  // mean 256 of 8 experts, 4608 -> 1152 (207 wide tiles) 70 / 63.
   const Operands o{L.qw, L.wscale, L.l2, L.bias, L.n, L.rank};
-  const bool wide = mean >= 256 && grouped_row_blocks(b, L.experts, 128) * ((L.n + 127) / 128) >= 3 * kMaxCUs;
   hipStream_t st = (hipStream_t)stream;
-  return wide ? launch_grouped_tiles<Cfg>(qx, ascale, z, o, G, groups, b, y_dtype, ep, st)
-              : launch_grouped_tiles<CfgG>(qx, ascale, z, o, G, groups, b, y_dtype, ep, st);
+  return plan.tile_m == Cfg::TM ? launch_grouped_tiles<Cfg>(qx, ascale, z, o, G, groups, b, y_dtype, ep, plan, st)
+                                : launch_grouped_tiles<CfgG>(qx, ascale, z, o, G, groups, b, y_dtype, ep, plan, st);
 }
 
 }  // namespace svdq

@@ -192,6 +192,23 @@ constexpr long long grouped_row_blocks(long long b, long long experts, long long
 }
 // Rows up to which the INT4 and NVFP4 products with an epilogue use the row kernel.
 constexpr int kRowsMax = 64;
+// A launch of 2^32 threads or more is cut short without an error.
+constexpr bool launch_fits(long long grid, long long threads) { return grid * threads < 0x100000000LL; }
+// How a row kernel's workgroup is cut: nwk waves split the channel groups of the
+// same columns, nwc take neighbouring column blocks.
+struct RowsSplit {
+  int nwk, nwc;
+  long long grid;
+};
+RowsSplit rows_split(long long row_blocks, int n, int G, int rb);
+// The kernel of a grouped product: the row kernel (rb 16-row blocks a workgroup),
+// or tiles of tile_m rows x 128 columns (rb = 0); its largest launch.
+struct GroupedPlan {
+  int rb, tile_m;
+  long long grid;
+  int threads;
+};
+GroupedPlan grouped_plan(int b, int n, int m, int experts);
 int launch_gemm_epi(const uint8_t* qx, const uint16_t* ascale, const float* z, const svdq_layer& L, int b,
                     int y_dtype, const EpiArgs& ep, void* ws, void* stream);
 int launch_gemm8_epi(const int8_t* qx, const uint16_t* ascale, const float* z, const svdq_w8a8_layer& L, int b,

@@ -31,7 +31,8 @@ int scratch_free(const void* kernel) {
 }
 
 template <class K, class... Args>
-int launch_checked(K kernel, int grid, int threads, hipStream_t st, Args... args) {
+int launch_checked(K kernel, long long grid, int threads, hipStream_t st, Args... args) {
+  if (!launch_fits(grid, threads)) return (int)hipErrorInvalidConfiguration;
   const int ok = scratch_free(reinterpret_cast<const void*>(kernel));
   if (ok != 0) return ok;
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), 0, st, args...);

@@ -1,6 +1,6 @@
-// Launch plan of the GEMM kernels (host logic; the kernels are in
+// Launch plans of the GEMM kernels (host logic; the kernels are in
 // gemm_kernels.hip, which checks its builds against the tiling and
-// residencies declared in internal.h).
+// residencies declared in internal.h, epi_kernels.hip and rows_kernels.hip).
 #include <algorithm>
 
 #include "internal.h"
@@ -58,6 +58,50 @@ GemmPlan gemm_plan(int b, int n, int m, int cus, int fmt) {
   const long long max_slots = kcap >= 2 ? std::min(round, T128 * kcap) + std::min(T128, round / 2) : 0;
   p.partial_bytes = (size_t)max_slots * kGemmTileM * kGemmTileN * 4;
   p.ws_bytes = p.partial_bytes;
+  return p;
+}
+
+// Waves to split the groups over: up to the 16 waves a CU that are resident
+// together (more would wait for a second round), each with two groups at the
+// least; then column blocks until a workgroup has four waves.
+RowsSplit rows_split(long long row_blocks, int n, int G, int rb) {
+  const long long tiles = row_blocks * ((n + 15) / 16);
+  RowsSplit s{1, 1, 0};
+  while (s.nwk < (rb == 4 ? 8 : 16) && tiles * s.nwk <= 2048 && G >= 4 * s.nwk) s.nwk *= 2;
+  if (s.nwk < 4) s.nwc = 4 / s.nwk;
+  s.grid = row_blocks * ((n + 16 * s.nwc - 1) / (16 * s.nwc));
+  return s;
+}
+
+// The row kernel or tiles.  The row kernel's cost is the (16 RB rows) x (16
+// columns) x group steps it takes; a tile's waves share the weights, but each
+// tile walks all groups at about half a microsecond a step, so too few tiles
+// leave the chip waiting.  Product alone, us, row kernel against 64 x 128 tiles:
+//   mean rows 4   of 64 experts, 2048 -> 1408: 21 / 26;  mean 16: 38 / 33;  mean 32: 53 / 43
+//   mean rows 16  of 8 experts,  1152 -> 4608: 14 / 18 (324 tiles);  mean 64: 25 / 19 (540 tiles)
+//   mean rows 150 of 4 experts,  4608 -> 1152: 21 / 39 (117 tiles)
+// 128 x 128 tiles do the most work per staged record, 64 x 128 tiles leave less
+// of an expert's last row block empty and fill the chip with fewer rows: mean
+// rows 64 of 64 experts (2048 -> 1408) 66 / 51 us, 128: 80 / 73, 281: 133 / 140;
+// mean 256 of 8 experts, 4608 -> 1152 (207 wide tiles) 70 / 63.
+GroupedPlan grouped_plan(int b, int n, int m, int experts) {
+  const int G = m / 64;
+  const long long mean = (b + experts - 1) / experts;  // rows of an expert; the real counts are on the device
+  const long long cols = (n + kGemmTileN - 1) / kGemmTileN;
+  GroupedPlan p{mean <= 16 ? 1 : 2, 0, 0, 0};
+  const long long blocks = grouped_row_blocks(b, experts, 16 * p.rb), steps = blocks * ((n + 15) / 16) * G;
+  const long long tiles = grouped_row_blocks(b, experts, 64) * cols;
+  if (mean <= 8 || (tiles <= 384 && steps <= 160000)) {
+    const RowsSplit s = rows_split(blocks, n, G, p.rb);
+    p.grid = s.grid;
+    p.threads = 64 * s.nwk * s.nwc;
+    return p;
+  }
+  p.rb = 0;
+  const long long wide = grouped_row_blocks(b, experts, 128) * cols;
+  p.tile_m = mean >= 256 && wide >= 3 * kMaxCUs ? 128 : 64;
+  p.grid = p.tile_m == 128 ? wide : tiles;
+  p.threads = 256;
   return p;
 }
 

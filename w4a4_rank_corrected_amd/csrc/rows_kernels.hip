@@ -252,16 +252,10 @@ __global__ __launch_bounds__(RB == 4 ? 512 : 1024) void gemm_w4a4_rows_kernel(Ro
 
 template <int RB, bool OUT_BF16, bool GROUPED, int FMT>
 int launch_rows(const RowsArgs& a, hipStream_t st) {
-  // Waves to split the groups over: up to the 16 waves a CU that are resident
-  // together (more would wait for a second round), each with two groups at the
-  // least; then column blocks until a workgroup has four waves.
-  const long long blocks = GROUPED ? grouped_row_blocks(a.b, a.groups.experts, 16 * RB) : 1;
-  const long long tiles = blocks * ((a.n + 15) / 16);
-  int nwk = 1;
-  while (nwk < (RB == 4 ? 8 : 16) && tiles * nwk <= 2048 && a.G >= 4 * nwk) nwk *= 2;
-  const int nwc = nwk < 4 ? 4 / nwk : 1;
-  const long long grid = blocks * ((a.n + 16 * nwc - 1) / (16 * nwc));
-  if (grid > 0x7FFFFFFF) return (int)hipErrorInvalidValue;
+  const RowsSplit split = rows_split(GROUPED ? grouped_row_blocks(a.b, a.groups.experts, 16 * RB) : 1, a.n, a.G, RB);
+  const int nwk = split.nwk, nwc = split.nwc;
+  const long long grid = split.grid;
+  if (!launch_fits(grid, 64 * nwk * nwc)) return (int)hipErrorInvalidConfiguration;
   const size_t lds = (size_t)nwk * nwc * RB * 1024;
   const bool swv = a.n % 4 == 0 && ((uintptr_t)a.wscale & 7u) == 0;
   auto go = [&](auto kernel) {
