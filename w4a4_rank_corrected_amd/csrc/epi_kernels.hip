@@ -118,14 +118,23 @@ void whole_tiles(GemmPlan& p, int b, int n) {
 //     200 x 1152 -> 4608 16.4 / 14.5, 500 rows 22.4 / 19.5, 1000 x 2048 -> 2048
 //     24.4 / 21.9; 500 x 2048 -> 2048 17.5 / 20.6, 256 x 4096 -> 8000 31.9 / 36.6,
 //     1000 x 4608 -> 1152 24.7 / 39.9).
-// 8 bits, whose tiles are bound by the matrix units:
-//   * up to 384 tiles are cut into 64 x 64 tiles instead, unsplit (plain plan /
-//     64 x 64: 500 x 2048 -> 2048 17.5 / 11.0; 1000 x 1152 -> 4608 33.2 / 20.8;
-//     1500 x 4608 -> 2048 36.4 / 29.1; 576 tiles, 2000 x 4608 -> 4608: 64 / 76),
-//     unless they are fewer than CUs and long (256 x 4608 -> 1152: 14.1 / 16.3);
-//   * a launch that is split whole gets as many pieces as give every CU one
-//     workgroup, not three (1000 x 4608 -> 1152, 72 tiles: 3 pieces 21.4 us, 2:
-//     24.0, 4: 23.4, 10: 27.3).
+// 8 bits, up to 384 tiles (more keep the plain plan: 576, 2000 x 4608 -> 4608, 64
+// us, 64 x 64 tiles 76): the quicker of
+//   * 64 x 64 tiles, unsplit: 5.2 us + 0.155 us a group, and 0.42 of that again
+//     for each further round of one tile a CU;
+//   * as many pieces as give every CU one workgroup, two at the least: 8.5 us +
+//     0.3 us a group of a piece + 0.02 us a piece (more pieces are slower: 1000 x
+//     4608 -> 1152, 72 tiles, 3 pieces 21.0 us, 10 27.1).
+// 64 x 64 / pieces, rank 16, gate, residual, us:
+//   1 x 1152 -> 4608 7.3 / 11.7; 128 x 2048 -> 2048 10.2 / 12.1; 256 x 3008 -> 1152
+//   13.6 / 13.4; 1 x 4032 -> 1152 13.0 / 10.8; 100 x 4032 -> 512 14.2 / 10.2; 256 x
+//   4032 -> 1152 15.8 / 13.8; 400 x 4032 -> 1152 15.4 / 15.6; 256 x 4096 -> 2048
+//   15.7 / 16.8; 256 x 4608 -> 1152 16.8 / 14.0; 500 x 4608 -> 1152 16.8 / 16.4; 500
+//   x 4608 -> 2048 17.4 / 20.2; 65 x 8192 -> 2048 23.5 / 14.1; 1 x 8192 -> 8192 22.8 /
+//   23.2; 1000 x 4608 -> 1152 (288 tiles of 64 x 64) 21.8 / 21.0; 600 x 8192 -> 2048
+//   31.5 / 27.0; 1000 x 4096 -> 2048 23.0 / 28.5; 1500 x 4608 -> 2048 31.0 / 37.4.
+// On 60 random shapes (1..3000 rows, 256..8960 -> 64..9216) the choice was within
+// 7 % of the quicker side.
 // NVFP4, which the plain product never splits: into as many pieces as two
 // workgroups a CU take, where the 0.62 us a group that they save pay for the
 // launch and for 0.03 us a piece (whole / split, us: 256 x 4608 -> 1152 51.6 /
@@ -155,11 +164,15 @@ GemmPlan epi_plan(int b, int n, int m, int fmt) {
     }
   }
   if (fmt == kFmtInt8) {
+    const long long cus = device_cus();
     const long long small = (long long)((b + Cfg8S::TM - 1) / Cfg8S::TM) * ((n + Cfg8S::TN - 1) / Cfg8S::TN);
-    if (T <= 384 && (p.G < 64 || small >= device_cus())) {
+    const long long k = std::min<long long>(p.pieces, cus / T);
+    const double whole = (5.2 + 0.155 * p.G) * (1.0 + 0.42 * (double)((small - 1) / cus));
+    const double split = 8.5 + 0.3 * p.G / (double)std::max<long long>(k, 1) + 0.02 * (double)(T * k);
+    if (T <= 384 && (k < 2 || whole <= split)) {
       whole_tiles<Cfg8S>(p, b, n);
     } else if (p.split && p.split_tiles == T) {
-      p.pieces = (int)std::max<long long>(2, std::min<long long>(p.pieces, device_cus() / T));
+      p.pieces = (int)std::max<long long>(2, k);
       p.split_grid = p.grid = (int)T * p.pieces;
     }
   }

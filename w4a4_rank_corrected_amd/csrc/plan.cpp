@@ -80,6 +80,11 @@ RowsSplit rows_split(long long row_blocks, int n, int G, int rb) {
 //   mean rows 4   of 64 experts, 2048 -> 1408: 21 / 26;  mean 16: 38 / 33;  mean 32: 53 / 43
 //   mean rows 16  of 8 experts,  1152 -> 4608: 14 / 18 (324 tiles);  mean 64: 25 / 19 (540 tiles)
 //   mean rows 150 of 4 experts,  4608 -> 1152: 21 / 39 (117 tiles)
+// and about the limits, where the slower side was taken by 10 % at the most:
+//   mean 8  of 64 experts, 2048 -> 1408 (259 000 steps) 26.4 / 31.9;  mean 10 (282 000): 29.6 / 32.5
+//   mean 24 of 8 experts,  1152 -> 4608 (360 tiles) 17.0 / 18.0;  mean 32 (396 tiles): 17.2 / 18.3
+//   mean 200 of 4 experts, 4608 -> 1152 (145 000 steps) 26.6 / 38.1;  mean 128 of 8 (202 000): 37.6 / 38.4
+//   mean 10 of 128 experts, 1152 -> 512 (584 tiles) 18.7 / 18.7
 // 128 x 128 tiles do the most work per staged record, 64 x 128 tiles leave less
 // of an expert's last row block empty and fill the chip with fewer rows: mean
 // rows 64 of 64 experts (2048 -> 1408) 66 / 51 us, 128: 80 / 73, 281: 133 / 140;
