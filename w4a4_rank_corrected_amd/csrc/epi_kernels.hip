@@ -17,13 +17,19 @@ namespace {
 using namespace dev;
 
 // INT4 is bound by the two FMAs per output and channel group that apply the
-// scales (4096 x 1152 -> 4608 with GELU: 55 us, of which the 18 groups are 33 and
-// y's write, Z L2 and GELU the rest); 8 bits by the steps over the groups when
-// tiles are few (1000 x 4608 -> 1152: 72 steps in 21 us); NVFP4 by the
-// dequantization, which every wave does for its own operands (2304 x 1152 -> 4608
-// with GELU: 40.1 us, 128 vector instructions a group beside 32 MFMAs; 42.5 us
-// with the block scales widened bit by bit, 44.9 us with 32 LDS reads a group
-// instead of 10 as well).
+// scales (4096 x 1152 -> 4608 with GELU: 52.6 us, of which the 18 groups are 33 and
+// y's write, Z L2 and GELU the rest).  8 bits with hundreds of rows: neither the
+// vector nor the matrix units are busy (1000 x 4608 -> 1152: 14.8 us and 6.7 us of
+// reduction, 0.34 M MFMAs are 2 us of them); the pieces fetch 52 MB past the L2s
+// for 10 MB of codes, since every XCD's L2 takes its own copy, and write 19 MB of
+// sums.  How much of the time that is, and how much the latency of the steps,
+// is not told apart: 64 x 64 tiles (36 MB, no sums to write) take 21.8 us.
+// NVFP4: the dequantization, which every wave does for its own operands (2304 x
+// 1152 -> 4608 with GELU: 39.6 us; 128 vector instructions a group for it, 265 a
+// group by the counters with staging, addresses and the epilogue, 45 % of the
+// vector units' time, beside 33 MFMAs, 25 % of theirs), and 648 tiles on 256 CUs,
+// 3 on the fullest (42.5 us with the block scales widened bit by bit, 44.9 us with
+// 32 LDS reads a group instead of 10 as well).
 template <class C, bool OUT_BF16, int FMT, bool SK>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE))) void gemm_epi_kernel(
     const uint8_t* __restrict__ qx, const uint16_t* __restrict__ ascale, const float* __restrict__ z, Operands L, int b,
@@ -43,8 +49,8 @@ using CfgG = GemmCfg<64, 128, 64, 32, 3, 2>;
 
 // One tile of one expert per workgroup; the workgroups past the last tile end.
 // Bound as the dense INT4 product, plus the empty rows of each expert's last row
-// block: 8192 rows of 8 experts, 1152 -> 4608: 98 us; 18006 rows of 64 experts,
-// 2048 -> 1408: 117 us, 27 % more tile rows than rows.
+// block: 8192 rows of 8 experts, 1152 -> 4608: 98.8 us; 18006 rows of 64 experts,
+// 2048 -> 1408: 118 us, 27 % more tile rows than rows.
 template <class C, bool OUT_BF16>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPE, C::WPE))) void gemm_grouped_kernel(
     const uint8_t* __restrict__ qx, const uint16_t* __restrict__ ascale, const float* __restrict__ z, Operands L, int b,

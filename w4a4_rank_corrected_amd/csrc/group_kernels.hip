@@ -33,7 +33,9 @@ using namespace dev;
 // rows, kept the address path busy instead: 26.4 against 18.5 us for 18006 rows
 // of 2048 channels at rank 16, 43.6 against 26.8 us for 8192 of 4608 at rank 32.
 // What bounds it now is the gather: 94 MB of rows and codes in those 18.5 us,
-// 5.1 TB/s (a large copy reaches 5.1).
+// 5.1 TB/s (a large copy reaches 5.1).  These are of the kernel alone, over and
+// over; between the products of a layer's calls, which leave little of x in the
+// caches, the first shape takes 21.8 us (4.3 TB/s).
 // A row index outside [0, x_rows) reads as a row of zeros.
 // Q = kActQuantNone: Z alone, of ranks rank0 .. rank0 + 16 TB - 1 (further ranks
 // of layers with more than 64).
@@ -211,7 +213,7 @@ __attribute__((amdgpu_waves_per_eu(group_waves_per_simd(TB)))) void grouped_act_
 // with element-aligned vectors (gfx950 loads and stores them at any address);
 // only the last columns of a row are taken one by one.  An index outside [0, R)
 // adds nothing.
-// Bound by memory: 4096 tokens x 6 rows of 2048 bf16 28.6 us, 4.7 TB/s (36 us
+// Bound by memory: 4096 tokens x 6 rows of 2048 bf16 28.1 us, 4.8 TB/s (36 us
 // with the rows widened to fp32 on arrival: 100 registers).
 // ---------------------------------------------------------------------------
 constexpr int kCombineBatch = 8;

@@ -140,10 +140,11 @@ __device__ __forceinline__ void quant_store(const float (&v)[16], int g, int b, 
 //   codes: round_half_even(fl32(v / s)) needs v / s only near a tie k + 1/2.  A
 //     bf16 v (8 significant bits) and an fp16 s (11) have v / s = k + 1/2 exactly
 //     or at least 2^-12 away from it, for |v / s| in 1/4 .. 8 (a nonzero
-//     2 v - (2k+1) s is a multiple of the coarser of v's and s's last bits).  With
-//     rc = 1/s to an ulp, v rc is off by at most 2^-20, so fma(v, rc, 384), which
-//     rounds to multiples of 2^-15, lands on the tie exactly where there is one
-//     and on its own side of it elsewhere; the clamp and the rounding addition
+//     2 v - (2k+1) s is a multiple of the finer of s's last bit and twice v's: s's
+//     is s 2^-11 or more, twice v's v 2^-7 or more, and the distance is that over
+//     2 s).  With rc = 1/s to an ulp, v rc is off by at most 2^-20, so fma(v, rc,
+//     384), which rounds to multiples of 2^-15, lands on the tie exactly where there
+//     is one and on its own side of it elsewhere; the clamp and the rounding addition
 //     then give the definition's code (384 is even, so ties keep their parity).
 __device__ __forceinline__ void quant_store_int4(const float (&v)[16], int g, int b, uint32_t q_off, uint32_t s_off,
                                                  uint8_t* __restrict__ qx, uint16_t* __restrict__ ascale) {

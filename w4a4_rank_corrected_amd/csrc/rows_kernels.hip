@@ -14,9 +14,9 @@
 // so weights and activations go from memory to registers to the MFMA, D groups
 // ahead.  Any channel order serves, as both operands unpack alike.
 //
-// Measured: 64 experts, 128 rows, 2048 -> 1408: 17.5-19 us for 93 MB, nearly all
-// weights, 5 TB/s (a large copy reaches 5.1).  One row, 4608 -> 1152: 5.9 us, and
-// 13 rows, 2048 -> 5001: 6.3 us, which is a launch and one chain of dependent
+// Measured: 64 experts, 128 rows, 2048 -> 1408: 19.0 us (17.4 at the least) for 93
+// MB, nearly all weights, 4.9 TB/s (a large copy reaches 5.1).  One row, 4608 ->
+// 1152: 5.8 us, and 13 rows, 2048 -> 5001: 6.1 us, which is a launch and one chain of dependent
 // loads, not bandwidth.  Against tiles (12288 -> 3000, one layer): 1 to 64 rows
 // 10.5-17 us, tiles 20-24 us; for 65 to 128 rows it was faster on some shapes and
 // 20-25 % slower on others, so tiles take those.  NVFP4 against split tiles, 8192
