@@ -38,11 +38,11 @@ __device__ __forceinline__ float gelu_tanh(float v) {
 // GELU with the normal distribution's integral, v Phi(v).  With a = |v|,
 // Phi(-a) = 2^q / 2, q = log2(2 Phi(-a)) = a P(a): q is smooth, 0 at 0, and an
 // error d of q is one of Phi(-a) d ln 2 in the result, so q's rounding costs
-// least where q is large, and no terms of opposite signs meet.  P: degree 9,
+// least where q is large; P's terms of opposite signs are small.  P: degree 9,
 // fitted to |error of Phi(-a)| on [0, 5.5] by linear programming (1e-9; a weight
 // of at least 2e-4 keeps 5e-6 relative up to a = 5); past it q falls below
 // every bound there, to -inf.  In 32 bits, with v_exp_f32 off by an ulp either
-// way, Phi is off by at most 9e-8 (swept over all of v by the tests); a sum of
+// way, Phi is off by at most 9e-8 (the tests sweep every v); a sum of
 // alternating terms times exp(-v^2/2) was off by 4e-7.
 __device__ __forceinline__ float gelu_erf(float v) {
   constexpr float kPhi[10] = {-1.15110421f,   -0.459222108f,   -0.0524303243f,  0.00691764802f,  3.67327812e-05f,
