@@ -20,7 +20,8 @@ def test_host_checks(tmp_path, program, says):
     exe = str(tmp_path / program)
     sources = [os.path.join(CSRC, f) for f in ("api.cpp", "epi_api.cpp", "prep.cpp", "bundle.cpp", "plan.cpp")] + \
               [os.path.join(NATIVE, f) for f in ("device_stubs.cpp", "epi_stubs.cpp", program + ".cpp")]
-    res = subprocess.run(["g++", "-std=c++17", "-O1", "-ffp-contract=off", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}",
+    res = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined",
+                          "-fno-sanitize-recover=undefined", "-ffp-contract=off", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}",
                           *sources, "-o", exe, "-pthread"], capture_output=True, text=True)
     assert res.returncode == 0, res.stderr[-4000:]
     run = subprocess.run([exe], capture_output=True, text=True, timeout=120)
