@@ -538,7 +538,8 @@ int svdq_fp4_linear(const uint16_t* x, const svdq_fp4_layer* layer, int b, void*
 enum { SVDQ_ACT_NONE = 0, SVDQ_ACT_GELU_TANH = 1, SVDQ_ACT_GELU_ERF = 2, SVDQ_ACT_SILU = 3, SVDQ_ACT_RELU = 4 };
 
 /*   act, act_begin  0 <= act_begin <= n.
- *   gate            bf16 [ceil(b / gate_rows)][n] or NULL (= 1); any alignment.
+ *   gate            bf16 [ceil(b / gate_rows)][n] or NULL (= 1); any alignment;
+ *                   apart from y.
  *   gate_rows       rows that share a gate row; 0 = all b rows share one.
  *   residual        y's type, row i at residual + i * ldr, or NULL (= 0); element
  *                   alignment.  It may be y itself (same address and stride);
@@ -575,7 +576,8 @@ int svdq_fp4_gemm_lowrank_up_epi(const uint8_t* qx, const uint8_t* ascale, const
                                  size_t workspace_bytes, void* stream);
 
 /* DEVICE: the whole layer with an epilogue: the activation kernels of
- * svdq_linear (svdq_w8a8_linear, svdq_fp4_linear), then the product above.
+ * svdq_linear (svdq_w8a8_linear, svdq_fp4_linear), then the product above.  x
+ * may be y (and the residual).
  * Workspace: 256-byte aligned, >= svdq_linear_epi_workspace_size (8 bits:
  * svdq_w8a8_linear_workspace_size; NVFP4: svdq_fp4_linear_epi_workspace_size)
  * bytes; up to 64 rows take less than svdq_linear's and svdq_fp4_linear's. */

@@ -138,3 +138,58 @@ def test_8bit_small_tiles_and_pieces(S, b, m, n, rank):
     c = Case(S, "w8a8", b, m, n, rank, bias=rank == 0)
     c.run(act="gelu_erf", act_begin=n // 3, gate_rows=max(1, b // 3), residual=True, out="bf16", inplace=True)
     c.run(out="f32")
+
+
+def _whole_layer(S, fmt, m, n, rank, seed):
+    """(layer, its linear call) with random codes, smoothing and branch."""
+    c = Case(S, fmt, 1, m, n, rank, seed=seed)
+    rng = np.random.default_rng([seed, m])
+    l1 = torch.from_numpy(rng.standard_normal((rank, m)).astype(np.float32) / np.float32(np.sqrt(m))).cuda().bfloat16()
+    inv = torch.from_numpy(np.exp(0.3 * rng.standard_normal(m)).astype(np.float32)).cuda()
+    L = c.layer
+    head = (m, n, rank) + ((L.t_x, L.t_w) if fmt == "fp4" else ())
+    linear = {"int4": S.svdq_linear_epi, "w8a8": S.svdq_w8a8_linear_epi, "fp4": S.svdq_fp4_linear_epi}[fmt]
+    return type(L).from_tensors(*head, L.qw, L.wscale, l1, L.l2, inv, L.bias), linear
+
+
+@pytest.mark.parametrize("fmt", ["int4", "w8a8", "fp4"])
+@pytest.mark.parametrize("b", [5, 150])
+def test_whole_layers_in_a_graph(S, fmt, b):
+    """Two layers one after the other in one graph, without workspaces of the caller's: replays equal eager calls."""
+    _say(f"graph of whole layers {fmt} b={b}")
+    m, n = 512, 2112
+    (up, call), (down, _) = _whole_layer(S, fmt, m, n, 16, 1), _whole_layer(S, fmt, n, m, 24, 2)
+    x = torch.randn(b, m, device="cuda").bfloat16()
+    gate = torch.randn(1, m, device="cuda").bfloat16()
+    y = torch.empty_like(x)
+
+    def block(out):
+        h = call(x, up, act="gelu_erf", act_begin=100)
+        return call(h, down, gate=gate, residual=x, y=out)
+
+    block(y)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        block(y)
+    for k in range(4):
+        x.copy_(torch.randn_like(x))
+        want = block(None)
+        torch.cuda.synchronize()
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), k
+
+
+@pytest.mark.parametrize("fmt", ["int4", "w8a8", "fp4"])
+@pytest.mark.parametrize("b", [1, 40, 300])
+def test_layer_in_place_on_its_input(S, fmt, b):
+    """x is the residual and y too: the activations are quantized before the product writes."""
+    _say(f"in place {fmt} b={b}")
+    layer, call = _whole_layer(S, fmt, 1024, 1024, 16, 3)
+    x = torch.randn(b, 1024, device="cuda").bfloat16()
+    want = call(x, layer, act="silu", residual=x)
+    got = call(x, layer, act="silu", residual=x, y=x)
+    torch.cuda.synchronize()
+    assert got.data_ptr() == x.data_ptr() and torch.equal(got, want)
