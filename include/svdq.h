@@ -659,6 +659,149 @@ int svdq_grouped_linear(const uint16_t* x, int x_rows, const int32_t* row_index,
 int svdq_combine_rows(const void* rows, int R, int n, int dtype, const int32_t* index, const float* weight, int t,
                       int k, const void* residual, void* y, void* stream);
 
+/* DEVICE: the rows of a router's choice in the order of their experts, with
+ * which the grouped layers and svdq_combine_rows are called.
+ *   expert  device int32 [t][k]: the expert of slot (t, q); one outside
+ *           [0, experts) drops the slot (a padding token's).
+ * The b = t k slots are sorted by expert, those of one expert in their order in
+ * `expert`, the dropped ones behind the last expert.  Outputs, all written:
+ *   offsets    int32 [experts + 1]: rows offsets[e] .. offsets[e+1]-1 are expert
+ *              e's; offsets[experts] .. b-1 the dropped slots'.
+ *   row_index  int32 [b]: the token of each row.
+ *   index      int32 [t][k]: the row r of each slot, -1 - r of a dropped one
+ *              (svdq_combine_rows adds nothing for it).
+ * Element alignment; no two of the four overlap.  t, t k <= SVDQ_MAX_DIM;
+ * 1 <= k <= SVDQ_MAX_EXPERTS; 1 <= experts <= SVDQ_MAX_EXPERTS.
+ * Workspace: 16-byte aligned, >= svdq_sort_rows_workspace_size(t, k, experts)
+ * bytes (0 for few slots), not shared by calls that overlap in time, no part of
+ * it needs clearing. */
+size_t svdq_sort_rows_workspace_size(int t, int k, int experts);
+int svdq_sort_rows(const int32_t* expert, int t, int k, int experts, int32_t* offsets, int32_t* row_index,
+                   int32_t* index, void* workspace, size_t workspace_bytes, void* stream);
+
+/* DEVICE: the tokens' rows in the order that `index` gives (the transpose of
+ * svdq_combine_rows):
+ *     rows[index[t,q], j] = weight[t,q] x[t,j]
+ * one product in fp32, rounded once.
+ *   x [t][n] in dtype (SVDQ_OUT_BF16 or SVDQ_OUT_F32); weight fp32 [t][k] or NULL
+ *   (= 1: rows are copies); rows [R][n] in dtype, apart from x.  index device
+ *   int32 [t][k] as svdq_sort_rows writes it: a negative -1 - r (a dropped slot's
+ *   row) makes row r zero; a row outside [0, R) is not written, and neither is a
+ *   row that no slot names.  A row that several slots name gets the product of
+ *   any one of them, in pieces.  Element alignment.  1 <= k <= SVDQ_MAX_EXPERTS. */
+int svdq_dispatch_rows(const void* x, int t, int n, int dtype, const int32_t* index, const float* weight, int k, int R,
+                       void* rows, void* stream);
+
+/* DEVICE: the gradient of svdq_combine_rows.  For dy = d loss / d y:
+ *     drows[index[t,q], j] = weight[t,q] dy[t,j]     (as svdq_dispatch_rows)
+ *     dweight[t,q] = sum_j dy[t,j] rows[index[t,q], j]    (fp32, a fixed order)
+ * and dweight 0 for an index outside [0, R).  The residual's gradient is dy.
+ *   dy [t][n], rows [R][n], drows [R][n] in dtype; dweight fp32 [t][k].  drows
+ *   or dweight may be NULL (not wanted; without dweight rows is not used).
+ *   weight NULL: ones.  index: each row named once at the most, as
+ *   svdq_sort_rows writes it; of a row that several slots name drows gets one
+ *   slot's part, in pieces, not the sum (dweight is right all the same).
+ *   drows and dweight are apart from each other and from the inputs, except that
+ *   drows may be rows when each row is named once at the most.  Element
+ *   alignment.  1 <= k <= SVDQ_MAX_EXPERTS.
+ * The gradient of a grouped layer's gather (row_index) is svdq_combine_rows of
+ * the rows' gradients without weights. */
+int svdq_combine_rows_grad(const void* dy, int t, int n, int dtype, const int32_t* index, const float* weight, int k,
+                           const void* rows, int R, void* drows, float* dweight, void* stream);
+
+/* ===========================================================================
+ * The 8-bit floating-point setting: E4M3 codes with one power-of-two scale for
+ * each block of 128, for layers that 4 bits do not carry and for experts.
+ * No smoothing and no low-rank branch: a block's own exponent and the codes'
+ * four significant bits hold an activation's strong channels.
+ *   blocks  X: 128 channels of a row.  W: 128 input x 128 output channels.  The
+ *           last block of a dimension that 128 does not divide is shorter.
+ *   scale   2^e with the least e that brings the block's largest magnitude to at
+ *           most 448 2^e, -126 <= e; a block of zeros has e = -126.  Stored as
+ *           the byte e + 127 (E8M0).
+ *   code    E4M3 (bias 7, largest 448, steps of 2^-9 below 2^-6) of value 2^-e,
+ *           rounded to nearest, ties to even.  A block that holds an infinity or
+ *           a NaN has e = 0 and the NaN code 0x7F everywhere, so that its row (or
+ *           its columns) of Y is NaN.
+ *   v[i,j] = sum_g 2^(ex[g,i] + ew[g,j/128]) sum_{k in g} cx[i,k] cw[k,j] + bias[j]
+ * Scaling by powers of two is exact and the matrix instruction applies it, so
+ * that the products of all blocks run through its accumulators in fp32.
+ * Layouts, G = ceil(m / 128):
+ *   codes of X   [G][rows][128]: byte t of a record is channel 128 g + t's code,
+ *                zero behind channel m - 1;   scales of X  [G][rows].
+ *   codes of W   [G][n][128], likewise;       scales of W  [G][ceil(n / 128)].
+ * m and n are any dimensions here (1 .. SVDQ_MAX_DIM).
+ * ========================================================================= */
+#define SVDQ_FP8_BLOCK 128
+
+/* A layer on the device: qw and wscale as above (svdq_fp8_quantize_weights makes
+ * them), bias bf16 [n] or NULL (element alignment).  wscale: any alignment. */
+typedef struct svdq_fp8_layer {
+  int32_t m, n;
+  const uint8_t* qw;
+  const uint8_t* wscale;
+  const uint16_t* bias;
+} svdq_fp8_layer;
+
+/* One layer per expert, every tensor with a leading expert dimension. */
+typedef struct svdq_fp8_grouped_layer {
+  int32_t experts, m, n;
+  const uint8_t* qw;
+  const uint8_t* wscale;
+  const uint16_t* bias;
+} svdq_fp8_grouped_layer;
+
+/* DEVICE: weights to codes and scales, `experts` layers at a time (1: one layer;
+ * any number up to SVDQ_MAX_DIM).
+ *   W  [experts][m][n], or with transposed != 0 [experts][n][m], in w_dtype
+ *      (SVDQ_OUT_BF16 or SVDQ_OUT_F32), element alignment.
+ *   qw [experts][G][n][128], wscale [experts][G][ceil(n / 128)].
+ * The blocks of W's transpose are the transposed blocks, so the layer n -> m of
+ * W^T (m and n exchanged, `transposed` the other way) has the same values: with
+ * it svdq_fp8_linear of dY is dX = dY W^T, the gradient of a layer's input. */
+int svdq_fp8_quantize_weights(const void* W, int w_dtype, int experts, int m, int n, int transposed, uint8_t* qw,
+                              uint8_t* wscale, void* stream);
+
+/* DEVICE: x bf16 [b][m] (element alignment) to qx [G][b][128], ascale [G][b]
+ * (any alignment). */
+int svdq_fp8_quantize_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t* ascale, void* stream);
+
+/* DEVICE: the product with an epilogue (epi NULL: none) of svdq_*_epi's kind.
+ * The order of the fp32 sums depends only on the shape and the device's CU
+ * count.  Workspace: 16-byte aligned, >= svdq_fp8_gemm_workspace_size(b, n, m)
+ * bytes (0 where no tile is split), one for each of the calls that overlap in
+ * time. */
+size_t svdq_fp8_gemm_workspace_size(int b, int n, int m);
+int svdq_fp8_gemm(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer* layer, const svdq_epilogue* epi, int b,
+                  void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* DEVICE: the whole layer, quantization and product.  x may be y (and the
+ * residual).  Workspace: 256-byte aligned, >= svdq_fp8_linear_workspace_size
+ * bytes. */
+size_t svdq_fp8_linear_workspace_size(int b, int m, int n);
+int svdq_fp8_linear(const uint16_t* x, const svdq_fp8_layer* layer, const svdq_epilogue* epi, int b, void* y,
+                    int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* DEVICE: the product of b rows sorted by expert (offsets as in the INT4 layers
+ * grouped by expert above, with the same guarantees) with their experts' layers
+ * and the activation of an epilogue (its gate and residual must be NULL).
+ *   qx [G][x_rows][128], ascale [G][x_rows]: the codes of svdq_fp8_quantize_act,
+ *   which are the same for every expert, so that each token is quantized once;
+ *   row i of the product is row row_index[i] of them (NULL: row i, x_rows >= b;
+ *   an index outside [0, x_rows) stands for a row of zeros).
+ * Rows without an expert are not written.  No workspace. */
+int svdq_fp8_grouped_gemm(const uint8_t* qx, const uint8_t* ascale, int x_rows, const int32_t* row_index,
+                          const int32_t* offsets, const svdq_fp8_grouped_layer* layer, const svdq_epilogue* epi, int b,
+                          void* y, int y_dtype, void* stream);
+
+/* DEVICE: x's x_rows rows quantized, then the product above.  x may be y.
+ * Workspace: 256-byte aligned, >= svdq_fp8_grouped_linear_workspace_size bytes,
+ * not shared by calls that overlap in time. */
+size_t svdq_fp8_grouped_linear_workspace_size(int b, int x_rows, int experts, int m, int n);
+int svdq_fp8_grouped_linear(const uint16_t* x, int x_rows, const int32_t* row_index, const int32_t* offsets,
+                            const svdq_fp8_grouped_layer* layer, const svdq_epilogue* epi, int b, void* y, int y_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

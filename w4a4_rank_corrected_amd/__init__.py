@@ -21,7 +21,11 @@ from ._binding import (  # noqa: F401
     svdq_w8a8_gemm_lowrank_up_epi, svdq_fp4_gemm_lowrank_up_epi, svdq_linear_epi_workspace_size, svdq_linear_epi,
     svdq_w8a8_linear_epi, svdq_fp4_linear_epi_workspace_size, svdq_fp4_linear_epi, GroupedDeviceLayer, svdq_grouped_quantize_act_lowrank_down,
     svdq_grouped_gemm_w4a4_lowrank_up, svdq_grouped_linear_workspace_size, svdq_grouped_linear,
-    svdq_combine_rows)
+    svdq_combine_rows,
+    svdq_sort_rows_workspace_size, svdq_sort_rows, svdq_dispatch_rows, svdq_combine_rows_grad, SVDQ_FP8_BLOCK,
+    DeviceLayerFp8, GroupedDeviceLayerFp8, svdq_fp8_quantize_weights, svdq_fp8_quantize_act,
+    svdq_fp8_gemm_workspace_size, svdq_fp8_gemm, svdq_fp8_linear_workspace_size, svdq_fp8_linear,
+    svdq_fp8_grouped_gemm, svdq_fp8_grouped_linear_workspace_size, svdq_fp8_grouped_linear)
 
 __all__ = [
     "SVDQ_GROUP", "SVDQ_MAX_RANK", "SVDQ_OUT_BF16", "SVDQ_OUT_F32", "SvdqError", "DeviceLayer",
@@ -42,4 +46,9 @@ __all__ = [
     "svdq_linear_epi", "svdq_w8a8_linear_epi", "svdq_fp4_linear_epi_workspace_size", "svdq_fp4_linear_epi", "GroupedDeviceLayer", "svdq_grouped_quantize_act_lowrank_down",
     "svdq_grouped_gemm_w4a4_lowrank_up", "svdq_grouped_linear_workspace_size", "svdq_grouped_linear",
     "svdq_combine_rows",
+    "svdq_sort_rows_workspace_size", "svdq_sort_rows", "svdq_dispatch_rows", "svdq_combine_rows_grad",
+    "SVDQ_FP8_BLOCK", "DeviceLayerFp8", "GroupedDeviceLayerFp8", "svdq_fp8_quantize_weights",
+    "svdq_fp8_quantize_act", "svdq_fp8_gemm_workspace_size", "svdq_fp8_gemm",
+    "svdq_fp8_linear_workspace_size", "svdq_fp8_linear", "svdq_fp8_grouped_gemm",
+    "svdq_fp8_grouped_linear_workspace_size", "svdq_fp8_grouped_linear",
 ]

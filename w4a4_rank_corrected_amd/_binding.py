@@ -29,6 +29,7 @@ SVDQ_MAX_RANK = 256
 SVDQ_MAX_DIM = 1 << 22
 SVDQ_W8A8_MAX_M = 131072
 SVDQ_MAX_EXPERTS = 1024
+SVDQ_FP8_BLOCK = 128
 ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "gelu_erf": 2, "silu": 3, "relu": 4}  # SVDQ_ACT_*
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsvdq.so")
@@ -76,6 +77,17 @@ class svdq_grouped_layer(ctypes.Structure):
     _fields_ = [("experts", ctypes.c_int32), ("m", ctypes.c_int32), ("n", ctypes.c_int32), ("rank", ctypes.c_int32),
                 ("group", ctypes.c_int32), ("smooth_inv", _vp), ("qw", _vp), ("wscale", _vp), ("l1", _vp),
                 ("l2", _vp), ("bias", _vp)]
+
+
+class svdq_fp8_layer(ctypes.Structure):
+    """Mirror of ``struct svdq_fp8_layer`` (all pointers are device addresses)."""
+    _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("qw", _vp), ("wscale", _vp), ("bias", _vp)]
+
+
+class svdq_fp8_grouped_layer(ctypes.Structure):
+    """Mirror of ``struct svdq_fp8_grouped_layer`` (all pointers are device addresses)."""
+    _fields_ = [("experts", ctypes.c_int32), ("m", ctypes.c_int32), ("n", ctypes.c_int32), ("qw", _vp), ("wscale", _vp),
+                ("bias", _vp)]
 
 
 # (name, restype, argtypes) for every exported symbol of include/svdq.h
@@ -160,6 +172,26 @@ SIGNATURES = [
       _vp, _size, _vp]),
     ("svdq_combine_rows", _c_int,
      [_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp]),
+    ("svdq_sort_rows_workspace_size", _size, [_c_int, _c_int, _c_int]),
+    ("svdq_sort_rows", _c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _size, _vp]),
+    ("svdq_dispatch_rows", _c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp]),
+    ("svdq_combine_rows_grad", _c_int,
+     [_vp, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_int, _vp, _vp, _vp]),
+    ("svdq_fp8_quantize_weights", _c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    ("svdq_fp8_quantize_act", _c_int, [_vp, _c_int, _c_int, _vp, _vp, _vp]),
+    ("svdq_fp8_gemm_workspace_size", _size, [_c_int, _c_int, _c_int]),
+    ("svdq_fp8_gemm", _c_int,
+     [_vp, _vp, ctypes.POINTER(svdq_fp8_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size, _vp]),
+    ("svdq_fp8_linear_workspace_size", _size, [_c_int, _c_int, _c_int]),
+    ("svdq_fp8_linear", _c_int,
+     [_vp, ctypes.POINTER(svdq_fp8_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int, _vp, _size, _vp]),
+    ("svdq_fp8_grouped_gemm", _c_int,
+     [_vp, _vp, _c_int, _vp, _vp, ctypes.POINTER(svdq_fp8_grouped_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp,
+      _c_int, _vp]),
+    ("svdq_fp8_grouped_linear_workspace_size", _size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    ("svdq_fp8_grouped_linear", _c_int,
+     [_vp, _c_int, _vp, _vp, ctypes.POINTER(svdq_fp8_grouped_layer), ctypes.POINTER(svdq_epilogue), _c_int, _vp, _c_int,
+      _vp, _size, _vp]),
 ]
 
 _lib = None
@@ -1224,4 +1256,316 @@ def svdq_combine_rows(rows, index, weight=None, residual=None, out_dtype=None, y
         _dev(y, "y", rows.dtype, (t, n), dev)
         _check(lib().svdq_combine_rows(_ptr(rows), R, n, _out_code(rows.dtype), _ptr(index), _ptr(weight), t, k,
                                        _ptr(residual), _ptr(y), handle))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# the routing of rows to experts
+# ---------------------------------------------------------------------------
+
+def svdq_sort_rows_workspace_size(t: int, k: int, experts: int) -> int:
+    return int(lib().svdq_sort_rows_workspace_size(t, k, experts))
+
+
+def svdq_sort_rows(expert, experts: int, offsets=None, row_index=None, index=None, workspace=None, stream=None):
+    """The slots of a router's choice (expert int32 [t][k]; outside [0, experts):
+    a dropped slot) in the order of their experts.  Returns (offsets int32
+    [experts + 1], row_index int32 [t k]: each row's token, index int32 [t][k]:
+    each slot's row r, -1 - r of a dropped one), what svdq_grouped_linear and
+    svdq_combine_rows take."""
+    import torch
+    _dev(expert, "expert", torch.int32)
+    if expert is None or expert.dim() != 2:
+        raise ValueError("expert must be 2-D [t][k]")
+    if not 1 <= experts <= SVDQ_MAX_EXPERTS:
+        raise ValueError(f"experts must be in [1, {SVDQ_MAX_EXPERTS}], got {experts}")
+    dev, (t, k) = expert.device, expert.shape
+    with _On(dev, stream) as handle:
+        if offsets is None:
+            offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+        if row_index is None:
+            row_index = torch.empty(t * k, dtype=torch.int32, device=dev)
+        if index is None:
+            index = torch.empty((t, k), dtype=torch.int32, device=dev)
+        _dev(offsets, "offsets", torch.int32, (experts + 1,), dev)
+        _dev(row_index, "row_index", torch.int32, (t * k,), dev)
+        _dev(index, "index", torch.int32, (t, k), dev)
+        need = svdq_sort_rows_workspace_size(t, k, experts) if workspace is None else 0
+        workspace, wsb = _workspace(workspace, need, dev)
+        _check(lib().svdq_sort_rows(_ptr(expert), t, k, experts, _ptr(offsets), _ptr(row_index), _ptr(index),
+                                    workspace.data_ptr(), wsb, handle))
+    return offsets, row_index, index
+
+
+def _scatter_operands(x, name, index, weight):
+    """Checks [t][n] rows of bf16 or fp32 with their index [t][k] and weight; returns (t, n, k)."""
+    import torch
+    _dev(x, name)
+    if x is None or x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be a bf16 or fp32 matrix [t][n]")
+    _dev(index, "index", torch.int32, None, x.device)
+    if index is None or index.dim() != 2 or index.shape[0] != x.shape[0]:
+        raise ValueError(f"index must be [t][k] with t = {x.shape[0]}")
+    _dev(weight, "weight", torch.float32, tuple(index.shape), x.device)
+    return x.shape[0], x.shape[1], index.shape[1]
+
+
+def svdq_dispatch_rows(x, index, weight=None, rows=None, stream=None):
+    """rows[index[t, q]] = weight[t, q] x[t] (weight None: copies), index int32
+    [t][k] as svdq_sort_rows gives it: a dropped slot's row (-1 - index) becomes
+    zero.  rows: [R][n] of x's dtype; allocated here, it has t k rows."""
+    import torch
+    t, n, k = _scatter_operands(x, "x", index, weight)
+    dev = x.device
+    with _On(dev, stream) as handle:
+        if rows is None:
+            rows = torch.empty((t * k, n), dtype=x.dtype, device=dev)
+        if rows.dim() != 2:
+            raise ValueError("rows must be 2-D [R][n]")
+        _dev(rows, "rows", x.dtype, (rows.shape[0], n), dev)
+        _check(lib().svdq_dispatch_rows(_ptr(x), t, n, _out_code(x.dtype), _ptr(index), _ptr(weight), k, rows.shape[0],
+                                        _ptr(rows), handle))
+    return rows
+
+
+def svdq_combine_rows_grad(dy, index, weight=None, rows=None, drows=None, dweight=None, stream=None):
+    """The gradient of svdq_combine_rows(rows, index, weight): (drows, dweight) with
+    drows[index[t, q]] = weight[t, q] dy[t] and dweight[t, q] = dy[t] . rows[index[t, q]]
+    (0 for a dropped slot).  The residual's gradient is dy.
+
+    rows: [R][n] of dy's dtype; without it only drows (t k rows, unless given) is
+    computed and dweight is None.  index: each row named once at the most, as
+    svdq_sort_rows gives it."""
+    import torch
+    t, n, k = _scatter_operands(dy, "dy", index, weight)
+    dev = dy.device
+    for name, v in (("rows", rows), ("drows", drows)):
+        if v is not None and v.dim() != 2:
+            raise ValueError(f"{name} must be 2-D [R][n]")
+    R = rows.shape[0] if rows is not None else drows.shape[0] if drows is not None else t * k
+    if dweight is not None and rows is None:
+        raise ValueError("dweight needs rows")
+    with _On(dev, stream) as handle:
+        if drows is None:
+            drows = torch.empty((R, n), dtype=dy.dtype, device=dev)
+        if dweight is None and rows is not None:
+            dweight = torch.empty((t, k), dtype=torch.float32, device=dev)
+        _dev(rows, "rows", dy.dtype, (R, n), dev)
+        _dev(drows, "drows", dy.dtype, (R, n), dev)
+        _dev(dweight, "dweight", torch.float32, (t, k), dev)
+        _check(lib().svdq_combine_rows_grad(_ptr(dy), t, n, _out_code(dy.dtype), _ptr(index), _ptr(weight), k,
+                                            _ptr(rows), R, _ptr(drows), _ptr(dweight), handle))
+    return drows, dweight
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit floating-point setting: E4M3 codes, a power-of-two scale for each block of 128
+# ---------------------------------------------------------------------------
+
+def _fp8_blocks(d: int) -> int:
+    return -(-d // SVDQ_FP8_BLOCK)
+
+
+def svdq_fp8_quantize_weights(w, transposed: bool = False, qw=None, wscale=None, stream=None):
+    """(qw uint8 [G][n][128], wscale uint8 [G][ceil(n / 128)]), G = ceil(m / 128), of
+    w [m][n] (transposed: [n][m], as torch's Linear holds it), bf16 or fp32; with a
+    leading expert dimension where w has one."""
+    import torch
+    _dev(w, "w")
+    if w is None or w.dim() not in (2, 3) or w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("w must be a bf16 or fp32 tensor [m][n] or [experts][m][n]")
+    if w.numel() == 0:
+        raise ValueError(f"w is empty: {tuple(w.shape)}")
+    lead = tuple(w.shape[:-2])
+    m, n = (w.shape[-1], w.shape[-2]) if transposed else (w.shape[-2], w.shape[-1])
+    dev, G = w.device, _fp8_blocks(m)
+    with _On(dev, stream) as handle:
+        if qw is None:
+            qw = torch.empty(lead + (G, n, SVDQ_FP8_BLOCK), dtype=torch.uint8, device=dev)
+        if wscale is None:
+            wscale = torch.empty(lead + (G, _fp8_blocks(n)), dtype=torch.uint8, device=dev)
+        _dev(qw, "qw", torch.uint8, lead + (G, n, SVDQ_FP8_BLOCK), dev)
+        _dev(wscale, "wscale", torch.uint8, lead + (G, _fp8_blocks(n)), dev)
+        _check(lib().svdq_fp8_quantize_weights(_ptr(w), _out_code(w.dtype), lead[0] if lead else 1, m, n, int(transposed),
+                                               _ptr(qw), _ptr(wscale), handle))
+    return qw, wscale
+
+
+class DeviceLayerFp8:
+    """A layer of the 8-bit floating-point setting in device memory: w (a GPU tensor
+    [m][n], transposed: [n][m]) quantized on the current stream, bias bf16 [n] or
+    None, plus its ``svdq_fp8_layer`` struct."""
+
+    def __init__(self, w, bias=None, transposed: bool = False):
+        if w.dim() != 2:
+            raise ValueError(f"w must be 2-D, got shape {tuple(w.shape)}")
+        m, n = (w.shape[1], w.shape[0]) if transposed else (w.shape[0], w.shape[1])
+        self._init(m, n, *svdq_fp8_quantize_weights(w, transposed), bias)
+
+    def _init(self, m, n, qw, wscale, bias):
+        import torch
+        dev, G = qw.device, _fp8_blocks(m)
+        _dev(qw, "qw", torch.uint8, (G, n, SVDQ_FP8_BLOCK), dev)
+        _dev(wscale, "wscale", torch.uint8, (G, _fp8_blocks(n)), dev)
+        _dev(bias, "bias", torch.bfloat16, (n,), dev)
+        self.m, self.n, self.qw, self.wscale, self.bias = m, n, qw, wscale, bias
+        self.struct = svdq_fp8_layer(m, n, _ptr(qw), _ptr(wscale), _ptr(bias))
+
+    @classmethod
+    def from_tensors(cls, m, n, qw, wscale, bias=None):
+        self = cls.__new__(cls)
+        self._init(m, n, qw, wscale, bias)
+        return self
+
+
+class GroupedDeviceLayerFp8:
+    """One layer per expert: w [experts][m][n] (transposed: [experts][n][m]), bias
+    bf16 [experts][n] or None."""
+
+    def __init__(self, w, bias=None, transposed: bool = False):
+        if w.dim() != 3:
+            raise ValueError(f"w must be 3-D, got shape {tuple(w.shape)}")
+        m, n = (w.shape[2], w.shape[1]) if transposed else (w.shape[1], w.shape[2])
+        self._init(w.shape[0], m, n, *svdq_fp8_quantize_weights(w, transposed), bias)
+
+    def _init(self, experts, m, n, qw, wscale, bias):
+        import torch
+        dev, G = qw.device, _fp8_blocks(m)
+        _dev(qw, "qw", torch.uint8, (experts, G, n, SVDQ_FP8_BLOCK), dev)
+        _dev(wscale, "wscale", torch.uint8, (experts, G, _fp8_blocks(n)), dev)
+        _dev(bias, "bias", torch.bfloat16, (experts, n), dev)
+        self.experts, self.m, self.n = experts, m, n
+        self.qw, self.wscale, self.bias = qw, wscale, bias
+        self.struct = svdq_fp8_grouped_layer(experts, m, n, _ptr(qw), _ptr(wscale), _ptr(bias))
+
+    @classmethod
+    def from_tensors(cls, experts, m, n, qw, wscale, bias=None):
+        self = cls.__new__(cls)
+        self._init(experts, m, n, qw, wscale, bias)
+        return self
+
+
+def svdq_fp8_quantize_act(x, qx=None, ascale=None, stream=None):
+    """(qx uint8 [G][b][128], ascale uint8 [G][b]) of x bf16 [b][m]."""
+    import torch
+    b, m = _input(x)
+    dev, G = x.device, _fp8_blocks(m)
+    with _On(dev, stream) as handle:
+        if qx is None:
+            qx = torch.empty((G, b, SVDQ_FP8_BLOCK), dtype=torch.uint8, device=dev)
+        if ascale is None:
+            ascale = torch.empty((G, b), dtype=torch.uint8, device=dev)
+        _dev(qx, "qx", torch.uint8, (G, b, SVDQ_FP8_BLOCK), dev)
+        _dev(ascale, "ascale", torch.uint8, (G, b), dev)
+        _check(lib().svdq_fp8_quantize_act(_ptr(x), b, m, _ptr(qx), _ptr(ascale), handle))
+    return qx, ascale
+
+
+def _fp8_operands(qx, ascale, layer):
+    """Checks a product's activation operands; returns their rows."""
+    import torch
+    G, dev = _fp8_blocks(layer.m), layer.qw.device
+    if qx is None or qx.dim() != 3:
+        raise ValueError("qx must be 3-D [G][b][128]")
+    b = qx.shape[1]
+    _dev(qx, "qx", torch.uint8, (G, b, SVDQ_FP8_BLOCK), dev)
+    if ascale is None:
+        raise ValueError("ascale must not be None")
+    _dev(ascale, "ascale", torch.uint8, (G, b), dev)
+    return b
+
+
+def svdq_fp8_gemm_workspace_size(b: int, n: int, m: int) -> int:
+    return int(lib().svdq_fp8_gemm_workspace_size(b, n, m))
+
+
+def svdq_fp8_gemm(qx, ascale, layer: DeviceLayerFp8, act: str = "none", act_begin: int = 0, gate=None,
+                  gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None, stream=None):
+    """The product of svdq_fp8_quantize_act's codes with a layer, with the epilogue
+    of svdq_gemm_w4a4_lowrank_up_epi."""
+    b, device, n = _fp8_operands(qx, ascale, layer), qx.device, layer.n
+    with _On(device, stream) as handle:
+        y, code, epi = _epilogue(b, n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
+        need = svdq_fp8_gemm_workspace_size(b, n, layer.m) if workspace is None else 0
+        workspace, wsb = _workspace(workspace, need, device)
+        _check(lib().svdq_fp8_gemm(_ptr(qx), _ptr(ascale), ctypes.byref(layer.struct), ctypes.byref(epi), b,
+                                   y.data_ptr(), code, workspace.data_ptr(), wsb, handle))
+    return y
+
+
+def svdq_fp8_linear_workspace_size(b: int, m: int, n: int) -> int:
+    return int(lib().svdq_fp8_linear_workspace_size(b, m, n))
+
+
+def svdq_fp8_linear(x, layer: DeviceLayerFp8, act: str = "none", act_begin: int = 0, gate=None,
+                    gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None, stream=None):
+    """y = residual + gate * act(x W + bias) of a layer in 8-bit floating point (the
+    arguments of svdq_linear_epi; workspace: svdq_fp8_linear_workspace_size bytes)."""
+    b, m = _input(x)
+    device = layer.qw.device
+    _dev(x, "x", device=device)
+    if m != layer.m:
+        raise ValueError(f"x has {m} channels, the layer {layer.m}")
+    with _On(device, stream) as handle:
+        y, code, epi = _epilogue(b, layer.n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
+        need = svdq_fp8_linear_workspace_size(b, m, layer.n) if workspace is None else 0
+        workspace, wsb = _workspace(workspace, need, device)
+        _check(lib().svdq_fp8_linear(x.data_ptr(), ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code,
+                                     workspace.data_ptr(), wsb, handle))
+    return y
+
+
+def svdq_fp8_grouped_gemm(qx, ascale, offsets, layer: GroupedDeviceLayerFp8, row_index=None, act: str = "none",
+                          act_begin: int = 0, out_dtype=None, y=None, stream=None):
+    """The product of rows sorted by expert with their experts' layers: row i takes
+    row row_index[i] (None: i) of the codes, which svdq_fp8_quantize_act made of the
+    tokens.  Rows without an expert are not written."""
+    import torch
+    x_rows, dev = _fp8_operands(qx, ascale, layer), qx.device
+    b = _fp8_rows(offsets, layer, row_index, x_rows, dev)
+    with _On(dev, stream) as handle:
+        y, code, epi = _epilogue(b, layer.n, dev, y, out_dtype, act, act_begin)
+        _check(lib().svdq_fp8_grouped_gemm(_ptr(qx), _ptr(ascale), x_rows, _ptr(row_index), _ptr(offsets),
+                                           ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code, handle))
+    return y
+
+
+def _fp8_rows(offsets, layer, row_index, x_rows, device):
+    """The rows of a grouped product."""
+    import torch
+    if offsets is None:
+        raise ValueError("offsets must not be None")
+    _dev(offsets, "offsets", torch.int32, (layer.experts + 1,), device)
+    if row_index is None:
+        return x_rows
+    if row_index.dim() != 1:
+        raise ValueError(f"row_index must be 1-D, got shape {tuple(row_index.shape)}")
+    _dev(row_index, "row_index", torch.int32, None, device)
+    return row_index.shape[0]
+
+
+def svdq_fp8_grouped_linear_workspace_size(b: int, x_rows: int, experts: int, m: int, n: int) -> int:
+    return int(lib().svdq_fp8_grouped_linear_workspace_size(b, x_rows, experts, m, n))
+
+
+def svdq_fp8_grouped_linear(x, offsets, layer: GroupedDeviceLayerFp8, row_index=None, act: str = "none",
+                            act_begin: int = 0, out_dtype=None, y=None, workspace=None, stream=None):
+    """svdq_grouped_linear in the 8-bit floating-point setting: act(x[row_index[i]]
+    W_e + bias_e) for row i of expert e; the rows without an expert are not
+    written."""
+    x_rows, m = _input(x)
+    dev = layer.qw.device
+    _dev(x, "x", device=dev)
+    if m != layer.m:
+        raise ValueError(f"x has {m} channels, the layer {layer.m}")
+    b = _fp8_rows(offsets, layer, row_index, x_rows, dev)
+    with _On(dev, stream) as handle:
+        y, code, epi = _epilogue(b, layer.n, dev, y, out_dtype, act, act_begin)
+        need = 0
+        if workspace is None:
+            need = svdq_fp8_grouped_linear_workspace_size(b, x_rows, layer.experts, m, layer.n)
+        workspace, wsb = _workspace(workspace, need, dev)
+        _check(lib().svdq_fp8_grouped_linear(x.data_ptr(), x_rows, _ptr(row_index), _ptr(offsets),
+                                             ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code,
+                                             workspace.data_ptr(), wsb, handle))
     return y

@@ -1,5 +1,5 @@
 // Argument checks and workspace layouts shared by the C-ABI sources (defined in
-// api.cpp).  A check returns an svdq_status and sets the thread's message.
+// api.cpp unless stated).  A check returns an svdq_status and sets the thread's message.
 #pragma once
 
 #include <cstddef>
@@ -12,6 +12,10 @@ namespace svdq {
 constexpr size_t kAlign = 256;
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+inline bool element_aligned(const void* p, int dtype) {
+  return ((uintptr_t)p & (dtype == SVDQ_OUT_F32 ? 3u : 1u)) == 0;
+}
 
 #define REQUIRE(cond, code, ...)  \
   do {                            \
@@ -32,6 +36,10 @@ int check_layer_fp4(const svdq_fp4_layer* L);
 int check_y(void* y, int y_dtype, int b);
 int check_linear(const uint16_t* x, const svdq_layer* layer, int b, void* y, int y_dtype, bool* done);
 int hip_status(int err, const char* what);
+// (defined in epi_api.cpp; check_epilogue fills the kernels' arguments for an output of b x n)
+int check_epilogue(const svdq_epilogue* epi, int b, int n, void* y, int y_dtype, EpiArgs* out);
+int check_rows(int b);
+int check_workspace(const void* ws, size_t have, size_t need, uintptr_t align);
 
 size_t gemm_ws_bytes(int b, int n, int m);
 LinearWorkspace linear_ws_layout(int b, int m, int n, int rank);

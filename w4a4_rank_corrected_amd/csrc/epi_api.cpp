@@ -10,10 +10,6 @@ using namespace svdq;
 
 namespace {
 
-bool element_aligned(const void* p, int dtype) {
-  return ((uintptr_t)p & (dtype == SVDQ_OUT_F32 ? 3u : 1u)) == 0;
-}
-
 // Whether two row-major matrices of `rows` rows of n elements share an element
 // (a, b: addresses; lda, ldb: row strides; size: bytes per element).
 bool overlap(const void* a, int lda, const void* b, int ldb, int rows, int n, int size) {
@@ -25,6 +21,10 @@ bool overlap(const void* a, int lda, const void* b, int ldb, int rows, int n, in
   const uintptr_t row = (uintptr_t)lda * size, off = (pa > pb ? pa - pb : pb - pa) % row, width = (uintptr_t)n * size;
   return off < width || row - off < width;
 }
+
+}  // namespace
+
+namespace svdq {
 
 // Checks an epilogue for an output of b x n and fills the kernels' arguments.
 int check_epilogue(const svdq_epilogue* epi, int b, int n, void* y, int y_dtype, EpiArgs* out) {
@@ -68,6 +68,10 @@ int check_workspace(const void* ws, size_t have, size_t need, uintptr_t align) {
   REQUIRE(((uintptr_t)ws & (align - 1)) == 0, SVDQ_ERR_ALIGNMENT, "workspace must be %zu-byte aligned", (size_t)align);
   return SVDQ_OK;
 }
+
+}  // namespace svdq
+
+namespace {
 
 // The product's activation-side operands.
 int check_operands(const void* qx, const void* ascale, const float* z, int rank, uintptr_t scale_align) {

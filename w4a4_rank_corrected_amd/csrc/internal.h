@@ -237,6 +237,51 @@ int launch_grouped_act(const uint16_t* x, int x_rows, const int32_t* row_index, 
                        const svdq_grouped_layer& L, int b, uint8_t* qx, uint16_t* ascale, float* z, void* stream);
 int launch_combine(const void* rows, int R, int n, int dtype, const int32_t* index, const float* weight, int t, int k,
                    const void* residual, void* y, void* stream);
+
+// ---- the routing of rows to experts ----------------------------------------------
+// The sort's chunks of slots, one per workgroup (a multiple of its threads each).
+constexpr int kSortThreads = 512;
+struct SortPlan {
+  int chunk, chunks;
+};
+SortPlan sort_plan(int b);
+int launch_sort_rows(const int32_t* expert, int b, int k, int experts, int32_t* offsets, int32_t* row_index,
+                     int32_t* index, void* ws, void* stream);
+// drows NULL: the weights' gradient only; dweight NULL: the rows only.
+int launch_scatter_rows(const void* x, int t, int n, int dtype, const int32_t* index, const float* weight, int k,
+                        const void* rows, int R, void* drows, float* dweight, void* stream);
+
+// ---- the 8-bit floating-point setting --------------------------------------------
+constexpr int fp8_blocks(int d) { return (d + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK; }
+// Workgroups of the activation kernel: 16 rows and kFp8ActBlocks blocks of each.
+constexpr int kFp8ActBlocks = 4;
+constexpr long long fp8_act_grid(int b, int m) {
+  return (long long)((b + 15) / 16) * ((fp8_blocks(m) + kFp8ActBlocks - 1) / kFp8ActBlocks);
+}
+// A product of b rows, row i's codes being row row_index[i] (or i) of the x_rows of qx.
+struct Fp8Args {
+  const uint8_t* qx;
+  const uint8_t* ascale;
+  const uint8_t* qw;
+  const uint8_t* wscale;
+  const uint16_t* bias;
+  const int32_t* row_index;
+  int b, x_rows, n, G;
+  Groups groups;  // offsets NULL: one layer
+  EpiArgs ep;
+};
+// The kernel of a product (experts 0: one layer) and its largest launch: the row
+// kernel with rb 16-row blocks a workgroup.
+struct Fp8Plan {
+  int rb, threads;
+  RowsSplit split;
+  size_t ws_bytes;
+};
+Fp8Plan fp8_plan(int b, int n, int m, int experts);
+int launch_fp8_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t* ascale, void* stream);
+int launch_fp8_weights(const void* w, int dtype, int experts, int m, int n, bool transposed, uint8_t* qw,
+                       uint8_t* wscale, void* stream);
+int launch_fp8_gemm(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream);
 // Launcher status (not a hipError_t) of a kernel that would use scratch memory.
 constexpr int kErrKernelScratch = -1000;
 

@@ -110,4 +110,26 @@ GroupedPlan grouped_plan(int b, int n, int m, int experts) {
   return p;
 }
 
+// The sort of the slots: 8 a thread, more where that would be over 256 chunks
+// (every workgroup reads the counts of all chunks).
+SortPlan sort_plan(int b) {
+  const long long even = ((long long)b + 256LL * kSortThreads - 1) / (256LL * kSortThreads) * kSortThreads;
+  SortPlan p;
+  p.chunk = (int)std::max<long long>(8 * kSortThreads, even);
+  p.chunks = std::max((int)(((long long)b + p.chunk - 1) / p.chunk), 1);
+  return p;
+}
+
+// The 8-bit floating-point product.
+Fp8Plan fp8_plan(int b, int n, int m, int experts) {
+  const int G = fp8_blocks(m);
+  const long long mean = experts > 0 ? (b + experts - 1) / experts : b;
+  Fp8Plan p{mean <= 16 ? 1 : (mean <= 32 ? 2 : 4), 0, {1, 1, 0}, 0};
+  const long long rows = 16 * p.rb;
+  const long long blocks = experts > 0 ? grouped_row_blocks(b, experts, rows) : (b + rows - 1) / rows;
+  p.split = rows_split(blocks, n, 2 * G, p.rb);
+  p.threads = 64 * p.split.nwk * p.split.nwc;
+  return p;
+}
+
 }  // namespace svdq
