@@ -7,6 +7,15 @@ m additions, and the sums of a few pieces and the bias at most 24 more, each off
 by 2 u (additions of the matrix instruction may truncate) of S, the sum of the
 magnitudes:  |dv| <= (m + 24) 2 u S,  which product_values(x, w, m) of epi_ref
 states.
+
+bf16 outputs of many rows (tiles): v_mfma_scale_f32_16x16x128_f8f6f4 adds the
+products of eight neighbouring channels at the exponent of the largest and keeps 13
+bits below it (measured on gfx950: beside a product of 2^16 one of 2^3 survives, one
+of 2^2 does not; sums of such eights keep 23).  A product's exponent is that of its
+factors', and a factor below E4M3's normal numbers counts as 2^-6.  With
+p = max(|x|, 2^(ex-6)) max(|w|, 2^(ew-6)), each of the eight products is off by at
+most 2^-13 of the largest p, so v by at most  8 2^-13 sum_eights max p  more, which
+aligned(...) returns.
 """
 import numpy as np
 
@@ -80,3 +89,22 @@ def records(codes):
     p = np.zeros((R, G * BLOCK), np.uint8)
     p[:, :c] = codes
     return np.ascontiguousarray(p.reshape(R, G, BLOCK).transpose(1, 0, 2))
+
+
+def aligned(xq, wq, w_by=BLOCK):
+    """The additional bound of the 8-bit matrix instruction for quantize()'s results of X [b][m] and W^T [n][m]."""
+    def factor(q, by):
+        codes, es, val = q
+        R, c = val.shape
+        e = np.repeat(np.repeat(es, by, 0)[:R], BLOCK, 1)
+        p = np.zeros(e.shape)
+        p[:, :c] = np.abs(val)
+        return np.maximum(p, 2.0 ** (e - 6.0))
+    x, w = factor(xq, 1), factor(wq, w_by)
+    out = np.zeros((x.shape[0], w.shape[0]))
+    for k in range(0, x.shape[1], 8):
+        top = np.zeros_like(out)
+        for i in range(k, k + 8):
+            np.maximum(top, np.outer(x[:, i], w[:, i]), out=top)
+        out += top
+    return out * 2.0 ** -10

@@ -73,10 +73,13 @@ class Layer:
         else:
             self.layer = S.DeviceLayerFp8(wd[0], None if bd is None else bd[0], transposed=transposed)
 
-    def product(self, x, e=0):
-        """(v, bound) of rows x (bf16 values)."""
-        xv = F.quantize(x, 1)[2]
-        return R.product_values(xv, self.val[e], self.m, bias=None if self.bias is None else self.bias[e])
+    def product(self, x, e=0, tiles=False):
+        """(v, bound) of rows x (bf16 values); tiles: by the 8-bit matrix instruction."""
+        xq = F.quantize(x, 1)
+        v, dv = R.product_values(xq[2], self.val[e], self.m, bias=None if self.bias is None else self.bias[e])
+        if tiles:
+            dv = dv + F.aligned(xq, (self.codes[e], self.es[e], self.val[e]))
+        return v, dv
 
 
 # ---------------------------------------------------------------------------
@@ -203,7 +206,8 @@ def test_transposed_layer_has_the_same_values(S):
 # ---------------------------------------------------------------------------
 
 SHAPES = [(1, 1, 1), (1, 128, 16), (1, 1152, 700), (2, 130, 33), (7, 1000, 513), (16, 256, 128), (17, 384, 130), (33, 700, 64),
-          (64, 2048, 96), (65, 129, 257), (130, 640, 300), (257, 1152, 200), (300, 4200, 72), (512, 300, 520)]
+          (64, 2048, 96), (65, 129, 257), (130, 640, 300), (257, 1152, 200), (300, 4200, 72), (512, 300, 520),
+          (2048, 130, 257), (2300, 400, 513), (2500, 1100, 300)]
 
 
 @pytest.mark.parametrize("b,m,n", SHAPES)
@@ -214,7 +218,7 @@ def test_linear(S, b, m, n, out):
     X = Layer(S, m, n, bias=b % 2 == 1, seed=2)
     x = rows_like(rng, b, m)
     x[b // 2] = 0
-    v, dv = X.product(x)
+    v, dv = X.product(x, tiles=out == "bf16" and b > 64)
     act, begin = ACTS[(b + n) % 5], (n // 3 if n % 2 else 0)
     y, bound = R.epilogue(v, dv, act, begin, out=out)
     xd = dev_bf16(x)
@@ -225,7 +229,7 @@ def test_linear(S, b, m, n, out):
     assert torch.equal(got, two)
 
 
-@pytest.mark.parametrize("b", [1, 40, 200])
+@pytest.mark.parametrize("b", [1, 40, 200, 2049])
 @pytest.mark.parametrize("act", ACTS)
 def test_epilogue(S, b, act):
     """Gate, residual and strides, each with an activation; nothing is written between the rows."""
@@ -238,7 +242,7 @@ def test_epilogue(S, b, act):
     for out in ("f32", "bf16"):
         res = rng.standard_normal((b, n))
         res = R.bf16(res) if out == "bf16" else res.astype(np.float32).astype(np.float64)
-        v, dv = X.product(x)
+        v, dv = X.product(x, tiles=out == "bf16" and b > 64)
         y, bound = R.epilogue(v, dv, act, 31, gate=gate, gate_rows=rows, residual=res, out=out)
         wide = torch.full((b, n + 9), 5.0, dtype=dtype_of(out)).cuda()
         wres = torch.full((b, n + 3), 7.0, dtype=dtype_of(out)).cuda()
@@ -291,17 +295,17 @@ def test_unaligned_operands(S, b):
     assert torch.equal(got, got2)
 
 
-@pytest.mark.parametrize("b", [3, 70, 300])
-def test_nonfinite_rows_and_columns_stay_their_own(S, b):
+@pytest.mark.parametrize("b,out", [(3, "f32"), (70, "f32"), (300, "f32"), (70, "bf16"), (300, "bf16"), (2100, "bf16")])
+def test_nonfinite_rows_and_columns_stay_their_own(S, b, out):
     m, n = 640, 300
     rng = np.random.default_rng(b)
     w = torch.from_numpy(rng.standard_normal((n, m)) / 25).bfloat16().cuda()
     x = dev_bf16(rows_like(rng, b, m))
-    want = S.svdq_fp8_linear(x, S.DeviceLayerFp8(w, transposed=True), out_dtype=torch.float32)
+    want = S.svdq_fp8_linear(x, S.DeviceLayerFp8(w, transposed=True), out_dtype=dtype_of(out))
     x2, w2 = x.clone(), w.clone()
     x2[b // 2, 600] = float("inf")
     w2[130, 5] = float("nan")  # columns 128 .. 255
-    got = S.svdq_fp8_linear(x2, S.DeviceLayerFp8(w2, transposed=True), out_dtype=torch.float32)
+    got = S.svdq_fp8_linear(x2, S.DeviceLayerFp8(w2, transposed=True), out_dtype=dtype_of(out))
     bad = torch.zeros(b, n, dtype=torch.bool).cuda()
     bad[b // 2] = True
     bad[:, 128:256] = True
@@ -318,7 +322,8 @@ def test_b0(S):
     assert S.svdq_fp8_gemm(qx, asc, X.layer).shape == (0, 30)
 
 
-def test_extreme_scales(S):
+@pytest.mark.parametrize("rows,out", [(6, "f32"), (100, "f32"), (100, "bf16"), (2100, "bf16")])
+def test_extreme_scales(S, rows, out):
     """Scales far apart within a row and a product near the ends of fp32's range."""
     m, n = 512, 40
     rng = np.random.default_rng(11)
@@ -333,8 +338,12 @@ def test_extreme_scales(S):
     x[3, :128] *= 2.0 ** 100
     x = R.bf16(x)
     lay = S.DeviceLayerFp8(dev_bf16(w), transposed=True)
-    v, dv = R.product_values(F.quantize(x, 1)[2], F.quantize(w, 128)[2], m)
-    close(S.svdq_fp8_linear(dev_bf16(x), lay, out_dtype=torch.float32), *R.epilogue(v, dv))
+    x = np.tile(x, (-(-rows // 6), 1))[:rows]
+    xq, wq = F.quantize(x, 1), F.quantize(w, 128)
+    v, dv = R.product_values(xq[2], wq[2], m)
+    if out == "bf16":
+        dv = dv + F.aligned(xq, wq)
+    close(S.svdq_fp8_linear(dev_bf16(x), lay, out_dtype=dtype_of(out)), *R.epilogue(v, dv, out=out))
 
 
 # ---------------------------------------------------------------------------
@@ -376,7 +385,7 @@ def test_grouped(S, E, b, m, n, pad, gather, out):
         if off[e] == off[e + 1]:
             continue
         live[s] = True
-        v, dv = X.product(gone[s], e)
+        v, dv = X.product(gone[s], e, tiles=out == "bf16" and b > 64 * E)
         y, bound = R.epilogue(v, dv, act, begin, out=out)
         close(got[s], y, bound, e)
     assert (got[torch.from_numpy(~live).cuda()] == 99).all()
@@ -412,7 +421,7 @@ def test_offsets_of_any_content(S, b):
 def test_same_inputs_same_bits_and_side_stream(S):
     X = Layer(S, 1152, 640, seed=10)
     side = torch.cuda.Stream()
-    for b in (1, 48, 260):
+    for b in (1, 48, 260, 2200):
         x = dev_bf16(rows_like(np.random.default_rng(b), b, 1152))
         want = S.svdq_fp8_linear(x, X.layer, act="gelu_tanh")
         torch.cuda.synchronize()

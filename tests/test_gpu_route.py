@@ -231,10 +231,19 @@ class Net:
         rng = np.random.default_rng(seed)
         self.E, self.m, self.h, self.S = E, m, hidden, S
         w1, w2 = R.bf16(rng.standard_normal((E, hidden, m)) / np.sqrt(m)), R.bf16(rng.standard_normal((E, m, hidden)) / np.sqrt(hidden))
-        self.v1, self.v2 = ([F.quantize(v, 128)[2] for v in w] for w in (w1, w2))
+        self.q1, self.q2 = ([F.quantize(v, 128) for v in w] for w in (w1, w2))
         d1, d2 = dev_bf16(w1), dev_bf16(w2)
         self.fc1, self.fc2 = (S.GroupedDeviceLayerFp8(d, transposed=True) for d in (d1, d2))
         self.bc1, self.bc2 = (S.GroupedDeviceLayerFp8(d) for d in (d1, d2))  # of the transposes
+
+    @staticmethod
+    def layer(x, q, transpose=False, tiles=False):
+        """(v, bound) of rows x through a layer's quantize() result (or its transpose's)."""
+        xq = F.quantize(x, 1)
+        if transpose:
+            q = tuple(a.T for a in q)
+        v, dv = R.product_values(xq[2], q[2], x.shape[1])
+        return v, dv + F.aligned(xq, q) if tiles else dv
 
     def forward(self, x, ids, gate):
         S = self.S
@@ -265,6 +274,7 @@ def test_experts_forwards_and_backwards(S, t, k, E, m, hidden):
     x, gate = R.bf16(rng.standard_normal((t, m))), rng.random((t, k)).astype(np.float32)
     dy = R.bf16(rng.standard_normal((t, m)))
     gd = torch.from_numpy(gate).cuda()
+    tiles = t * k > 64 * E
     y, saved = net.forward(dev_bf16(x), torch.from_numpy(ids.astype(np.int32)).cuda(), gd)
     dx, dgate = net.backward(dev_bf16(dy), gd, saved)
     off, row, index = sorted_slots(ids, E)
@@ -274,9 +284,9 @@ def test_experts_forwards_and_backwards(S, t, k, E, m, hidden):
         s = slice(off[e], off[e + 1])
         if off[e] == off[e + 1]:
             continue
-        yv, b = R.epilogue(*R.product_values(F.quantize(x[row[s]], 1)[2], net.v1[e], m), "relu", out="bf16")
+        yv, b = R.epilogue(*net.layer(x[row[s]], net.q1[e], tiles=tiles), "relu", out="bf16")
         assert (np.abs(mid[s] - yv) <= b).all()
-        yv, b = R.epilogue(*R.product_values(F.quantize(mid[s], 1)[2], net.v2[e], hidden), out="bf16")
+        yv, b = R.epilogue(*net.layer(mid[s], net.q2[e], tiles=tiles), out="bf16")
         assert (np.abs(rows[s] - yv) <= b).all()
     want = x.copy()
     size = np.abs(x)
@@ -299,11 +309,11 @@ def test_experts_forwards_and_backwards(S, t, k, E, m, hidden):
         s = slice(off[e], off[e + 1])
         if off[e] == off[e + 1]:
             continue
-        dm, bm = R.epilogue(*R.product_values(F.quantize(drows[s], 1)[2], net.v2[e].T, m), out="bf16")
+        dm, bm = R.epilogue(*net.layer(drows[s], net.q2[e], True, tiles), out="bf16")
         got = S.svdq_fp8_grouped_linear(dev_bf16(drows), saved[0], net.bc2, y=torch.zeros_like(saved[3]))
         assert (np.abs(to_np(got)[s] - dm) <= bm).all()
         g = np.where(mid[s] > 0, to_np(got)[s], 0)
-        di, bi = R.epilogue(*R.product_values(F.quantize(g, 1)[2], net.v1[e].T, hidden), out="bf16")
+        di, bi = R.epilogue(*net.layer(g, net.q1[e], True, tiles), out="bf16")
         want_rows = di  # (the token's sum below takes the library's own rounding of these: within bi of them)
         for r in range(off[e], off[e + 1]):
             want[row[r]] += want_rows[r - off[e]]

@@ -13,6 +13,27 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
+// 32 codes of a lane.
+__device__ __forceinline__ i32x8 operand(const u32x4& lo, const u32x4& hi) {
+  return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// acc + A B over 128 channels with the scales' bytes, A's in byte 0 of sa, B's in
+// byte `sel` of sb (a constant once inlined): v_mfma_scale_f32_16x16x128_f8f6f4,
+// both operands E4M3.  The instruction takes a scale for every 32 channels, lane l
+// those of channels 32 (l / 16) .. + 31 of row l % 16; a block of 128 has one, the
+// same in all four.  Any order of the channels serves, being the same in both
+// operands.
+__device__ __forceinline__ f32x4 mfma_scaled(const i32x8& a, const i32x8& b, const f32x4& acc, uint32_t sa, uint32_t sb,
+                                             int sel) {
+  switch (sel) {
+    case 0: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, (int)sa, 0, (int)sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, (int)sa, 1, (int)sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, (int)sa, 2, (int)sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 0, 0, 0, (int)sa, 3, (int)sb);
+  }
+}
+
 // Eight codes times their block's scale (a power of two, as a float) in bf16, which
 // holds them exactly: four significant bits.
 __device__ __forceinline__ bf16x8 decode8(uint32_t lo, uint32_t hi, float scale) {

@@ -1,5 +1,7 @@
 // C-ABI entry points of the 8-bit floating-point setting (declared in
 // include/svdq.h).  Arguments are validated on the host before any HIP call.
+#include <algorithm>
+
 #include "checks.h"
 #include "internal.h"
 
@@ -45,7 +47,7 @@ int check_product(const svdq_fp8_layer* L, const svdq_epilogue* epi, int b, void
   if (st || b == 0) return st;
   st = check_weights(L->qw, L->wscale, L->bias);
   if (st) return st;
-  const Fp8Plan plan = fp8_plan(b, L->n, L->m, 0);
+  const Fp8Plan plan = fp8_plan(b, L->n, L->m, 0, y_dtype);
   REQUIRE(launch_fits(plan.split.grid, plan.threads), SVDQ_ERR_UNSUPPORTED, "too many output tiles (b=%d, n=%d)", b,
           L->n);
   return SVDQ_OK;
@@ -72,10 +74,15 @@ int check_grouped_product(const svdq_fp8_grouped_layer* L, const svdq_epilogue* 
   REQUIRE(x_rows <= SVDQ_MAX_DIM, SVDQ_ERR_UNSUPPORTED, "x_rows must be <= %d (got %d)", SVDQ_MAX_DIM, x_rows);
   st = check_weights(L->qw, L->wscale, L->bias);
   if (st) return st;
-  const Fp8Plan plan = fp8_plan(b, L->n, L->m, L->experts);
+  const Fp8Plan plan = fp8_plan(b, L->n, L->m, L->experts, y_dtype);
   REQUIRE(launch_fits(plan.split.grid, plan.threads), SVDQ_ERR_UNSUPPORTED,
           "too many output tiles (b=%d, n=%d, experts=%d)", b, L->n, L->experts);
   return SVDQ_OK;
+}
+
+// The product's workspace, whatever its output's type.
+size_t fp8_gemm_ws_bytes(int b, int n, int m) {
+  return std::max(fp8_plan(b, n, m, 0, SVDQ_OUT_BF16).ws_bytes, fp8_plan(b, n, m, 0, SVDQ_OUT_F32).ws_bytes);
 }
 
 // Codes, scales and the product's share of a whole layer's workspace.
@@ -133,7 +140,7 @@ int svdq_fp8_quantize_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t*
 
 size_t svdq_fp8_gemm_workspace_size(int b, int n, int m) {
   if (b <= 0 || b > SVDQ_MAX_DIM || n <= 0 || n > SVDQ_MAX_DIM || m <= 0 || m > SVDQ_MAX_DIM) return 0;
-  return fp8_plan(b, n, m, 0).ws_bytes;
+  return fp8_gemm_ws_bytes(b, n, m);
 }
 
 int svdq_fp8_gemm(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer* layer, const svdq_epilogue* epi, int b,
@@ -143,8 +150,8 @@ int svdq_fp8_gemm(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer
   int st = check_product(layer, epi, b, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_codes(qx, ascale);
-  const Fp8Plan plan = fp8_plan(b, layer->n, layer->m, 0);
-  if (!st) st = check_workspace(workspace, workspace_bytes, plan.ws_bytes, 16);
+  const Fp8Plan plan = fp8_plan(b, layer->n, layer->m, 0, y_dtype);
+  if (!st) st = check_workspace(workspace, workspace_bytes, fp8_gemm_ws_bytes(b, layer->n, layer->m), 16);
   if (st) return st;
   return hip_status(launch_fp8_gemm(product_args(qx, ascale, *layer, b, ep), plan, y_dtype, workspace, stream),
                     "fp8_gemm");
@@ -152,7 +159,7 @@ int svdq_fp8_gemm(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer
 
 size_t svdq_fp8_linear_workspace_size(int b, int m, int n) {
   if (b <= 0 || b > SVDQ_MAX_DIM || n <= 0 || n > SVDQ_MAX_DIM || m <= 0 || m > SVDQ_MAX_DIM) return 0;
-  return fp8_ws_layout(b, m, fp8_plan(b, n, m, 0).ws_bytes).total;
+  return fp8_ws_layout(b, m, fp8_gemm_ws_bytes(b, n, m)).total;
 }
 
 int svdq_fp8_linear(const uint16_t* x, const svdq_fp8_layer* layer, const svdq_epilogue* epi, int b, void* y,
@@ -162,8 +169,8 @@ int svdq_fp8_linear(const uint16_t* x, const svdq_fp8_layer* layer, const svdq_e
   int st = check_product(layer, epi, b, y, y_dtype, &ep);
   if (st || b == 0) return st;
   st = check_x(x, b, layer->m);
-  const Fp8Plan plan = fp8_plan(b, layer->n, layer->m, 0);
-  const Fp8Workspace w = fp8_ws_layout(b, layer->m, plan.ws_bytes);
+  const Fp8Plan plan = fp8_plan(b, layer->n, layer->m, 0, y_dtype);
+  const Fp8Workspace w = fp8_ws_layout(b, layer->m, fp8_gemm_ws_bytes(b, layer->n, layer->m));
   if (!st) st = check_workspace(workspace, workspace_bytes, w.total, kAlign);
   if (st) return st;
   uint8_t* ws = (uint8_t*)workspace;
@@ -183,7 +190,7 @@ int svdq_fp8_grouped_gemm(const uint8_t* qx, const uint8_t* ascale, int x_rows, 
   st = check_codes(qx, ascale);
   if (st) return st;
   return hip_status(launch_fp8_gemm(grouped_args(qx, ascale, x_rows, row_index, offsets, *layer, b, ep),
-                                    fp8_plan(b, layer->n, layer->m, layer->experts), y_dtype, nullptr, stream),
+                                    fp8_plan(b, layer->n, layer->m, layer->experts, y_dtype), y_dtype, nullptr, stream),
                     "fp8_grouped_gemm");
 }
 
@@ -209,7 +216,7 @@ int svdq_fp8_grouped_linear(const uint16_t* x, int x_rows, const int32_t* row_in
   st = hip_status(launch_fp8_act(x, x_rows, layer->m, ws, ws + w.as_off, stream), "fp8_quantize_act");
   if (st) return st;
   return hip_status(launch_fp8_gemm(grouped_args(ws, ws + w.as_off, x_rows, row_index, offsets, *layer, b, ep),
-                                    fp8_plan(b, layer->n, layer->m, layer->experts), y_dtype, nullptr, stream),
+                                    fp8_plan(b, layer->n, layer->m, layer->experts, y_dtype), y_dtype, nullptr, stream),
                     "fp8_grouped_gemm");
 }
 

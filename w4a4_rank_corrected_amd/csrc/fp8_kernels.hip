@@ -293,14 +293,18 @@ int launch_fp8_weights(const void* w, int dtype, int experts, int m, int n, bool
   return transposed ? go(fp8_weight_kernel<false, true>) : go(fp8_weight_kernel<false, false>);
 }
 
-int launch_fp8_gemm(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream) {
-  (void)ws;
+int launch_fp8_rows(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   const bool bf = y_dtype == SVDQ_OUT_BF16;
   if (plan.rb == 1) return launch_fp8_rows_rb<1>(a, plan.split, bf, st);
   if (plan.rb == 2) return launch_fp8_rows_rb<2>(a, plan.split, bf, st);
   if (plan.rb == 4) return launch_fp8_rows_rb<4>(a, plan.split, bf, st);
   return (int)hipErrorInvalidValue;
+}
+
+int launch_fp8_gemm(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream) {
+  (void)ws;
+  return plan.rb ? launch_fp8_rows(a, plan, y_dtype, stream) : launch_fp8_tiles(a, plan, y_dtype, stream);
 }
 
 }  // namespace svdq

@@ -271,16 +271,18 @@ struct Fp8Args {
   EpiArgs ep;
 };
 // The kernel of a product (experts 0: one layer) and its largest launch: the row
-// kernel with rb 16-row blocks a workgroup.
+// kernel with rb 16-row blocks a workgroup, or (rb 0) tiles of tile_m rows.
 struct Fp8Plan {
-  int rb, threads;
+  int rb, tile_m, threads;
   RowsSplit split;
   size_t ws_bytes;
 };
-Fp8Plan fp8_plan(int b, int n, int m, int experts);
+Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype);
 int launch_fp8_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t* ascale, void* stream);
 int launch_fp8_weights(const void* w, int dtype, int experts, int m, int n, bool transposed, uint8_t* qw,
                        uint8_t* wscale, void* stream);
+int launch_fp8_rows(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* stream);
+int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* stream);
 int launch_fp8_gemm(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream);
 // Launcher status (not a hipError_t) of a kernel that would use scratch memory.
 constexpr int kErrKernelScratch = -1000;

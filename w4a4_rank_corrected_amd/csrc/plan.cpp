@@ -121,10 +121,18 @@ SortPlan sort_plan(int b) {
 }
 
 // The 8-bit floating-point product.
-Fp8Plan fp8_plan(int b, int n, int m, int experts) {
+Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
   const int G = fp8_blocks(m);
   const long long mean = experts > 0 ? (b + experts - 1) / experts : b;
-  Fp8Plan p{mean <= 16 ? 1 : (mean <= 32 ? 2 : 4), 0, {1, 1, 0}, 0};
+  Fp8Plan p{mean <= 16 ? 1 : (mean <= 32 ? 2 : 4), 0, 0, {1, 1, 0}, 0};
+  if (mean > 64) {
+    p.rb = 0;
+    p.tile_m = experts == 0 && b >= 2048 && y_dtype == SVDQ_OUT_BF16 ? 256 : 128;
+    p.threads = p.tile_m == 256 ? 512 : 256;
+    const long long tr = experts > 0 ? grouped_row_blocks(b, experts, p.tile_m) : (b + p.tile_m - 1) / p.tile_m;
+    p.split.grid = tr * ((n + p.tile_m - 1) / p.tile_m);
+    return p;
+  }
   const long long rows = 16 * p.rb;
   const long long blocks = experts > 0 ? grouped_row_blocks(b, experts, rows) : (b + rows - 1) / rows;
   p.split = rows_split(blocks, n, 2 * G, p.rb);
