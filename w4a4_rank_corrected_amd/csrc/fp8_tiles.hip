@@ -24,8 +24,11 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
 }
 
 // Records in LDS: record r's 16-byte piece p lies at place p ^ key(r), so that the
-// lanes of an operand read, 16 records at the same piece, fall on all 64 banks.
-__device__ __forceinline__ int record_key(int r) { return (r >> 1) & 7; }
+// lanes of an operand read, which want one piece of 16 records, spread over the banks.
+__device__ __forceinline__ int record_key(int r) { return r & 7; }
+
+// s_waitcnt's operand: at most vm loads and lgkm LDS accesses under way.
+constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | 0x70 | lgkm << 8 | (vm >> 4) << 14; }
 
 template <int QB, int NWM, int NWN, bool EXACT, bool OUT_BF16, bool GROUPED>
 __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int tiles_m, int tiles_n) {
@@ -71,23 +74,31 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
     row_end = a.b;
   }
 
-  // what this lane loads: piece (lane & 7) of records 8 (wave + NW i) + lane / 8
-  uint32_t xoff[LX], woff[LW];
+  // What this lane loads: piece (lane & 7) ^ key of records 8 (wave + NW i) + lane / 8.
+  // From load to load i the records are 8 NW further, and so are the rows (unless they
+  // are gathered) and the columns.
+  constexpr uint32_t kNext = 8 * NW * 128;
+  const int rec = 8 * wave + (lane >> 3);
+  const uint32_t piece = 16u * ((lane & 7) ^ record_key(rec));
+  uint32_t xoff[LX];
+  if constexpr (GROUPED) {
 #pragma unroll
-  for (int i = 0; i < LX; ++i) {
-    const int rec = 8 * (wave + NW * i) + (lane >> 3);
-    int s = i0 + rec < row_end ? i0 + rec : -1;
-    if (GROUPED && s >= 0 && a.row_index) s = a.row_index[s];
-    xoff[i] = ((unsigned)s < (unsigned)xr ? (uint32_t)s * 128u : 0x7FFFFF80u) + 16u * ((lane & 7) ^ record_key(rec));
+    for (int i = 0; i < LX; ++i) {
+      int s = i0 + rec + 8 * NW * i;
+      if (s >= row_end) s = -1;
+      if (s >= 0 && a.row_index) s = a.row_index[s];
+      xoff[i] = ((unsigned)s < (unsigned)xr ? (uint32_t)s * 128u : 0x7FFFFF80u) + piece;
+    }
+  } else {
+    xoff[0] = (uint32_t)(i0 + rec) * 128u + piece;  // (rows behind the last are past the resource's end)
   }
-#pragma unroll
-  for (int i = 0; i < LW; ++i) {
-    // record 64 w + 16 f + 4 c + v holds column 64 w + 16 c + 4 f + v: a lane's
-    // results of the four blocks f are then 16 neighbouring columns
-    const int rec = 8 * (wave + NW * i) + (lane >> 3);
-    const int col = j0 + (rec & ~63) + 16 * ((rec >> 2) & 3) + 4 * ((rec >> 4) & 3) + (rec & 3);
-    woff[i] = (uint32_t)col * 128u + 16u * ((lane & 7) ^ record_key(rec));
-  }
+  // bf16: record 64 w + 16 f + 4 c + v holds column 64 w + 32 (f / 2) + 8 c + 4 (f % 2) + v,
+  // so that a lane's results of two blocks f are eight neighbouring columns and four
+  // lanes' are 64 bytes of a row (fp32 has those in the records' own order)
+  static_assert(NW % 4 == 0, "32 records on are 32 columns on");
+  const int rf = rec >> 4 & 3;
+  const int col = OUT_BF16 ? (rec & ~63) + 32 * (rf >> 1) + 8 * (rec >> 2 & 3) + 4 * (rf & 1) + (rec & 3) : rec;
+  const uint32_t woff = (uint32_t)(j0 + col) * 128u + piece;
   // the row whose scale this thread stages, and its place
   uint32_t soff = 0x7FFFFFFFu;
   if (tid < TM && i0 + tid < row_end) {
@@ -97,14 +108,24 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
   }
   const int splace = (tid / (16 * QB)) * 16 * QB + (tid & 15) * QB + (tid >> 4) % QB;
 
-  auto load_codes = [&](int g, uint8_t* to) {  // (past the last step zeros, without memory traffic)
+  struct Source {
+    __amdgpu_buffer_rsrc_t x, w;
+    uint32_t x0, w0;
+  };
+  auto source = [&](int g) {  // (past the last step zeros, without memory traffic)
     const size_t at = g < G ? (size_t)g : 0;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.qx + at * xr * 128, g < G ? (uint32_t)xr * 128u : 0u);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(qw + at * n * 128, g < G ? (uint32_t)n * 128u : 0u);
-#pragma unroll
-    for (int i = 0; i < LX; ++i) load_to_lds(rx, xoff[i], to + 1024 * (wave + NW * i));
-#pragma unroll
-    for (int i = 0; i < LW; ++i) load_to_lds(rw, woff[i], to + TM * 128 + 1024 * (wave + NW * i));
+    Source f{make_rsrc(a.qx + at * xr * 128, g < G ? (uint32_t)xr * 128u : 0u),
+             make_rsrc(qw + at * n * 128, g < G ? (uint32_t)n * 128u : 0u), xoff[0], woff};
+    // (a load's offset is formed where it is issued, by one addition, not kept in a register)
+    asm("" : "+v"(f.x0), "+v"(f.w0));
+    return f;
+  };
+  // load k of a step's LX + LW
+  auto load_codes = [&](const Source& f, uint8_t* to, int k) {
+    if (k < LX)
+      load_to_lds(f.x, GROUPED ? xoff[k] : f.x0 + k * kNext, to + 1024 * (wave + NW * k));
+    else
+      load_to_lds(f.w, f.w0 + (k - LX) * kNext, to + TM * 128 + 1024 * (wave + NW * (k - LX)));
   };
   // (past the last step the last one's, unused)
   auto load_sx = [&](int g) -> uint32_t {
@@ -115,146 +136,167 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
     const __amdgpu_buffer_rsrc_t rw = make_rsrc(wscale + (size_t)min(g, G - 1) * NB, (uint32_t)NB);
     return __builtin_amdgcn_raw_buffer_load_b8(rw, (uint32_t)(j0 + 64 * wn) / 128u, 0, 0);
   };
-  auto read = [&](const uint8_t* records, int rec) -> i32x8 {
-    const uint8_t* p = records + rec * 128;
-    const int key = record_key(rec);
-    return operand(*reinterpret_cast<const u32x4*>(p + 16 * ((2 * c) ^ key)),
-                   *reinterpret_cast<const u32x4*>(p + 16 * ((2 * c + 1) ^ key)));
+  // this lane's pieces 2 c and 2 c + 1 of record r of 16
+  const uint32_t lane_at = r * 128 + 16 * ((2 * c) ^ record_key(r));
+  auto read = [&](const uint8_t* records, uint32_t at) -> i32x8 {
+    return operand(*reinterpret_cast<const u32x4*>(records + at), *reinterpret_cast<const u32x4*>(records + (at ^ 16)));
   };
-  auto read_w = [&](const uint8_t* buf, int f) { return read(buf + TM * 128 + wn * 8192, 16 * f + r); };
-  auto read_x = [&](const uint8_t* buf, int q) { return read(buf + wm * QB * 2048, 16 * q + r); };
+  auto read_w = [&](const uint8_t* buf, int f, uint32_t at) {
+    return read(buf + TM * 128 + wn * 8192 + f * 2048, at);
+  };
+  auto read_x = [&](const uint8_t* buf, int q, uint32_t at) { return read(buf + (wm * QB + q) * 2048, at); };
 
   f32x4 acc[4][QB];
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
     for (int q = 0; q < QB; ++q) acc[f][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-  i32x8 wv[4], xv[QB];
-  uint32_t sx[QB / 4], sw;         // the step's scales: bytes of the rows' four blocks, the columns'
-  uint32_t sx_ahead, sw_ahead;     // in flight: the byte this thread stages, two steps ahead; the columns', one ahead
+  constexpr int R = QB / 2;     // blocks of rows in registers at a time
+  i32x8 w_even[4], w_odd[4], xv[R];
+  uint32_t sx[QB / 4], sw;      // the step's scales: bytes of the rows' four blocks, the columns'
+  uint32_t sx_ahead, sw_ahead;  // in flight: the byte this thread stages, two steps ahead; the columns', one ahead
 
-  // A step: the operands of step g are in registers (or on their way), step g+1's
-  // records in `next` or on their way there, and `cur` is free once every wave has
-  // its operands of step g.  Each operand's registers are read again from `next`
-  // as soon as its last multiplication has been issued.
-  auto step = [&](int g, uint8_t* cur, const uint8_t* next, uint8_t* s_cur, const uint8_t* s_next) {
-    auto multiply = [&](int f, int q) {
-      if constexpr (EXACT) {
-        const float ss = scale_of((sx[q / 4] >> (8 * (q & 3))) & 255u), sc = scale_of(sw);
+  // A step.  Its columns and its first R blocks of rows are in registers (or on their
+  // way), the other blocks follow from `cur`, each into the registers of the block R
+  // before it once that one's multiplications are issued.  In the middle, when every
+  // wave has all it needs of `cur`, the loads of step g+2 go there, and what has
+  // arrived in `next` is read in the same way for step g+1: no multiplication waits
+  // for a read issued just before it.
+  auto step = [&](int g, uint8_t* cur, const uint8_t* next, uint8_t* s_cur, const uint8_t* s_next, const i32x8(&w)[4],
+                  i32x8(&w_next)[4]) {
+    uint32_t sw_next = 0, sx_next[QB / 4];
+    Source from;
+    uint32_t at = lane_at;
+    asm("" : "+v"(at));  // (addresses are formed in the step, not kept over all of them)
+    constexpr int kEach = (LX + LW) / R;  // loads behind each block of the second half
+    static_assert(kEach * R == LX + LW && 4 % R == 0, "");
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              decode8((uint32_t)wv[f][2 * h], (uint32_t)wv[f][2 * h + 1], sc),
-              decode8((uint32_t)xv[q][2 * h], (uint32_t)xv[q][2 * h + 1], ss), acc[f][q], 0, 0, 0);
-      } else {
-        acc[f][q] = mfma_scaled(wv[f], xv[q], acc[f][q], sw, sx[q / 4], q & 3);
-      }
-    };
-#pragma unroll
-    for (int f = 0; f < 4; ++f) multiply(f, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0): this wave's loads of step g+1 and its reads of step g
-    __syncthreads();
-    const uint32_t sw_next = sw_ahead;
-    if (tid < TM) s_cur[splace] = (uint8_t)sx_ahead;
-    sx_ahead = load_sx(g + 3);
-    sw_ahead = load_sw(g + 2);
-    load_codes(g + 2, cur);
-    uint32_t sx_next[QB / 4];
-#pragma unroll
-    for (int q = 0; q < QB; q += 4)
-      sx_next[q / 4] = *reinterpret_cast<const uint32_t*>(s_next + wm * 16 * QB + r * QB + q);
-    xv[0] = read_x(next, 0);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int q = 1; q < QB; ++q) {
+    for (int q = 0; q < QB; ++q) {
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        multiply(f, q);
-        if (q == QB - 1) {
-          __builtin_amdgcn_sched_barrier(0);
-          wv[f] = read_w(next, f);
-          __builtin_amdgcn_sched_barrier(0);
+        if constexpr (EXACT) {
+          const float ss = scale_of((sx[q / 4] >> (8 * (q & 3))) & 255u), sc = scale_of(sw);
+#pragma unroll
+          for (int h = 0; h < 8; h += 2)
+            acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                decode8((uint32_t)w[f][h], (uint32_t)w[f][h + 1], sc),
+                decode8((uint32_t)xv[q % R][h], (uint32_t)xv[q % R][h + 1], ss), acc[f][q], 0, 0, 0);
+        } else {
+          acc[f][q] = mfma_scaled(w[f], xv[q % R], acc[f][q], sw, sx[q / 4], q & 3);
         }
       }
+      // (keeps the multiplications here: nothing else orders them and the barrier)
+      asm volatile("" : "+v"(acc[0][q]), "+v"(acc[1][q]), "+v"(acc[2][q]), "+v"(acc[3][q]));
       __builtin_amdgcn_sched_barrier(0);
-      xv[q] = read_x(next, q);
+      if (q < R) {
+        xv[q % R] = read_x(cur, q + R, at);
+      } else {
+        if (q == R) {
+          // this wave's loads of step g+1 and its reads of step g
+          __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
+          __syncthreads();
+          sw_next = sw_ahead;
+          if (tid < TM) s_cur[splace] = (uint8_t)sx_ahead;
+          sx_ahead = load_sx(g + 3);
+          sw_ahead = load_sw(g + 2);
+          from = source(g + 2);
+#pragma unroll
+          for (int p = 0; p < QB; p += 4)
+            sx_next[p / 4] = *reinterpret_cast<const uint32_t*>(s_next + wm * 16 * QB + r * QB + p);
+        }
+        xv[q % R] = read_x(next, q - R, at);
+#pragma unroll
+        for (int f = (q - R) * 4 / R; f < (q - R + 1) * 4 / R; ++f) w_next[f] = read_w(next, f, at);
+#pragma unroll
+        for (int k = (q - R) * kEach; k < (q - R + 1) * kEach; ++k) load_codes(from, cur, k);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     sw = sw_next;
 #pragma unroll
-    for (int q = 0; q < QB / 4; ++q) sx[q] = sx_next[q];
+    for (int p = 0; p < QB / 4; ++p) sx[p] = sx_next[p];
   };
 
-  load_codes(0, s_even);
   {
     const uint32_t first = load_sx(0), second = load_sx(1);
     sw = load_sw(0);
     sw_ahead = load_sw(1);
     sx_ahead = load_sx(2);
+    const Source f0 = source(0), f1 = source(1);
+#pragma unroll
+    for (int k = 0; k < LX + LW; ++k) load_codes(f0, s_even, k);
+#pragma unroll
+    for (int k = 0; k < LX + LW; ++k) load_codes(f1, s_odd, k);
     if (tid < TM) s_scale_even[splace] = (uint8_t)first, s_scale_odd[splace] = (uint8_t)second;
   }
-  __builtin_amdgcn_s_waitcnt(0x0070);
+  __builtin_amdgcn_s_waitcnt(wait_for(LX + LW, 0));  // all but the loads of step 1
   __syncthreads();
-  load_codes(1, s_odd);
 #pragma unroll
   for (int q = 0; q < QB; q += 4)
     sx[q / 4] = *reinterpret_cast<const uint32_t*>(s_scale_even + wm * 16 * QB + r * QB + q);
 #pragma unroll
-  for (int f = 0; f < 4; ++f) wv[f] = read_w(s_even, f);
+  for (int f = 0; f < 4; ++f) w_even[f] = read_w(s_even, f, lane_at);
 #pragma unroll
-  for (int q = 0; q < QB; ++q) xv[q] = read_x(s_even, q);
-  for (int g = 0; g < G; g += 2) {
-    step(g, s_even, s_odd, s_scale_even, s_scale_odd);
-    if (g + 1 < G) step(g + 1, s_odd, s_even, s_scale_odd, s_scale_even);
+  for (int q = 0; q < R; ++q) xv[q] = read_x(s_even, q, lane_at);
+  for (int g = 0;; g += 2) {
+    step(g, s_even, s_odd, s_scale_even, s_scale_odd, w_even, w_odd);
+    if (g + 1 >= G) break;  // (no way from the even step to itself: its reads need not wait for its loads)
+    step(g + 1, s_odd, s_even, s_scale_odd, s_scale_even, w_odd, w_even);
+    if (g + 2 >= G) break;
   }
   // no load into LDS may be under way when the workgroup's LDS is given away
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __builtin_amdgcn_s_waitcnt(wait_for(0, 15));
 
-  // rows 16 q + r of the wave, 16 columns from 16 c on
-  const int j = j0 + 64 * wn + 16 * c;
-  if (j >= n) return;
-  constexpr int W = OUT_BF16 ? 8 : 4;
-  float bv[16];
+  // Rows 16 q + r of the wave, W columns of each of its column units.  One copy of the
+  // whole for each activation, so that a call's instructions lie together.
+  constexpr int W = OUT_BF16 ? 8 : 4, UNITS = 16 / W;
+  const int jw = j0 + 64 * wn + W * c;
+  auto finish = [&](auto A) {
 #pragma unroll
-  for (int e = 0; e < 16; e += 4) {
-    const f32x4 t = bias ? load4<true>(bias, j + e, n) : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < UNITS; ++u) {
+      const int j = jw + 4 * W * u;
+      if (j >= n) break;
+      float bv[W];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) bv[e + v] = t[v];
-  }
+      for (int e = 0; e < W; e += 4) {
+        const f32x4 t = bias ? load4<true>(bias, j + e, n) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int q = 0; q < QB; ++q) {
-    const int i = i0 + wm * 16 * QB + 16 * q + r;
-    if (i >= row_end) continue;
+        for (int v = 0; v < 4; ++v) bv[e + v] = t[v];
+      }
 #pragma unroll
-    for (int e0 = 0; e0 < 16; e0 += W) {
-      if (j + e0 >= n) break;
-      float v[W];
-#pragma unroll
-      for (int e = 0; e < W; ++e) v[e] = acc[(e0 + e) / 4][q][e & 3] + bv[e0 + e];
-      with_act(a.ep.act, [&](auto A) {
+      for (int q = 0; q < QB; ++q) {
+        const int i = i0 + wm * 16 * QB + 16 * q + r;
+        if (i >= row_end) continue;
+        float v[W];
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          const float t = act_value<decltype(A)::value>(v[e]);
-          v[e] = j + e0 + e >= a.ep.act_begin ? t : v[e];
+          v[e] = acc[W / 4 * u + e / 4][q][e & 3] + bv[e];
+          if constexpr (decltype(A)::value != SVDQ_ACT_NONE) {
+            const float t = act_value<decltype(A)::value>(v[e]);
+            v[e] = j + e >= a.ep.act_begin ? t : v[e];
+          }
         }
-      });
-      if (a.ep.gate) {
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(row_of<true>(a.ep.gate, i / a.ep.gate_rows, n));
-        float gv[W];
-        load_cols<W, true>(row, j + e0, n, gv);
+        if (a.ep.gate) {
+          const uint16_t* row = reinterpret_cast<const uint16_t*>(row_of<true>(a.ep.gate, i / a.ep.gate_rows, n));
+          float gv[W];
+          load_cols<W, true>(row, j, n, gv);
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] *= gv[e];
-      }
-      if (a.ep.residual) {
-        float rv[W];
-        load_cols<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.residual, i, a.ep.ldr), j + e0, n, rv);
+          for (int e = 0; e < W; ++e) v[e] *= gv[e];
+        }
+        if (a.ep.residual) {
+          float rv[W];
+          load_cols<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.residual, i, a.ep.ldr), j, n, rv);
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
+          for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
+        }
+        store_cols<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.y, i, a.ep.ldy), j, n, v);
       }
-      store_cols<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.y, i, a.ep.ldy), j + e0, n, v);
     }
-  }
+  };
+  if (a.ep.act == SVDQ_ACT_NONE || a.ep.act_begin >= j0 + 64 * wn + 64)
+    finish(std::integral_constant<int, SVDQ_ACT_NONE>{});
+  else
+    with_act(a.ep.act, finish);
 }
 
 template <int QB, int NWM, int NWN, bool EXACT, bool OUT_BF16, bool GROUPED>
