@@ -231,9 +231,10 @@ def test_linear(S, b, m, n, out):
 
 @pytest.mark.parametrize("b", [1, 40, 200, 2049])
 @pytest.mark.parametrize("act", ACTS)
-def test_epilogue(S, b, act):
+@pytest.mark.parametrize("n,begin", [(150, 31), (256, 128), (512, 0), (256, 200)])
+def test_epilogue(S, b, act, n, begin):
     """Gate, residual and strides, each with an activation; nothing is written between the rows."""
-    m, n = 384, 150
+    m = 384
     rng = np.random.default_rng([b, 7])
     X = Layer(S, m, n, seed=3)
     x = rows_like(rng, b, m)
@@ -243,17 +244,17 @@ def test_epilogue(S, b, act):
         res = rng.standard_normal((b, n))
         res = R.bf16(res) if out == "bf16" else res.astype(np.float32).astype(np.float64)
         v, dv = X.product(x, tiles=out == "bf16" and b > 64)
-        y, bound = R.epilogue(v, dv, act, 31, gate=gate, gate_rows=rows, residual=res, out=out)
+        y, bound = R.epilogue(v, dv, act, begin, gate=gate, gate_rows=rows, residual=res, out=out)
         wide = torch.full((b, n + 9), 5.0, dtype=dtype_of(out)).cuda()
         wres = torch.full((b, n + 3), 7.0, dtype=dtype_of(out)).cuda()
         wres[:, 2: 2 + n] = torch.from_numpy(res).to(dtype_of(out)).cuda()
-        got = S.svdq_fp8_linear(dev_bf16(x), X.layer, act=act, act_begin=31, gate=dev_bf16(gate), gate_rows=rows,
+        got = S.svdq_fp8_linear(dev_bf16(x), X.layer, act=act, act_begin=begin, gate=dev_bf16(gate), gate_rows=rows,
                                 residual=wres[:, 2: 2 + n], y=wide[:, 5: 5 + n])
         close(got, y, bound, out)
         assert (wide[:, :5] == 5).all() and (wide[:, 5 + n:] == 5).all()
         # in place on the residual
         own = wres[:, 2: 2 + n]
-        S.svdq_fp8_linear(dev_bf16(x), X.layer, act=act, act_begin=31, gate=dev_bf16(gate), gate_rows=rows, residual=own, y=own)
+        S.svdq_fp8_linear(dev_bf16(x), X.layer, act=act, act_begin=begin, gate=dev_bf16(gate), gate_rows=rows, residual=own, y=own)
         assert torch.equal(own, got)
         assert (wres[:, :2] == 7).all() and (wres[:, 2 + n:] == 7).all()
 

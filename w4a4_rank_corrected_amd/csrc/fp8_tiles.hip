@@ -27,6 +27,31 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_
 // lanes of an operand read, which want one piece of 16 records, spread over the banks.
 __device__ __forceinline__ int record_key(int r) { return r & 7; }
 
+// W (4, or 8 of bf16) whole columns of a row from column j on, at any element's address.
+template <int W, bool BF16>
+__device__ __forceinline__ void load_whole(const void* row, int j, float (&v)[W]) {
+  if constexpr (BF16 && W == 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4_loose*>(reinterpret_cast<const uint16_t*>(row) + j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[2 * e] = bf16_lo(w[e]), v[2 * e + 1] = bf16_hi(w[e]);
+  } else if constexpr (BF16) {
+    const uint2 w = *reinterpret_cast<const uint2_loose*>(reinterpret_cast<const uint16_t*>(row) + j);
+    v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+  } else {
+    const f32x4 w = *reinterpret_cast<const f32x4_loose*>(reinterpret_cast<const float*>(row) + j);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = w[e];
+  }
+}
+template <int W, bool BF16>
+__device__ __forceinline__ void store_whole(void* to, const float (&v)[W]) {
+  if constexpr (BF16)
+    *reinterpret_cast<u32x4_loose*>(to) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                                pack_bf16x2(v[6], v[7])};
+  else
+    *reinterpret_cast<f32x4_loose*>(to) = f32x4{v[0], v[1], v[2], v[3]};
+}
+
 // s_waitcnt's operand: at most vm loads and lgkm LDS accesses under way.
 constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | 0x70 | lgkm << 8 | (vm >> 4) << 14; }
 
@@ -146,11 +171,16 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
   };
   auto read_x = [&](const uint8_t* buf, int q, uint32_t at) { return read(buf + (wm * QB + q) * 2048, at); };
 
+  // the sums start from the bias: the columns of this lane's results of block f
+  const int jw = j0 + 64 * wn;  // the wave's first column
+  auto column = [&](int f) { return jw + (OUT_BF16 ? 32 * (f >> 1) + 8 * c + 4 * (f & 1) : 16 * f + 4 * c); };
   f32x4 acc[4][QB];
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
+  for (int f = 0; f < 4; ++f) {
+    const f32x4 t = bias ? load4<true>(bias, column(f), n) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int q = 0; q < QB; ++q) acc[f][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < QB; ++q) acc[f][q] = t;
+  }
   constexpr int R = QB / 2;     // blocks of rows in registers at a time
   i32x8 w_even[4], w_odd[4], xv[R];
   uint32_t sx[QB / 4], sw;      // the step's scales: bytes of the rows' four blocks, the columns'
@@ -244,42 +274,107 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
     step(g + 1, s_odd, s_even, s_scale_odd, s_scale_even, w_odd, w_even);
     if (g + 2 >= G) break;
   }
-  // no load into LDS may be under way when the workgroup's LDS is given away
+  // no load into LDS may be under way when the workgroup's LDS is given away, or used anew
   __builtin_amdgcn_s_waitcnt(wait_for(0, 15));
 
-  // Rows 16 q + r of the wave, W columns of each of its column units.  One copy of the
-  // whole for each activation, so that a call's instructions lie together.
+  // The activation, gate and residual, and y's rounding.  A lane holds W neighbouring
+  // columns of a row in each of UNITS units; four lanes' are 64 bytes of y.
   constexpr int W = OUT_BF16 ? 8 : 4, UNITS = 16 / W;
-  const int jw = j0 + 64 * wn + W * c;
-  auto finish = [&](auto A) {
+  const int row0 = i0 + wm * 16 * QB;
+  const int begin = a.ep.act == SVDQ_ACT_NONE ? n : a.ep.act_begin;
+  if (j0 + TN <= n && (begin <= j0 || begin >= j0 + TN || (begin - j0) % 64 == 0)) {
+    // Whole columns, each wave's all with the activation or all without: straight code,
+    // one copy for each case.  (With every case inside one loop over the accumulators
+    // the instructions to be fetched, anew for every launch, cost more than the stores:
+    // 256 x 128 -> 256, one tile: 7.6 us.)
+    auto finish = [&](auto A, auto MORE) {
+      uint8_t* y = reinterpret_cast<uint8_t*>(row_of<OUT_BF16>(a.ep.y, row0 + r, a.ep.ldy)) + (jw + W * c) * (OUT_BF16 ? 2 : 4);
+      const size_t next = (size_t)16 * a.ep.ldy * (OUT_BF16 ? 2 : 4);
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      const int j = jw + 4 * W * u;
-      if (j >= n) break;
-      float bv[W];
+      for (int q = 0; q < QB; ++q, y += next) {
+        const int i = row0 + 16 * q + r;
+        if (i >= row_end) break;
 #pragma unroll
-      for (int e = 0; e < W; e += 4) {
-        const f32x4 t = bias ? load4<true>(bias, j + e, n) : f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < UNITS; ++u) {
+          float v[W];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) bv[e + v] = t[v];
+          for (int e = 0; e < W; ++e) v[e] = act_value<decltype(A)::value>(acc[W / 4 * u + e / 4][q][e & 3]);
+          if constexpr (decltype(MORE)::value) {
+            const int j = jw + W * c + 4 * W * u;
+            if (a.ep.gate) {
+              float gv[W];
+              load_whole<W, true>(row_of<true>(a.ep.gate, i / a.ep.gate_rows, n), j, gv);
+#pragma unroll
+              for (int e = 0; e < W; ++e) v[e] *= gv[e];
+            }
+            if (a.ep.residual) {
+              float rv[W];
+              load_whole<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.residual, i, a.ep.ldr), j, rv);
+#pragma unroll
+              for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
+            }
+          }
+          store_whole<W, OUT_BF16>(y + 64 * u, v);
+        }
       }
+    };
+    auto with_more = [&](auto A) {
+      if (a.ep.gate || a.ep.residual)
+        finish(A, std::true_type{});
+      else
+        finish(A, std::false_type{});
+    };
+    if (begin >= jw + 64)
+      with_more(std::integral_constant<int, SVDQ_ACT_NONE>{});
+    else
+      with_act(a.ep.act, with_more);
+    return;
+  }
+
+  // The other tiles: 32 rows at a time through the wave's own part of LDS and one loop
+  // over the rows, with every column's own case.
+  __syncthreads();  // every wave is done with the buffers
+  constexpr int LANES = 64 / W;  // lanes of a row
+  constexpr int kPitch = 272;    // bytes of a row of 64 sums: rows on different banks
+  uint8_t* part = (wave < NW / 2 ? s_even : s_odd) + (wave % (NW / 2)) * 32 * kPitch;
+  static_assert(NW / 2 * 32 * kPitch <= (TM + TN) * 128, "the waves' parts fit the buffers");
+  const int rr = lane / LANES, cc = lane % LANES;
+  const int j = jw + W * cc;
+#pragma unroll 1
+  for (int p = 0; p < QB / 2; ++p) {
 #pragma unroll
-      for (int q = 0; q < QB; ++q) {
-        const int i = i0 + wm * 16 * QB + 16 * q + r;
-        if (i >= row_end) continue;
+    for (int b = 0; b < QB / 2; ++b)
+      if (b == p) {  // (accumulators are registers: a branch for each pair of blocks)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            *reinterpret_cast<f32x4*>(part + (16 * h + r) * kPitch + (column(f) - jw) * 4) = acc[f][2 * b + h];
+      }
+    // other lanes' results: LDS accesses of one wave complete in order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int k = rr; k < 32; k += 64 / LANES) {
+      const int i = row0 + 32 * p + k;
+      if (i < row_end && j < n) {
         float v[W];
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          v[e] = acc[W / 4 * u + e / 4][q][e & 3] + bv[e];
-          if constexpr (decltype(A)::value != SVDQ_ACT_NONE) {
+        for (int e = 0; e < W; e += 4) {
+          const f32x4 t = *reinterpret_cast<const f32x4*>(part + k * kPitch + (W * cc + e) * 4);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[e + x] = t[x];
+        }
+        with_act(a.ep.act, [&](auto A) {
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
             const float t = act_value<decltype(A)::value>(v[e]);
             v[e] = j + e >= a.ep.act_begin ? t : v[e];
           }
-        }
+        });
         if (a.ep.gate) {
-          const uint16_t* row = reinterpret_cast<const uint16_t*>(row_of<true>(a.ep.gate, i / a.ep.gate_rows, n));
           float gv[W];
-          load_cols<W, true>(row, j, n, gv);
+          load_cols<W, true>(row_of<true>(a.ep.gate, i / a.ep.gate_rows, n), j, n, gv);
 #pragma unroll
           for (int e = 0; e < W; ++e) v[e] *= gv[e];
         }
@@ -292,11 +387,9 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
         store_cols<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.y, i, a.ep.ldy), j, n, v);
       }
     }
-  };
-  if (a.ep.act == SVDQ_ACT_NONE || a.ep.act_begin >= j0 + 64 * wn + 64)
-    finish(std::integral_constant<int, SVDQ_ACT_NONE>{});
-  else
-    with_act(a.ep.act, finish);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
 }
 
 template <int QB, int NWM, int NWN, bool EXACT, bool OUT_BF16, bool GROUPED>
