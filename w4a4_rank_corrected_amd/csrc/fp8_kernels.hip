@@ -303,8 +303,7 @@ int launch_fp8_rows(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* st
 }
 
 int launch_fp8_gemm(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream) {
-  (void)ws;
-  return plan.rb ? launch_fp8_rows(a, plan, y_dtype, stream) : launch_fp8_tiles(a, plan, y_dtype, stream);
+  return plan.rb ? launch_fp8_rows(a, plan, y_dtype, stream) : launch_fp8_tiles(a, plan, y_dtype, ws, stream);
 }
 
 }  // namespace svdq

@@ -55,49 +55,158 @@ __device__ __forceinline__ void store_whole(void* to, const float (&v)[W]) {
 // s_waitcnt's operand: at most vm loads and lgkm LDS accesses under way.
 constexpr int wait_for(int vm, int lgkm) { return (vm & 15) | 0x70 | lgkm << 8 | (vm >> 4) << 14; }
 
-template <int QB, int NWM, int NWN, bool EXACT, bool OUT_BF16, bool GROUPED>
-__global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int tiles_m, int tiles_n) {
-  constexpr int TM = 16 * QB * NWM, TN = 64 * NWN, NW = NWM * NWN;
+// The first column of the four that block f of a lane's results holds.
+template <bool OUT_BF16>
+__device__ __forceinline__ int column_of(int jw, int c, int f) {
+  return jw + (OUT_BF16 ? 32 * (f >> 1) + 8 * c + 4 * (f & 1) : 16 * f + 4 * c);
+}
+
+// The activation, gate and residual, and y's rounding, for a wave's 16 QB rows from
+// row0 on and 64 columns from jw on.  A lane holds W neighbouring columns of a row in
+// each of UNITS units; four lanes' are 64 bytes of y.  part: 32 x 272 bytes of LDS of
+// the wave's own, not in use.
+template <int QB, bool OUT_BF16>
+__device__ __forceinline__ void finish_rows(const f32x4 (&acc)[4][QB], int row0, int row_end, int jw, int n,
+                                            const EpiArgs& ep, uint8_t* part) {
+  const int lane = (int)threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  constexpr int W = OUT_BF16 ? 8 : 4, UNITS = 16 / W;
+  const int begin = ep.act == SVDQ_ACT_NONE ? n : ep.act_begin;
+  if (jw >= n) return;
+  if (jw + 64 <= n && (begin <= jw || begin >= jw + 64)) {
+    // Whole columns, all with the activation or all without: straight code, one copy for
+    // each case, so that a call's instructions lie together.
+    auto finish = [&](auto A, auto MORE) {
+      uint8_t* y = reinterpret_cast<uint8_t*>(row_of<OUT_BF16>(ep.y, row0 + r, ep.ldy)) + (jw + W * c) * (OUT_BF16 ? 2 : 4);
+      const size_t next = (size_t)16 * ep.ldy * (OUT_BF16 ? 2 : 4);
+#pragma unroll
+      for (int q = 0; q < QB; ++q, y += next) {
+        const int i = row0 + 16 * q + r;
+        if (i >= row_end) break;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          float v[W];
+#pragma unroll
+          for (int e = 0; e < W; ++e) v[e] = act_value<decltype(A)::value>(acc[W / 4 * u + e / 4][q][e & 3]);
+          if constexpr (decltype(MORE)::value) {
+            const int j = jw + W * c + 4 * W * u;
+            if (ep.gate) {
+              float gv[W];
+              load_whole<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, gv);
+#pragma unroll
+              for (int e = 0; e < W; ++e) v[e] *= gv[e];
+            }
+            if (ep.residual) {
+              float rv[W];
+              load_whole<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, rv);
+#pragma unroll
+              for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
+            }
+          }
+          store_whole<W, OUT_BF16>(y + 64 * u, v);
+        }
+      }
+    };
+    auto with_more = [&](auto A) {
+      if (ep.gate || ep.residual)
+        finish(A, std::true_type{});
+      else
+        finish(A, std::false_type{});
+    };
+    if (begin >= jw + 64)
+      with_more(std::integral_constant<int, SVDQ_ACT_NONE>{});
+    else
+      with_act(ep.act, with_more);
+    return;
+  }
+
+  // The other waves: 32 rows at a time through LDS and one loop over the rows, with
+  // every column's own case.
+  constexpr int LANES = 64 / W;  // lanes of a row
+  constexpr int kPitch = 272;    // bytes of a row of 64 sums: rows on different banks
+  const int rr = lane / LANES, cc = lane % LANES;
+  const int j = jw + W * cc;
+#pragma unroll 1
+  for (int p = 0; p < (QB + 1) / 2; ++p) {
+#pragma unroll
+    for (int b = 0; b < (QB + 1) / 2; ++b)
+      if (b == p) {  // (accumulators are registers: a branch for each pair of blocks)
+#pragma unroll
+        for (int h = 0; h < 2 && 2 * b + h < QB; ++h)
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            *reinterpret_cast<f32x4*>(part + (16 * h + r) * kPitch + (column_of<OUT_BF16>(0, c, f)) * 4) = acc[f][2 * b + h];
+      }
+    // other lanes' results: LDS accesses of one wave complete in order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int k = rr; k < (QB > 1 ? 32 : 16); k += 64 / LANES) {
+      const int i = row0 + 32 * p + k;
+      if (i < row_end && j < n) {
+        float v[W];
+#pragma unroll
+        for (int e = 0; e < W; e += 4) {
+          const f32x4 t = *reinterpret_cast<const f32x4*>(part + k * kPitch + (W * cc + e) * 4);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[e + x] = t[x];
+        }
+        with_act(ep.act, [&](auto A) {
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const float t = act_value<decltype(A)::value>(v[e]);
+            v[e] = j + e >= ep.act_begin ? t : v[e];
+          }
+        });
+        if (ep.gate) {
+          float gv[W];
+          load_cols<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, gv);
+#pragma unroll
+          for (int e = 0; e < W; ++e) v[e] *= gv[e];
+        }
+        if (ep.residual) {
+          float rv[W];
+          load_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, rv);
+#pragma unroll
+          for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
+        }
+        store_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, v);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// One tile: rows i0 .. i0 + TM - 1 (those before row_end), columns j0 .. j0 + TN - 1,
+// channel blocks 0 .. G-1 of the operands given.  PARTIAL: the sums alone, to `sums`.
+//
+// NWM x NWN waves of 16 QB rows x 64 columns each.  Per block of 128 channels the
+// records of the tile's rows and columns go from memory into LDS (no registers in
+// between), two steps ahead; weights are the first operand of the matrix instruction,
+// so that a lane's four results are neighbouring columns of one row.
+template <int QB, int NWM, int NWN>
+struct TileShape {
+  static constexpr int TM = 16 * QB * NWM, TN = 64 * NWN, NW = NWM * NWN;
+  static constexpr int kCodes = (TM + TN) * 128;            // bytes of a step's records: rows, then columns
+  static constexpr int QS = (QB + 3) / 4 * 4;               // bytes of scales a lane reads
+  static constexpr int kScales = 16 * QS * NWM;             // [wave row][16 rows][QS]
+  static constexpr int kPart = 32 * 272;                    // finish_rows' part of a wave
+  static constexpr int kBuffer = kCodes > NW / 2 * kPart ? kCodes : NW / 2 * kPart;
+};
+template <int QB, int NWM, int NWN, bool EXACT, bool OUT_BF16, bool GROUPED, bool PARTIAL>
+__device__ __forceinline__ void tile(const Fp8Args& a, const uint8_t* qx, const uint8_t* ascale, const uint8_t* qw,
+                                     const uint8_t* wscale, const uint16_t* bias, int G, int i0, int j0, int row_end,
+                                     uint8_t* s_even, uint8_t* s_odd, uint8_t* s_scale_even, uint8_t* s_scale_odd,
+                                     f32x4* sums) {
+  typedef TileShape<QB, NWM, NWN> Shape;
+  constexpr int TM = Shape::TM, TN = Shape::TN, NW = Shape::NW, QS = Shape::QS;
   constexpr int LX = TM / (8 * NW), LW = TN / (8 * NW);  // 8-record loads a wave and step
   static_assert(LX * 8 * NW == TM && LW * 8 * NW == TN && TM <= 64 * NW, "whole loads");
-  // Two buffers of a step's records (rows, then columns) and of its rows' scales
-  // ([wave row][16 rows][QB]); arrays of their own, so that the compiler sees that
-  // loads into one are apart from reads of the other.
-  __shared__ __align__(16) uint8_t s_even[(TM + TN) * 128];
-  __shared__ __align__(16) uint8_t s_odd[(TM + TN) * 128];
-  __shared__ __align__(16) uint8_t s_scale_even[TM];
-  __shared__ __align__(16) uint8_t s_scale_odd[TM];
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / NWN, wn = wave - wm * NWN;
   const int r = lane & 15, c = lane >> 4;
-  const int n = a.n, G = a.G, NB = (n + 127) / 128, xr = a.x_rows;
-  const uint8_t* qw = a.qw;
-  const uint8_t* wscale = a.wscale;
-  const uint16_t* bias = a.bias;
-  int i0, j0, row_end;
-  if constexpr (GROUPED) {
-    const GroupTile g = find_tile<TM>(a.groups.offsets, a.groups.experts, a.b, tiles_n, (int)blockIdx.x,
-                                      [](int d, int T) { return xcd_range(d, T); });
-    if (!g.live) return;  // the whole workgroup
-    const int tj = g.u / g.blocks;
-    i0 = g.lo + (g.u - tj * g.blocks) * TM;
-    j0 = tj * TN;
-    row_end = g.hi;
-    const size_t e = (size_t)g.expert;
-    qw += e * G * (size_t)n * 128;
-    wscale += e * G * NB;
-    if (bias) bias += e * n;
-  } else {
-    // an XCD's workgroups take blocks of 8 row tiles by the column tiles, so that
-    // those running together share records in its L2
-    const int u = xcd_range((int)blockIdx.x, tiles_m * tiles_n);
-    const int band = u / (8 * tiles_n), in = u - band * 8 * tiles_n;
-    const int high = min(tiles_m - band * 8, 8), tj = in / high;
-    i0 = (band * 8 + in - tj * high) * TM;
-    j0 = tj * TN;
-    row_end = a.b;
-  }
+  const int n = a.n, NB = (n + 127) / 128, xr = a.x_rows;
 
   // What this lane loads: piece (lane & 7) ^ key of records 8 (wave + NW i) + lane / 8.
   // From load to load i the records are 8 NW further, and so are the rows (unless they
@@ -131,7 +240,7 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
     if (GROUPED && a.row_index) s = a.row_index[s];
     if ((unsigned)s < (unsigned)xr) soff = (uint32_t)s;
   }
-  const int splace = (tid / (16 * QB)) * 16 * QB + (tid & 15) * QB + (tid >> 4) % QB;
+  const int splace = (tid / (16 * QB)) * 16 * QS + (tid & 15) * QS + (tid >> 4) % QB;
 
   struct Source {
     __amdgpu_buffer_rsrc_t x, w;
@@ -139,7 +248,7 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
   };
   auto source = [&](int g) {  // (past the last step zeros, without memory traffic)
     const size_t at = g < G ? (size_t)g : 0;
-    Source f{make_rsrc(a.qx + at * xr * 128, g < G ? (uint32_t)xr * 128u : 0u),
+    Source f{make_rsrc(qx + at * xr * 128, g < G ? (uint32_t)xr * 128u : 0u),
              make_rsrc(qw + at * n * 128, g < G ? (uint32_t)n * 128u : 0u), xoff[0], woff};
     // (a load's offset is formed where it is issued, by one addition, not kept in a register)
     asm("" : "+v"(f.x0), "+v"(f.w0));
@@ -154,7 +263,7 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
   };
   // (past the last step the last one's, unused)
   auto load_sx = [&](int g) -> uint32_t {
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.ascale + (size_t)min(g, G - 1) * xr, (uint32_t)xr);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(ascale + (size_t)min(g, G - 1) * xr, (uint32_t)xr);
     return __builtin_amdgcn_raw_buffer_load_b8(rx, soff, 0, 0);
   };
   auto load_sw = [&](int g) -> uint32_t {
@@ -173,17 +282,16 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
 
   // the sums start from the bias: the columns of this lane's results of block f
   const int jw = j0 + 64 * wn;  // the wave's first column
-  auto column = [&](int f) { return jw + (OUT_BF16 ? 32 * (f >> 1) + 8 * c + 4 * (f & 1) : 16 * f + 4 * c); };
   f32x4 acc[4][QB];
 #pragma unroll
   for (int f = 0; f < 4; ++f) {
-    const f32x4 t = bias ? load4<true>(bias, column(f), n) : f32x4{0.f, 0.f, 0.f, 0.f};
+    const f32x4 t = !PARTIAL && bias ? load4<true>(bias, column_of<OUT_BF16>(jw, c, f), n) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < QB; ++q) acc[f][q] = t;
   }
   constexpr int R = QB / 2;     // blocks of rows in registers at a time
   i32x8 w_even[4], w_odd[4], xv[R];
-  uint32_t sx[QB / 4], sw;      // the step's scales: bytes of the rows' four blocks, the columns'
+  uint32_t sx[QS / 4], sw;      // the step's scales: bytes of the rows' four blocks, the columns'
   uint32_t sx_ahead, sw_ahead;  // in flight: the byte this thread stages, two steps ahead; the columns', one ahead
 
   // A step.  Its columns and its first R blocks of rows are in registers (or on their
@@ -194,7 +302,7 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
   // for a read issued just before it.
   auto step = [&](int g, uint8_t* cur, const uint8_t* next, uint8_t* s_cur, const uint8_t* s_next, const i32x8(&w)[4],
                   i32x8(&w_next)[4]) {
-    uint32_t sw_next = 0, sx_next[QB / 4];
+    uint32_t sw_next = 0, sx_next[QS / 4];
     Source from;
     uint32_t at = lane_at;
     asm("" : "+v"(at));  // (addresses are formed in the step, not kept over all of them)
@@ -231,8 +339,8 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
           sw_ahead = load_sw(g + 2);
           from = source(g + 2);
 #pragma unroll
-          for (int p = 0; p < QB; p += 4)
-            sx_next[p / 4] = *reinterpret_cast<const uint32_t*>(s_next + wm * 16 * QB + r * QB + p);
+          for (int p = 0; p < QS; p += 4)
+            sx_next[p / 4] = *reinterpret_cast<const uint32_t*>(s_next + (wm * 16 + r) * QS + p);
         }
         xv[q % R] = read_x(next, q - R, at);
 #pragma unroll
@@ -244,7 +352,7 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
     }
     sw = sw_next;
 #pragma unroll
-    for (int p = 0; p < QB / 4; ++p) sx[p] = sx_next[p];
+    for (int p = 0; p < QS / 4; ++p) sx[p] = sx_next[p];
   };
 
   {
@@ -262,8 +370,8 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
   __builtin_amdgcn_s_waitcnt(wait_for(LX + LW, 0));  // all but the loads of step 1
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < QB; q += 4)
-    sx[q / 4] = *reinterpret_cast<const uint32_t*>(s_scale_even + wm * 16 * QB + r * QB + q);
+  for (int q = 0; q < QS; q += 4)
+    sx[q / 4] = *reinterpret_cast<const uint32_t*>(s_scale_even + (wm * 16 + r) * QS + q);
 #pragma unroll
   for (int f = 0; f < 4; ++f) w_even[f] = read_w(s_even, f, lane_at);
 #pragma unroll
@@ -276,148 +384,155 @@ __global__ __launch_bounds__(64 * NWM * NWN) void fp8_tile_kernel(Fp8Args a, int
   }
   // no load into LDS may be under way when the workgroup's LDS is given away, or used anew
   __builtin_amdgcn_s_waitcnt(wait_for(0, 15));
+  if constexpr (PARTIAL) {
+    sums += (size_t)wave * QB * 4 * 64 + lane;
+#pragma unroll
+    for (int q = 0; q < QB; ++q)
+#pragma unroll
+      for (int f = 0; f < 4; ++f) sums[(q * 4 + f) * 64] = acc[f][q];
+  } else {
+    __syncthreads();  // (a wave's part of LDS is others' buffer)
+    finish_rows<QB, OUT_BF16>(acc, i0 + wm * 16 * QB, row_end, jw, n, a.ep,
+                              (wave < NW / 2 ? s_even : s_odd) + wave % (NW / 2) * Shape::kPart);
+  }
+}
 
-  // The activation, gate and residual, and y's rounding.  A lane holds W neighbouring
-  // columns of a row in each of UNITS units; four lanes' are 64 bytes of y.
-  constexpr int W = OUT_BF16 ? 8 : 4, UNITS = 16 / W;
-  const int row0 = i0 + wm * 16 * QB;
-  const int begin = a.ep.act == SVDQ_ACT_NONE ? n : a.ep.act_begin;
-  if (j0 + TN <= n && (begin <= j0 || begin >= j0 + TN || (begin - j0) % 64 == 0)) {
-    // Whole columns, each wave's all with the activation or all without: straight code,
-    // one copy for each case.  (With every case inside one loop over the accumulators
-    // the instructions to be fetched, anew for every launch, cost more than the stores:
-    // 256 x 128 -> 256, one tile: 7.6 us.)
-    auto finish = [&](auto A, auto MORE) {
-      uint8_t* y = reinterpret_cast<uint8_t*>(row_of<OUT_BF16>(a.ep.y, row0 + r, a.ep.ldy)) + (jw + W * c) * (OUT_BF16 ? 2 : 4);
-      const size_t next = (size_t)16 * a.ep.ldy * (OUT_BF16 ? 2 : 4);
-#pragma unroll
-      for (int q = 0; q < QB; ++q, y += next) {
-        const int i = row0 + 16 * q + r;
-        if (i >= row_end) break;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          float v[W];
-#pragma unroll
-          for (int e = 0; e < W; ++e) v[e] = act_value<decltype(A)::value>(acc[W / 4 * u + e / 4][q][e & 3]);
-          if constexpr (decltype(MORE)::value) {
-            const int j = jw + W * c + 4 * W * u;
-            if (a.ep.gate) {
-              float gv[W];
-              load_whole<W, true>(row_of<true>(a.ep.gate, i / a.ep.gate_rows, n), j, gv);
-#pragma unroll
-              for (int e = 0; e < W; ++e) v[e] *= gv[e];
-            }
-            if (a.ep.residual) {
-              float rv[W];
-              load_whole<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.residual, i, a.ep.ldr), j, rv);
-#pragma unroll
-              for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
-            }
-          }
-          store_whole<W, OUT_BF16>(y + 64 * u, v);
-        }
-      }
-    };
-    auto with_more = [&](auto A) {
-      if (a.ep.gate || a.ep.residual)
-        finish(A, std::true_type{});
-      else
-        finish(A, std::false_type{});
-    };
-    if (begin >= jw + 64)
-      with_more(std::integral_constant<int, SVDQ_ACT_NONE>{});
-    else
-      with_act(a.ep.act, with_more);
+// Tile u of tiles_m x tiles_n: bands of 8 row tiles by the column tiles, so that the
+// workgroups of an XCD (which take neighbouring u) share records in its L2.
+__device__ __forceinline__ void tile_at(int u, int tiles_m, int tiles_n, int& ti, int& tj) {
+  const int band = u / (8 * tiles_n), in = u - band * 8 * tiles_n;
+  const int high = min(tiles_m - band * 8, 8);
+  tj = in / high;
+  ti = band * 8 + in - tj * high;
+}
+
+// Tiles of 256 x 256, one workgroup a CU, for whole rounds of the CUs; the tiles left
+// over are cut into PARTS of 256 x 128 or 128 x 128, so that the last round takes every
+// CU for the time of a part.
+template <int PARTS>
+__global__ __launch_bounds__(512) void fp8_big_kernel(Fp8Args a, int tiles_m, int tiles_n, int full) {
+  typedef TileShape<8, 2, 4> Shape;
+  __shared__ __align__(16) uint8_t s_even[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_odd[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_scale_even[Shape::kScales];
+  __shared__ __align__(16) uint8_t s_scale_odd[Shape::kScales];
+  const int d = (int)blockIdx.x;
+  int ti, tj;
+  if (PARTS == 1 || d < full) {
+    tile_at(xcd_range(d, full), tiles_m, tiles_n, ti, tj);
+    tile<8, 2, 4, false, true, false, false>(a, a.qx, a.ascale, a.qw, a.wscale, a.bias, a.G, ti * 256, tj * 256, a.b,
+                                             s_even, s_odd, s_scale_even, s_scale_odd, nullptr);
     return;
   }
-
-  // The other tiles: 32 rows at a time through the wave's own part of LDS and one loop
-  // over the rows, with every column's own case.
-  __syncthreads();  // every wave is done with the buffers
-  constexpr int LANES = 64 / W;  // lanes of a row
-  constexpr int kPitch = 272;    // bytes of a row of 64 sums: rows on different banks
-  uint8_t* part = (wave < NW / 2 ? s_even : s_odd) + (wave % (NW / 2)) * 32 * kPitch;
-  static_assert(NW / 2 * 32 * kPitch <= (TM + TN) * 128, "the waves' parts fit the buffers");
-  const int rr = lane / LANES, cc = lane % LANES;
-  const int j = jw + W * cc;
-#pragma unroll 1
-  for (int p = 0; p < QB / 2; ++p) {
-#pragma unroll
-    for (int b = 0; b < QB / 2; ++b)
-      if (b == p) {  // (accumulators are registers: a branch for each pair of blocks)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-            *reinterpret_cast<f32x4*>(part + (16 * h + r) * kPitch + (column(f) - jw) * 4) = acc[f][2 * b + h];
-      }
-    // other lanes' results: LDS accesses of one wave complete in order
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-    for (int k = rr; k < 32; k += 64 / LANES) {
-      const int i = row0 + 32 * p + k;
-      if (i < row_end && j < n) {
-        float v[W];
-#pragma unroll
-        for (int e = 0; e < W; e += 4) {
-          const f32x4 t = *reinterpret_cast<const f32x4*>(part + k * kPitch + (W * cc + e) * 4);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) v[e + x] = t[x];
-        }
-        with_act(a.ep.act, [&](auto A) {
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const float t = act_value<decltype(A)::value>(v[e]);
-            v[e] = j + e >= a.ep.act_begin ? t : v[e];
-          }
-        });
-        if (a.ep.gate) {
-          float gv[W];
-          load_cols<W, true>(row_of<true>(a.ep.gate, i / a.ep.gate_rows, n), j, n, gv);
-#pragma unroll
-          for (int e = 0; e < W; ++e) v[e] *= gv[e];
-        }
-        if (a.ep.residual) {
-          float rv[W];
-          load_cols<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.residual, i, a.ep.ldr), j, n, rv);
-#pragma unroll
-          for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
-        }
-        store_cols<W, OUT_BF16>(row_of<OUT_BF16>(a.ep.y, i, a.ep.ldy), j, n, v);
-      }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+  if constexpr (PARTS > 1) {
+    const int u = xcd_range(d - full, (tiles_m * tiles_n - full) * PARTS);
+    tile_at(full + u / PARTS, tiles_m, tiles_n, ti, tj);
+    const int i0 = ti * 256 + (PARTS == 4 ? 128 * (u >> 1 & 1) : 0), j0 = tj * 256 + 128 * (u & 1);
+    if (i0 >= a.b || j0 >= a.n) return;  // (the whole workgroup)
+    if constexpr (PARTS == 2)
+      tile<4, 4, 2, false, true, false, false>(a, a.qx, a.ascale, a.qw, a.wscale, a.bias, a.G, i0, j0, a.b, s_even,
+                                               s_odd, s_scale_even, s_scale_odd, nullptr);
+    else
+      tile<2, 4, 2, false, true, false, false>(a, a.qx, a.ascale, a.qw, a.wscale, a.bias, a.G, i0, j0, a.b, s_even,
+                                               s_odd, s_scale_even, s_scale_odd, nullptr);
   }
 }
 
-template <int QB, int NWM, int NWN, bool EXACT, bool OUT_BF16, bool GROUPED>
-int launch_tiles_typed(const Fp8Args& a, const Fp8Plan& p, hipStream_t st) {
-  constexpr int TM = 16 * QB * NWM, TN = 64 * NWN, threads = 64 * NWM * NWN;
-  auto kernel = fp8_tile_kernel<QB, NWM, NWN, EXACT, OUT_BF16, GROUPED>;
-  if (!launch_fits(p.split.grid, threads)) return (int)hipErrorInvalidConfiguration;
-  const int ok = scratch_free(reinterpret_cast<const void*>(kernel));
-  if (ok != 0) return ok;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)p.split.grid), dim3(threads), 0, st, a, (a.b + TM - 1) / TM,
-                     (a.n + TN - 1) / TN);
-  return (int)hipGetLastError();
+// Tiles of 128 x 128, two workgroups a CU: experts' rows, fp32 results, and few tiles,
+// which may be split along the channels (PIECES: piece p of tile u takes every block
+// from p G / pieces to (p + 1) G / pieces and leaves its sums in slot u pieces + p).
+template <bool EXACT, bool GROUPED, bool PIECES>
+__global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8Args a, int tiles_m, int tiles_n, int pieces, f32x4* sums) {
+  typedef TileShape<4, 2, 2> Shape;
+  __shared__ __align__(16) uint8_t s_even[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_odd[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_scale_even[Shape::kScales];
+  __shared__ __align__(16) uint8_t s_scale_odd[Shape::kScales];
+  const uint8_t *qx = a.qx, *ascale = a.ascale, *qw = a.qw, *wscale = a.wscale;
+  const uint16_t* bias = a.bias;
+  const int NB = (a.n + 127) / 128;
+  int i0, j0, row_end, G = a.G;
+  if constexpr (GROUPED) {
+    const GroupTile g = find_tile<128>(a.groups.offsets, a.groups.experts, a.b, tiles_n, (int)blockIdx.x,
+                                       [](int d, int T) { return xcd_range(d, T); });
+    if (!g.live) return;  // the whole workgroup
+    const int tj = g.u / g.blocks;
+    i0 = g.lo + (g.u - tj * g.blocks) * 128;
+    j0 = tj * 128;
+    row_end = g.hi;
+    const size_t e = (size_t)g.expert;
+    qw += e * G * (size_t)a.n * 128;
+    wscale += e * G * NB;
+    if (bias) bias += e * a.n;
+  } else {
+    const int u = xcd_range((int)blockIdx.x, tiles_m * tiles_n * pieces);
+    int ti, tj;
+    tile_at(u / pieces, tiles_m, tiles_n, ti, tj);
+    i0 = ti * 128;
+    j0 = tj * 128;
+    row_end = a.b;
+    if constexpr (PIECES) {
+      const int p = u % pieces, g0 = (int)((long long)G * p / pieces);
+      G = (int)((long long)G * (p + 1) / pieces) - g0;
+      qx += (size_t)g0 * a.x_rows * 128;
+      ascale += (size_t)g0 * a.x_rows;
+      qw += (size_t)g0 * a.n * 128;
+      wscale += (size_t)g0 * NB;
+      sums += (size_t)u * (128 * 128 / 4);
+    }
+  }
+  tile<4, 2, 2, EXACT, !EXACT, GROUPED, PIECES>(a, qx, ascale, qw, wscale, bias, G, i0, j0, row_end, s_even, s_odd,
+                                                s_scale_even, s_scale_odd, sums);
 }
 
-template <int QB, int NWM, int NWN, bool EXACT>
-int launch_tiles(const Fp8Args& a, const Fp8Plan& p, hipStream_t st) {
-  return a.groups.offsets ? launch_tiles_typed<QB, NWM, NWN, EXACT, !EXACT, true>(a, p, st)
-                          : launch_tiles_typed<QB, NWM, NWN, EXACT, !EXACT, false>(a, p, st);
+// The pieces' sums of a tile added in their order, the bias, and the rest.  A workgroup
+// takes the blocks q of 16 rows of the tile's four waves.
+template <bool OUT_BF16>
+__global__ __launch_bounds__(256) void fp8_pieces_kernel(Fp8Args a, int tiles_m, int tiles_n, int pieces,
+                                                         const f32x4* __restrict__ sums) {
+  __shared__ __align__(16) uint8_t s_part[4][32 * 272];
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int u = (int)blockIdx.x >> 2, q = (int)blockIdx.x & 3;
+  int ti, tj;
+  tile_at(u, tiles_m, tiles_n, ti, tj);
+  const f32x4* from = sums + (size_t)u * pieces * (128 * 128 / 4) + (wave * 16 + q * 4) * 64 + lane;
+  const int jw = tj * 128 + 64 * (wave & 1);
+  f32x4 acc[4][1];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) acc[f][0] = from[f * 64];
+  for (int p = 1; p < pieces; ++p) {
+    from += 128 * 128 / 4;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[f][0] += from[f * 64];
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[f][0] += load4<true>(a.bias, column_of<OUT_BF16>(jw, lane >> 4, f), a.n);
+  }
+  finish_rows<1, OUT_BF16>(acc, ti * 128 + (wave >> 1) * 64 + 16 * q, a.b, jw, a.n, a.ep, s_part[wave]);
 }
 
 }  // namespace
 
-int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& p, int y_dtype, void* stream) {
+int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& p, int y_dtype, void* ws, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   const bool exact = y_dtype == SVDQ_OUT_F32;
-  if (p.tile_m == 256 && !exact) return launch_tiles<8, 2, 4, false>(a, p, st);
-  if (p.tile_m == 128) return exact ? launch_tiles<4, 2, 2, true>(a, p, st) : launch_tiles<4, 2, 2, false>(a, p, st);
-  return (int)hipErrorInvalidValue;
+  if (p.big) {
+    const int tm = (a.b + 255) / 256, tn = (a.n + 255) / 256;
+    auto go = [&](auto kernel) { return launch_checked(kernel, p.split.grid, 512, st, a, tm, tn, p.full); };
+    return p.parts == 1 ? go(fp8_big_kernel<1>) : p.parts == 2 ? go(fp8_big_kernel<2>) : go(fp8_big_kernel<4>);
+  }
+  const int tm = (a.b + 127) / 128, tn = (a.n + 127) / 128;
+  f32x4* sums = reinterpret_cast<f32x4*>(ws);
+  auto go = [&](auto kernel) { return launch_checked(kernel, p.split.grid, 256, st, a, tm, tn, p.pieces, sums); };
+  if (a.groups.offsets) return exact ? go(fp8_tile_kernel<true, true, false>) : go(fp8_tile_kernel<false, true, false>);
+  if (p.pieces == 1) return exact ? go(fp8_tile_kernel<true, false, false>) : go(fp8_tile_kernel<false, false, false>);
+  const int status = exact ? go(fp8_tile_kernel<true, false, true>) : go(fp8_tile_kernel<false, false, true>);
+  if (status != 0) return status;
+  auto join = [&](auto kernel) {
+    return launch_checked(kernel, (long long)tm * tn * 4, 256, st, a, tm, tn, p.pieces, (const f32x4*)sums);
+  };
+  return exact ? join(fp8_pieces_kernel<false>) : join(fp8_pieces_kernel<true>);
 }
 
 }  // namespace svdq

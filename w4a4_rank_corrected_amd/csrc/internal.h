@@ -271,9 +271,11 @@ struct Fp8Args {
   EpiArgs ep;
 };
 // The kernel of a product (experts 0: one layer) and its largest launch: the row
-// kernel with rb 16-row blocks a workgroup, or (rb 0) tiles of tile_m rows.
+// kernel with rb 16-row blocks a workgroup; or (rb 0) tiles of 128 x 128, in `pieces`
+// along the channels; or (big) the first `full` tiles of 256 x 256 and the others in
+// `parts` (1: there are no others).
 struct Fp8Plan {
-  int rb, tile_m, threads;
+  int rb, big, full, parts, pieces, threads;
   RowsSplit split;
   size_t ws_bytes;
 };
@@ -282,7 +284,7 @@ int launch_fp8_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t* ascale
 int launch_fp8_weights(const void* w, int dtype, int experts, int m, int n, bool transposed, uint8_t* qw,
                        uint8_t* wscale, void* stream);
 int launch_fp8_rows(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* stream);
-int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* stream);
+int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream);
 int launch_fp8_gemm(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream);
 // Launcher status (not a hipError_t) of a kernel that would use scratch memory.
 constexpr int kErrKernelScratch = -1000;
