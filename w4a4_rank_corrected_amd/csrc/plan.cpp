@@ -122,69 +122,70 @@ SortPlan sort_plan(int b) {
 
 namespace {
 
-// Microseconds of an 8-bit floating-point product of one layer by tiles of 128 x 128 in
-// k pieces, as measured: a launch and a tile's ends 4, a step 0.6 with one workgroup on
-// a CU and 0.96 for both of two (results in fp32: 0.96 and 1.65), and for pieces a second
-// launch, and the sums, 64 KB a piece, written and read.
+// Microseconds of an 8-bit floating-point product by tiles of 128 x 128 in k pieces, as
+// measured: a launch and a tile's ends 4, a step 0.6 with one workgroup on a CU and 0.96
+// for both of two (results in fp32: 0.96 and 1.65); for pieces a second launch, and the
+// sums, 64 KB a piece, written and read.
 //   tiles x pieces, steps of all pieces, bf16: 72 x 1, 36: 26.7; 72 x 2: 20.7; 72 x 4: 20.3;
 //   18 x 1, 36: 21.0; x 2: 15.4; x 4: 12.5; x 8: 15.0;  80 x 1, 16: 11.7; x 2: 15.5;
 //   128 x 1, 64: 43.7; x 2: 30.9; x 4: 27.7;  fp32: 72 x 1, 36: 39.5; x 2: 26.4; x 4: 25.8
 double fp8_tiles_us(long long tiles, int G, int k, bool exact) {
-  const long long units = tiles * k, rounds = (units + 2 * kMaxCUs - 1) / (2 * kMaxCUs);
+  const double units = (double)(tiles * k);
   const double step = units <= kMaxCUs ? (exact ? 0.96 : 0.6) : (exact ? 1.65 : 0.96);
-  return (4.0 + ((G + k - 1) / k) * step) * (double)rounds + (k > 1 ? 1.5 + 0.35 * k + 0.026 * (double)units : 0.0);
+  const double rounds = std::max(1.0, units / (2 * kMaxCUs));
+  return (4.0 + ((G + k - 1) / k) * step) * rounds + (k > 1 ? 1.5 + 0.35 * k + 0.026 * units : 0.0);
+}
+
+// The same by the row kernel, for `steps` of 16 rb rows x 16 columns x 128 channels:
+//   one layer: 1 row, 1152 -> 6912 5.8; 16 rows, 8192 -> 8192 19.3; 32: 25.7; 64: 42.7;
+//   100, 2048 -> 2048 8.6; 333, 1000 -> 1500 11.4; 256, 4608 -> 1152 25.6;
+//   64 experts, 2048 -> 1408, mean rows 1: 21.7 (tiles 15.1), 8: 52.9 (21.9), 32: 110 (37);
+//   8 experts, 4096 -> 1152, mean 1: 9.3 (18.9), 8: 16.1 (23.6), 16: 19.3 (23.5), 32: 27.4 (24.1)
+double fp8_rows_us(double steps, int rb, bool grouped) {
+  if (grouped) return 3.5 + (rb == 1 ? 0.00035 : 0.0006) * steps;
+  return rb == 1 ? 3.5 + 0.0005 * steps : (rb == 2 ? 4.0 + 0.0007 * steps : 4.5 + 0.0014 * steps);
 }
 
 }  // namespace
 
-// The 8-bit floating-point product of one layer (experts 0), by what was measured (us):
-//   * up to 64 rows the row kernel, which reads the weights once, at memory's rate; for
-//     more rows it reads them once for every 64 (2.5 + 0.0015 a step of 64 rows x 16
-//     columns x 128 channels: 100 x 2048 -> 2048 8.6, tiles 10.3; 333 x 1000 -> 1500 11.4
-//     and 9.8; 256 x 4608 -> 1152 25.6 and 12.5);
-//   * bf16 results with more than 128 tiles of 256 x 256: those tiles, which take half
-//     the records from the L2s that 128 x 128 ones do (16 TB/s of them were that
-//     kernel's limit: 8192 x 8192 -> 8192 487 against 377); their last round is cut
+// The 8-bit floating-point product of one layer (experts 0) or of experts' rows:
+//   * bf16 results of one layer with more than 128 tiles of 256 x 256: those tiles, which
+//     take half the records from the L2s that 128 x 128 ones do (16 TB/s of them were that
+//     kernel's limit: 8192 x 8192 -> 8192 487 us against 377); their last round is cut
 //     smaller where the tiles left over are few: 4608 x 4608 -> 12288 (96 of 864 left)
 //     212 whole, 204 in halves, 216 in quarters; 4096 x 1152 -> 4608 (32 of 288) 36.5,
 //     31.5, 29.1; 4608 x 3072 -> 9216 (136 of 648) 112, 125, 132;
-//   * otherwise 128 x 128 tiles, in the pieces that the estimate above likes best.
-// Grouped by expert: the row kernel up to 64 rows an expert on average, else 128 x 128
-// tiles.
+//   * otherwise tiles of 128 x 128, one layer's in the pieces that are quickest, or the
+//     row kernel, whichever the estimates above say is quicker.
 Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
   const int G = fp8_blocks(m);
-  const bool exact = y_dtype == SVDQ_OUT_F32;
-  const long long mean = experts > 0 ? (b + experts - 1) / experts : b;
-  const long long cols = (n + 127) / 128;
+  const bool exact = y_dtype == SVDQ_OUT_F32, grouped = experts > 0;
   Fp8Plan p{0, 0, 0, 1, 1, 256, {1, 1, 0}, 0};
   const long long big = (long long)((b + 255) / 256) * ((n + 255) / 256);
-  const long long tiles = (experts > 0 ? grouped_row_blocks(b, experts, 128) : (b + 127) / 128) * cols;
-  double best = 1e30;
-  if (experts == 0 && mean > 64) {
-    for (int k : {1, 2, 3, 4, 6, 8}) {
-      if (k > 1 && G < 2 * k) break;
-      const double us = fp8_tiles_us(tiles, G, k, exact);
-      if (us < best) best = us, p.pieces = k;
-    }
-  }
-  const double rows_us = 2.5 + 0.0015 * (double)((b + 63) / 64) * (double)((n + 15) / 16) * G;
-  if (mean <= 64 || (experts == 0 && rows_us < best)) {
-    p.rb = mean <= 16 ? 1 : (mean <= 32 ? 2 : 4);
-    p.pieces = 1;
-    const long long rows = 16 * p.rb;
-    const long long blocks = experts > 0 ? grouped_row_blocks(b, experts, rows) : (b + rows - 1) / rows;
-    p.split = rows_split(blocks, n, 2 * G, p.rb);
-    p.threads = 64 * p.split.nwk * p.split.nwc;
-    return p;
-  }
-  if (experts == 0 && !exact && big > 128) {
+  if (!grouped && !exact && big > 128) {
     p.big = 1;
-    p.pieces = 1;
     const long long full = big / kMaxCUs * kMaxCUs, left = big - full;
     p.parts = left == 0 || left > 128 ? 1 : (left > 64 ? 2 : 4);
     p.split.grid = p.parts == 1 ? big : full + left * p.parts;
     p.full = (int)(p.parts == 1 ? big : full);
     p.threads = 512;
+    return p;
+  }
+  const long long tiles = (grouped ? grouped_row_blocks(b, experts, 128) : (b + 127) / 128) * ((n + 127) / 128);
+  double best = fp8_tiles_us(tiles, G, 1, exact);
+  for (int k : {2, 3, 4, 6, 8}) {
+    if (grouped || G < 2 * k) break;
+    const double us = fp8_tiles_us(tiles, G, k, exact);
+    if (us < best) best = us, p.pieces = k;
+  }
+  const long long mean = grouped ? (b + experts - 1) / experts : b;
+  const int rb = mean <= 16 ? 1 : (mean <= 32 ? 2 : 4);
+  const long long blocks = grouped ? grouped_row_blocks(b, experts, 16 * rb) : (b + 16 * rb - 1) / (16 * rb);
+  if (fp8_rows_us((double)blocks * (double)((n + 15) / 16) * G, rb, grouped) < best) {
+    p.rb = rb;
+    p.pieces = 1;
+    p.split = rows_split(blocks, n, 2 * G, rb);
+    p.threads = 64 * p.split.nwk * p.split.nwc;
     return p;
   }
   p.split.grid = tiles * p.pieces;
