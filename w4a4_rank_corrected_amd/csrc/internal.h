@@ -240,7 +240,7 @@ int launch_combine(const void* rows, int R, int n, int dtype, const int32_t* ind
 
 // ---- the routing of rows to experts ----------------------------------------------
 // The sort's chunks of slots, one per workgroup (a multiple of its threads each).
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 512, kSortChunk = 8 * kSortThreads;
 struct SortPlan {
   int chunk, chunks;
 };

@@ -115,7 +115,7 @@ GroupedPlan grouped_plan(int b, int n, int m, int experts) {
 SortPlan sort_plan(int b) {
   const long long even = ((long long)b + 256LL * kSortThreads - 1) / (256LL * kSortThreads) * kSortThreads;
   SortPlan p;
-  p.chunk = (int)std::max<long long>(8 * kSortThreads, even);
+  p.chunk = (int)std::max<long long>(kSortChunk, even);
   p.chunks = std::max((int)(((long long)b + p.chunk - 1) / p.chunk), 1);
   return p;
 }

@@ -34,14 +34,28 @@ __device__ __forceinline__ int key_of(const int32_t* __restrict__ expert, int s,
   return (unsigned)e < (unsigned)experts ? e : experts;
 }
 
+// A wave's piece is taken 64 kKeys slots at a time, all of their keys loaded together.
+constexpr int kKeys = 8;
+static_assert(kKeys * kSortThreads == kSortChunk, "the usual chunk is one load of keys");
+
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* __restrict__ expert, int b, int chunk,
                                                                   int experts, int32_t* __restrict__ counts) {
   __shared__ int s_count[SVDQ_MAX_EXPERTS + 1];
   const int tid = (int)threadIdx.x, keys = experts + 1;
+  const int lo = (int)blockIdx.x * chunk, hi = min(lo + chunk, b);
   for (int e = tid; e < keys; e += kSortThreads) s_count[e] = 0;
   __syncthreads();
-  const int lo = (int)blockIdx.x * chunk, hi = min(lo + chunk, b);
-  for (int s = lo + tid; s < hi; s += kSortThreads) atomicAdd(&s_count[key_of(expert, s, experts)], 1);
+  for (int s0 = lo + tid; s0 < hi; s0 += kKeys * kSortThreads) {
+    int key[kKeys];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int s = s0 + i * kSortThreads;
+      key[i] = s < hi ? key_of(expert, s, experts) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if (key[i] >= 0) atomicAdd(&s_count[key[i]], 1);
+  }
   __syncthreads();
   for (int e = tid; e < keys; e += kSortThreads) counts[(size_t)blockIdx.x * keys + e] = s_count[e];
 }
@@ -56,13 +70,29 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
   __shared__ int s_total[kSortWaves];
   const int tid = (int)threadIdx.x, lane = tid & 63, keys = experts + 1;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int e = tid; e < keys * kSortWaves; e += kSortThreads) s_next[e] = 0;
-  __syncthreads();
   const int lo = (int)blockIdx.x * chunk, hi = min(lo + chunk, b);
   const int piece = chunk / kSortWaves;
   const int w0 = min(lo + wave * piece, hi), w1 = min(w0 + piece, hi);
+  int key[kKeys];
+  auto load_keys = [&](int s0) {  // slot s0 + 64 i + lane; -1 behind the piece
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int s = s0 + 64 * i + lane;
+      key[i] = s < w1 ? key_of(expert, s, experts) : -1;
+    }
+  };
+  load_keys(w0);
+  for (int e = tid; e < keys * kSortWaves; e += kSortThreads) s_next[e] = 0;
+  __syncthreads();
   int* next = s_next + wave * keys;
-  for (int s = w0 + lane; s < w1; s += 64) atomicAdd(&next[key_of(expert, s, experts)], 1);
+  for (int s0 = w0;;) {
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if (key[i] >= 0) atomicAdd(&next[key[i]], 1);
+    s0 += 64 * kKeys;
+    if (s0 >= w1) break;
+    load_keys(s0);
+  }
   __syncthreads();
   // rows before a key's first one: a scan over the keys, kSortThreads at a time
   int before = 0;
@@ -71,10 +101,15 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
     int total = 0, earlier = 0;  // the key's slots in all chunks, and in those before this one
     if (e < keys) {
       if (counts) {
-        for (int c = 0; c < chunks; ++c) {
-          const int v = counts[(size_t)c * keys + e];
-          total += v;
-          earlier += c < (int)blockIdx.x ? v : 0;
+        for (int c0 = 0; c0 < chunks; c0 += 8) {
+          int v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = c0 + i < chunks ? counts[(size_t)(c0 + i) * keys + e] : 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            total += v[i];
+            earlier += c0 + i < (int)blockIdx.x ? v[i] : 0;
+          }
         }
       } else {
 #pragma unroll
@@ -108,24 +143,30 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
     }
     __syncthreads();
   }
-  for (int s0 = w0; s0 < w1; s0 += 64) {
-    const int s = s0 + lane;
-    const bool live = s < w1;
-    const int key = live ? key_of(expert, s, experts) : 0;
-    uint64_t same = __ballot(live);
-    for (int i = 0; i < bits; ++i) {
-      const uint64_t set = __ballot(key >> i & 1);
-      same &= key >> i & 1 ? set : ~set;
+  if (piece > 64 * kKeys) load_keys(w0);  // (otherwise they are there)
+  for (int s0 = w0; s0 < w1;) {
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      if (s0 + 64 * i >= w1) break;
+      const int s = s0 + 64 * i + lane;
+      const bool live = key[i] >= 0;
+      uint64_t same = __ballot(live);
+      for (int d = 0; d < bits; ++d) {
+        const uint64_t set = __ballot(key[i] >> d & 1);
+        same &= key[i] >> d & 1 ? set : ~set;
+      }
+      const int rank = __popcll(same & ((1ULL << lane) - 1));
+      if (live) {
+        const int row = next[key[i]] + rank;
+        // the wave's lanes have read their rows before the last lane of each key
+        // moves it on: LDS accesses of a wave complete in order
+        if (rank + 1 == __popcll(same)) next[key[i]] = row + 1;
+        index[s] = key[i] < experts ? row : -1 - row;
+        row_index[row] = s / k;
+      }
     }
-    const int rank = __popcll(same & ((1ULL << lane) - 1));
-    if (live) {
-      const int row = next[key] + rank;
-      // the wave's lanes have read their rows before the last lane of each key
-      // moves it on: LDS accesses of a wave complete in order
-      if (rank + 1 == __popcll(same)) next[key] = row + 1;
-      index[s] = key < experts ? row : -1 - row;
-      row_index[row] = s / k;
-    }
+    s0 += 64 * kKeys;
+    if (s0 < w1) load_keys(s0);
   }
 }
 
@@ -148,9 +189,13 @@ struct RowVector {
   static constexpr int W = BF16 ? 8 : 4;  // columns of 16 bytes
   typedef typename std::conditional<BF16, uint16_t, uint32_t>::type Element;
   typedef typename std::conditional<BF16, u32x4_at2, u32x4_at4>::type Loose;  // gfx950 takes any element's address
+  template <bool ONCE>  // read this once only
   static __device__ __forceinline__ u32x4 get(const void* base, long long row, int n, int j) {
     const Element* p = reinterpret_cast<const Element*>(base) + (size_t)row * n + j;
-    if (j + W <= n) return *reinterpret_cast<const Loose*>(p);
+    if (j + W <= n) {
+      if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const Loose*>(p));
+      return *reinterpret_cast<const Loose*>(p);
+    }
     u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int e = 0; e < W; ++e)
@@ -165,7 +210,10 @@ struct RowVector {
   static __device__ __forceinline__ void put(void* base, long long row, int n, int j, const u32x4& v) {
     Element* p = reinterpret_cast<Element*>(base) + (size_t)row * n + j;
     if (j + W <= n) {
-      *reinterpret_cast<Loose*>(p) = v;
+      // past the L2: rows come in at their place once, and evicting what is read for them
+      // costs more (4096 x 6 rows of 2048: gradient bf16 53.6 -> 39.4 us, dispatch fp32
+      // 51.4 -> 41.1)
+      __builtin_nontemporal_store(v, reinterpret_cast<Loose*>(p));
       return;
     }
 #pragma unroll
@@ -209,13 +257,13 @@ __global__ __launch_bounds__(256) void scatter_rows_kernel(const void* __restric
       for (int j0 = part * 64 * W; j0 < n; j0 += nw * 64 * W) {
         const int j = j0 + lane * W;
         if (j >= n) continue;
-        const u32x4 xv = V::get(x, t, n, j);
+        const u32x4 xv = V::template get<false>(x, t, n, j);
         u32x4 rv[kRouteBatch];
         if constexpr (DOT) {
 #pragma unroll
           for (int q = 0; q < kRouteBatch; ++q) {
             rv[q] = u32x4{0u, 0u, 0u, 0u};
-            if (row[q] >= 0) rv[q] = V::get(rows, row[q], n, j);
+            if (row[q] >= 0) rv[q] = V::template get<true>(rows, row[q], n, j);
           }
 #pragma unroll
           for (int q = 0; q < kRouteBatch; ++q)
@@ -290,9 +338,13 @@ int launch_scatter_rows(const void* x, int t, int n, int dtype, const int32_t* i
                         const void* rows, int R, void* drows, float* dweight, void* stream) {
   const bool bf = dtype == SVDQ_OUT_BF16;
   const int units = (n + (bf ? 512 : 256) - 1) / (bf ? 512 : 256);  // a wave's chunks in a row
-  // one wave a token where that fills the chip
+  // Waves of a token: a whole chunk each, or a part where tokens alone do not fill the
+  // chip (4096 tokens x 6 rows of 2048, other rows every call: gradient bf16 57 us with
+  // one, 60 with two, 50 with four, fp32 105, 108, 91; 4096 x 2 rows of 1001 bf16:
+  // dispatch 7.9 with one, 8.8 with two; 300 x 6 rows of 4608 bf16: 18.9, 12.5, 9.8).
+  const int whole = n / (bf ? 512 : 256);
   int nw = 1;
-  while (nw < 4 && 2 * nw <= units && (long long)t * nw < 8 * kMaxCUs) nw *= 2;
+  while (nw < 4 && (2 * nw <= whole || (2 * nw <= units && (long long)t * nw < 8 * kMaxCUs))) nw *= 2;
   const int grid = (int)(((long long)t * nw + 3) / 4);
   auto go = [&](auto kernel) {
     return launch_checked(kernel, grid, 256, (hipStream_t)stream, x, t, n, index, weight, k, rows, R, drows, dweight,
