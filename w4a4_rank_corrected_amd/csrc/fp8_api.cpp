@@ -98,6 +98,13 @@ Fp8Workspace fp8_ws_layout(int rows, int m, size_t gemm) {
   return w;
 }
 
+// Whether no element of y lies in x's span of memory.
+bool apart_from_x(const uint16_t* x, int b, int m, const EpiArgs& ep, int n, int y_dtype) {
+  const uintptr_t px = (uintptr_t)x, py = (uintptr_t)ep.y;
+  const uintptr_t bytes_y = ((uintptr_t)(b - 1) * ep.ldy + n) * (y_dtype == SVDQ_OUT_F32 ? 4 : 2);
+  return px + (uintptr_t)b * m * 2 <= py || py + bytes_y <= px;
+}
+
 Fp8Args product_args(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer& L, int b, const EpiArgs& ep) {
   return Fp8Args{qx, ascale, L.qw, L.wscale, L.bias, nullptr, b, b, L.n, fp8_blocks(L.m), {nullptr, 0}, ep};
 }
@@ -174,6 +181,11 @@ int svdq_fp8_linear(const uint16_t* x, const svdq_fp8_layer* layer, const svdq_e
   if (!st) st = check_workspace(workspace, workspace_bytes, w.total, kAlign);
   if (st) return st;
   uint8_t* ws = (uint8_t*)workspace;
+  // few blocks of x: every workgroup of the product quantizes them itself, unless y is
+  // written where x may still be read
+  if (plan.rb == 1 && (long long)fp8_blocks(layer->m) * b <= kFp8FusedBlocks && apart_from_x(x, b, layer->m, ep, layer->n, y_dtype))
+    return hip_status(launch_fp8_rows_x(product_args(ws, ws + w.as_off, *layer, b, ep), x, layer->m, plan, y_dtype, stream),
+                      "fp8_gemm");
   st = hip_status(launch_fp8_act(x, b, layer->m, ws, ws + w.as_off, stream), "fp8_quantize_act");
   if (st) return st;
   return hip_status(launch_fp8_gemm(product_args(ws, ws + w.as_off, *layer, b, ep), plan, y_dtype, ws + w.gemm_off, stream),

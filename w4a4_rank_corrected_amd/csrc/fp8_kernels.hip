@@ -131,13 +131,21 @@ __global__ __launch_bounds__(256) void fp8_weight_kernel(const void* __restrict_
 // workgroup's waves, nwk split the channel blocks of the same columns (wave k
 // takes blocks k, k + nwk, ...; sums added in LDS in wave order), nwc take
 // neighbouring columns.
+//
+// X (one layer, RB 1): a.qx is x itself in bf16, m channels a row, and every workgroup
+// quantizes the few blocks there are into LDS while its first weights are on their way:
+// one launch instead of two for a row or a few (1 x 1152 -> 6912: 6.4 us, and 2.2 for
+// the quantization before it).
 // ---------------------------------------------------------------------------
 constexpr int fp8_rows_depth(int rb) { return rb == 1 ? 4 : (rb == 2 ? 3 : 2); }
 
-template <int RB, bool OUT_BF16, bool GROUPED>
-__global__ __launch_bounds__(RB == 4 ? 512 : 1024) void fp8_rows_kernel(Fp8Args a, int nwk, int nwc) {
+template <int RB, bool OUT_BF16, bool GROUPED, bool X>
+__global__ __launch_bounds__(RB == 4 ? 512 : 1024) void fp8_rows_kernel(Fp8Args a, int nwk, int nwc, int m) {
+  static_assert(!X || (RB == 1 && !GROUPED), "");
   extern __shared__ __align__(16) uint8_t fp8_rows_lds[];
   f32x4* part = reinterpret_cast<f32x4*>(fp8_rows_lds);  // [wave][row block][lane]
+  uint8_t* s_code = fp8_rows_lds + nwk * nwc * RB * 1024;  // X: records [G][b][128], then scales [G][b]
+  uint8_t* s_scale = s_code + a.G * a.b * 128;
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ct = wave / nwk, wk = wave - ct * nwk;
@@ -193,6 +201,7 @@ __global__ __launch_bounds__(RB == 4 ? 512 : 1024) void fp8_rows_kernel(Fp8Args 
     st.w[0] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, w_off, 0, 0));
     st.w[1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, w_off + 16u, 0, 0));
     st.sw = __builtin_amdgcn_raw_buffer_load_b8(rs, (uint32_t)j0 / 128u, 0, 0);
+    if constexpr (X) return;
 #pragma unroll
     for (int q = 0; q < RB; ++q) {
       const uint32_t off = src[q] * 128u + 32u * c;
@@ -204,7 +213,17 @@ __global__ __launch_bounds__(RB == 4 ? 512 : 1024) void fp8_rows_kernel(Fp8Args 
   f32x4 acc[RB];
 #pragma unroll
   for (int q = 0; q < RB; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](const Stage& st) {
+  auto compute = [&](int k, Stage& st) {
+    if constexpr (X) {
+      const int at = (wk + nwk * k) * a.b + r;
+      st.x[0][0] = st.x[0][1] = u32x4{0u, 0u, 0u, 0u};
+      st.sx[0] = 0;
+      if (r < a.b) {
+        st.x[0][0] = *reinterpret_cast<const u32x4*>(s_code + at * 128 + 32 * c);
+        st.x[0][1] = *reinterpret_cast<const u32x4*>(s_code + at * 128 + 32 * c + 16);
+        st.sx[0] = s_scale[at];
+      }
+    }
 #pragma unroll
     for (int q = 0; q < RB; ++q)
 #pragma unroll
@@ -229,17 +248,29 @@ __global__ __launch_bounds__(RB == 4 ? 512 : 1024) void fp8_rows_kernel(Fp8Args 
   const bool mine = tid < nwc * RB * 64 && unit_at(tid, ui, uj);
   EpiLoads el;
   if (mine) el = load_unit<OUT_BF16>(ui, uj, n, bias, a.ep);
+  if constexpr (X) {
+    // sixteen lanes a block, as fp8_act_kernel
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(a.qx);
+    for (int blk = tid >> 4; blk < a.b * G; blk += (int)blockDim.x >> 4) {
+      const int g = blk / a.b, row = blk - g * a.b;
+      const u32x4 v = load_bf16x8(x + (size_t)row * m, g * 128 + 8 * (tid & 15), m);
+      const int byte = block_scale_bf16(block_max16(v));
+      *reinterpret_cast<uint2*>(s_code + blk * 128 + 8 * (tid & 15)) = encode8(v, byte);
+      if ((tid & 15) == 0) s_scale[blk] = (uint8_t)stored_scale(byte);
+    }
+    __syncthreads();
+  }
   int k = 0;
   for (; k + D <= nk; k += D) {
 #pragma unroll
     for (int u = 0; u < D; ++u) {
-      compute(st[u]);
+      compute(k + u, st[u]);
       load(k + u + D, st[u]);
     }
   }
 #pragma unroll
   for (int u = 0; u + 1 < D; ++u)
-    if (k + u < nk) compute(st[u]);
+    if (k + u < nk) compute(k + u, st[u]);
 
 #pragma unroll
   for (int q = 0; q < RB; ++q) part[(wave * RB + q) * 64 + lane] = acc[q];
@@ -255,15 +286,15 @@ __global__ __launch_bounds__(RB == 4 ? 512 : 1024) void fp8_rows_kernel(Fp8Args 
     if (unit_at(u, ui, uj)) finish_unit<OUT_BF16>(sum(u), load_unit<OUT_BF16>(ui, uj, n, bias, a.ep), ui, uj, n, a.ep);
 }
 
-template <int RB, bool OUT_BF16, bool GROUPED>
-int launch_fp8_rows_typed(const Fp8Args& a, const RowsSplit& s, hipStream_t st) {
-  auto kernel = fp8_rows_kernel<RB, OUT_BF16, GROUPED>;
+template <int RB, bool OUT_BF16, bool GROUPED, bool X = false>
+int launch_fp8_rows_typed(const Fp8Args& a, const RowsSplit& s, hipStream_t st, int m = 0) {
+  auto kernel = fp8_rows_kernel<RB, OUT_BF16, GROUPED, X>;
   const int threads = 64 * s.nwk * s.nwc;
   if (!launch_fits(s.grid, threads)) return (int)hipErrorInvalidConfiguration;
   const int ok = scratch_free(reinterpret_cast<const void*>(kernel));
   if (ok != 0) return ok;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)s.grid), dim3((unsigned)threads), (size_t)s.nwk * s.nwc * RB * 1024, st, a,
-                     s.nwk, s.nwc);
+  const size_t lds = (size_t)s.nwk * s.nwc * RB * 1024 + (X ? (size_t)a.G * a.b * 129 : 0);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)s.grid), dim3((unsigned)threads), lds, st, a, s.nwk, s.nwc, m);
   return (int)hipGetLastError();
 }
 
@@ -300,6 +331,14 @@ int launch_fp8_rows(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* st
   if (plan.rb == 2) return launch_fp8_rows_rb<2>(a, plan.split, bf, st);
   if (plan.rb == 4) return launch_fp8_rows_rb<4>(a, plan.split, bf, st);
   return (int)hipErrorInvalidValue;
+}
+
+int launch_fp8_rows_x(const Fp8Args& a, const uint16_t* x, int m, const Fp8Plan& plan, int y_dtype, void* stream) {
+  if (plan.rb != 1 || a.groups.offsets || (long long)a.G * a.b > kFp8FusedBlocks) return (int)hipErrorInvalidValue;
+  Fp8Args f = a;
+  f.qx = reinterpret_cast<const uint8_t*>(x);
+  return y_dtype == SVDQ_OUT_BF16 ? launch_fp8_rows_typed<1, true, false, true>(f, plan.split, (hipStream_t)stream, m)
+                                  : launch_fp8_rows_typed<1, false, false, true>(f, plan.split, (hipStream_t)stream, m);
 }
 
 int launch_fp8_gemm(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream) {
