@@ -359,7 +359,7 @@ def ragged(rng, E, b, pad):
 
 
 GROUPED = [(1, 1, 64, 1, 0), (1, 30, 130, 70, 0), (3, 5, 200, 33, 0), (4, 70, 1024, 130, 9), (8, 300, 640, 200, 0),
-           (64, 90, 128, 40, 5), (65, 300, 300, 24, 0), (5, 700, 256, 300, 3), (3, 900, 129, 150, 0), (1024, 700, 64, 8, 0)]
+           (64, 90, 128, 40, 5), (65, 300, 300, 24, 0), (5, 700, 256, 300, 3), (3, 900, 129, 150, 0), (2, 2300, 260, 300, 5), (1024, 700, 64, 8, 0)]
 
 
 @pytest.mark.parametrize("E,b,m,n,pad", GROUPED)

@@ -438,6 +438,43 @@ __global__ __launch_bounds__(512) void fp8_big_kernel(Fp8Args a, int tiles_m, in
   }
 }
 
+// The tile of rows sorted by expert that this workgroup takes (grouped.h), with its
+// expert's operands; false: none.  An expert's row blocks of one column block are
+// neighbours: they share its weights in L2.
+struct GroupedTile {
+  const uint8_t *qw, *wscale;
+  const uint16_t* bias;
+  int i0, j0, row_end;
+};
+template <int TM, int TN>
+__device__ __forceinline__ bool grouped_tile(const Fp8Args& a, int tiles_n, GroupedTile& t) {
+  const GroupTile g = find_tile<TM>(a.groups.offsets, a.groups.experts, a.b, tiles_n, (int)blockIdx.x,
+                                    [](int d, int T) { return xcd_range(d, T); });
+  if (!g.live) return false;
+  const int tj = g.u / g.blocks;
+  const size_t e = (size_t)g.expert;
+  t.qw = a.qw + e * a.G * (size_t)a.n * 128;
+  t.wscale = a.wscale + e * a.G * ((a.n + 127) / 128);
+  t.bias = a.bias ? a.bias + e * a.n : nullptr;
+  t.i0 = g.lo + (g.u - tj * g.blocks) * TM;
+  t.j0 = tj * TN;
+  t.row_end = g.hi;
+  return true;
+}
+
+// 256 x 256 for experts of many rows.
+__global__ __launch_bounds__(512) void fp8_big_grouped_kernel(Fp8Args a, int tiles_n) {
+  typedef TileShape<8, 2, 4> Shape;
+  __shared__ __align__(16) uint8_t s_even[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_odd[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_scale_even[Shape::kScales];
+  __shared__ __align__(16) uint8_t s_scale_odd[Shape::kScales];
+  GroupedTile t;
+  if (!grouped_tile<256, 256>(a, tiles_n, t)) return;  // the whole workgroup
+  tile<8, 2, 4, false, true, true, false>(a, a.qx, a.ascale, t.qw, t.wscale, t.bias, a.G, t.i0, t.j0, t.row_end, s_even,
+                                          s_odd, s_scale_even, s_scale_odd, nullptr);
+}
+
 // Tiles of 128 x 128, two workgroups a CU: experts' rows, fp32 results, and few tiles,
 // which may be split along the channels (PIECES: piece p of tile u takes every block
 // from p G / pieces to (p + 1) G / pieces and leaves its sums in slot u pieces + p).
@@ -453,17 +490,14 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8Args a, int tiles_m, i
   const int NB = (a.n + 127) / 128;
   int i0, j0, row_end, G = a.G;
   if constexpr (GROUPED) {
-    const GroupTile g = find_tile<128>(a.groups.offsets, a.groups.experts, a.b, tiles_n, (int)blockIdx.x,
-                                       [](int d, int T) { return xcd_range(d, T); });
-    if (!g.live) return;  // the whole workgroup
-    const int tj = g.u / g.blocks;
-    i0 = g.lo + (g.u - tj * g.blocks) * 128;
-    j0 = tj * 128;
-    row_end = g.hi;
-    const size_t e = (size_t)g.expert;
-    qw += e * G * (size_t)a.n * 128;
-    wscale += e * G * NB;
-    if (bias) bias += e * a.n;
+    GroupedTile t;
+    if (!grouped_tile<128, 128>(a, tiles_n, t)) return;  // the whole workgroup
+    qw = t.qw;
+    wscale = t.wscale;
+    bias = t.bias;
+    i0 = t.i0;
+    j0 = t.j0;
+    row_end = t.row_end;
   } else {
     const int u = xcd_range((int)blockIdx.x, tiles_m * tiles_n * pieces);
     int ti, tj;
@@ -519,6 +553,7 @@ int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& p, int y_dtype, void* ws, 
   const bool exact = y_dtype == SVDQ_OUT_F32;
   if (p.big) {
     const int tm = (a.b + 255) / 256, tn = (a.n + 255) / 256;
+    if (a.groups.offsets) return launch_checked(fp8_big_grouped_kernel, p.split.grid, 512, st, a, tn);
     auto go = [&](auto kernel) { return launch_checked(kernel, p.split.grid, 512, st, a, tm, tn, p.full); };
     return p.parts == 1 ? go(fp8_big_kernel<1>) : p.parts == 2 ? go(fp8_big_kernel<2>) : go(fp8_big_kernel<4>);
   }

@@ -155,6 +155,9 @@ double fp8_rows_us(double steps, int rb, bool grouped) {
 //     smaller where the tiles left over are few: 4608 x 4608 -> 12288 (96 of 864 left)
 //     212 whole, 204 in halves, 216 in quarters; 4096 x 1152 -> 4608 (32 of 288) 36.5,
 //     31.5, 29.1; 4608 x 3072 -> 9216 (136 of 648) 112, 125, 132;
+//   * the same for experts of 1024 rows on average and more (8 experts, 4096 -> 4096,
+//     mean 2048: 314 by 128 x 128, 252; 1024: 150, 143; 512: 82, 95; 1152 -> 4608, mean
+//     1024: 59.5, 56.7): below, half-empty last row blocks cost more;
 //   * otherwise tiles of 128 x 128, one layer's in the pieces that are quickest, or the
 //     row kernel, whichever the estimates above say is quicker.
 Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
@@ -171,6 +174,13 @@ Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
     p.threads = 512;
     return p;
   }
+  const long long mean = grouped ? (b + experts - 1) / experts : b;
+  if (grouped && !exact && mean >= 1024) {
+    p.big = 1;
+    p.split.grid = grouped_row_blocks(b, experts, 256) * ((n + 255) / 256);
+    p.threads = 512;
+    return p;
+  }
   const long long tiles = (grouped ? grouped_row_blocks(b, experts, 128) : (b + 127) / 128) * ((n + 127) / 128);
   double best = fp8_tiles_us(tiles, G, 1, exact);
   for (int k : {2, 3, 4, 6, 8}) {
@@ -178,7 +188,6 @@ Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
     const double us = fp8_tiles_us(tiles, G, k, exact);
     if (us < best) best = us, p.pieces = k;
   }
-  const long long mean = grouped ? (b + experts - 1) / experts : b;
   const int rb = mean <= 16 ? 1 : (mean <= 32 ? 2 : 4);
   const long long blocks = grouped ? grouped_row_blocks(b, experts, 16 * rb) : (b + 16 * rb - 1) / (16 * rb);
   if (fp8_rows_us((double)blocks * (double)((n + 15) / 16) * G, rb, grouped) < best) {
