@@ -724,11 +724,19 @@ int svdq_combine_rows_grad(const void* dy, int t, int n, int dtype, const int32_
  *           a NaN has e = 0 and the NaN code 0x7F everywhere, so that its row (or
  *           its columns) of Y is NaN.
  *   v[i,j] = sum_g 2^(ex[g,i] + ew[g,j/128]) sum_{k in g} cx[i,k] cw[k,j] + bias[j]
- * Scaling by powers of two is exact and the matrix instruction applies it, so
- * that the products of all blocks run through its accumulators in fp32.
+ * Scaling by powers of two is exact, and sums are held in fp32.  How the products
+ * of a block are added depends on y's type:
+ *   fp32 y, and bf16 y of few rows: the scaled codes as bf16 (exact) through the
+ *     bf16 matrix instruction, which adds exact products in fp32;
+ *   bf16 y of many rows: the 8-bit matrix instruction, which adds the products of
+ *     eight neighbouring channels at the exponent of the largest and keeps 13 bits
+ *     below it (and adds those sums in fp32).  For v's sum that is an error of some
+ *     10^-5 of the sum of the products' magnitudes, where y's rounding is 2^-8 of y;
+ *     fp32 results of the same would show it.
  * Layouts, G = ceil(m / 128):
  *   codes of X   [G][rows][128]: byte t of a record is channel 128 g + t's code,
- *                zero behind channel m - 1;   scales of X  [G][rows].
+ *                zero behind channel m - 1 (X: of any value in a block of NaN);
+ *                scales of X  [G][rows].
  *   codes of W   [G][n][128], likewise;       scales of W  [G][ceil(n / 128)].
  * m and n are any dimensions here (1 .. SVDQ_MAX_DIM).
  * ========================================================================= */
@@ -767,16 +775,17 @@ int svdq_fp8_quantize_weights(const void* W, int w_dtype, int experts, int m, in
 int svdq_fp8_quantize_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t* ascale, void* stream);
 
 /* DEVICE: the product with an epilogue (epi NULL: none) of svdq_*_epi's kind.
- * The order of the fp32 sums depends only on the shape and the device's CU
- * count.  Workspace: 16-byte aligned, >= svdq_fp8_gemm_workspace_size(b, n, m)
- * bytes (0 where no tile is split), one for each of the calls that overlap in
+ * The order of the fp32 sums depends only on the shape and y's type.  Workspace:
+ * 16-byte aligned, >= svdq_fp8_gemm_workspace_size(b, n, m) bytes (0 where no tile
+ * is split for either type of y), one for each of the calls that overlap in
  * time. */
 size_t svdq_fp8_gemm_workspace_size(int b, int n, int m);
 int svdq_fp8_gemm(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer* layer, const svdq_epilogue* epi, int b,
                   void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
-/* DEVICE: the whole layer, quantization and product.  x may be y (and the
- * residual).  Workspace: 256-byte aligned, >= svdq_fp8_linear_workspace_size
+/* DEVICE: the whole layer, quantization and product (a row or a few in one
+ * launch).  x bf16 [b][m], element alignment; it may be y (and the residual).
+ * Workspace: 256-byte aligned, >= svdq_fp8_linear_workspace_size
  * bytes. */
 size_t svdq_fp8_linear_workspace_size(int b, int m, int n);
 int svdq_fp8_linear(const uint16_t* x, const svdq_fp8_layer* layer, const svdq_epilogue* epi, int b, void* y,
@@ -794,7 +803,8 @@ int svdq_fp8_grouped_gemm(const uint8_t* qx, const uint8_t* ascale, int x_rows, 
                           const int32_t* offsets, const svdq_fp8_grouped_layer* layer, const svdq_epilogue* epi, int b,
                           void* y, int y_dtype, void* stream);
 
-/* DEVICE: x's x_rows rows quantized, then the product above.  x may be y.
+/* DEVICE: x's x_rows rows (bf16 [x_rows][m], element alignment) quantized, then
+ * the product above.  x may be y.
  * Workspace: 256-byte aligned, >= svdq_fp8_grouped_linear_workspace_size bytes,
  * not shared by calls that overlap in time. */
 size_t svdq_fp8_grouped_linear_workspace_size(int b, int x_rows, int experts, int m, int n);

@@ -205,9 +205,12 @@ def test_transposed_layer_has_the_same_values(S):
 # products
 # ---------------------------------------------------------------------------
 
+# one row and a few (quantized in the product's kernel or before it), the row kernel, whole and split tiles of 128 x 128,
+# tiles of 256 x 256 with a last round whole, in halves and in quarters
 SHAPES = [(1, 1, 1), (1, 8192, 40), (1, 8193, 40), (4, 2048, 33), (9, 900, 20), (16, 512, 70), (1, 128, 16), (1, 1152, 700), (2, 130, 33), (7, 1000, 513), (16, 256, 128), (17, 384, 130), (33, 700, 64),
           (64, 2048, 96), (65, 129, 257), (130, 640, 300), (257, 1152, 200), (300, 4200, 72), (512, 300, 520),
-          (2048, 130, 257), (2300, 400, 513), (2500, 1100, 300)]
+          (2048, 130, 257), (2300, 400, 513), (2500, 1100, 300),
+          (300, 4608, 700), (400, 4700, 1100), (129, 8192, 1000), (4100, 140, 2300), (4608, 130, 4800), (4350, 260, 4150), (4096, 128, 4096)]
 
 
 @pytest.mark.parametrize("b,m,n", SHAPES)
@@ -433,10 +436,10 @@ def test_same_inputs_same_bits_and_side_stream(S):
         assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("b", [1, 40, 300])
-def test_graphs_on_two_streams(S, b):
+@pytest.mark.parametrize("b,m", [(1, 1024), (40, 1024), (300, 1024), (300, 4608), (2100, 1024)])
+def test_graphs_on_two_streams(S, b, m):
     """Two captured calls, each with a workspace of its own, replayed together on new inputs."""
-    m, n = 1024, 200
+    n = 4100 if b > 2000 else (700 if m > 4000 else 200)
     X = Layer(S, m, n, seed=12)
     xs = [dev_bf16(rows_like(np.random.default_rng([b, i]), b, m)) for i in range(8)]
     want = [S.svdq_fp8_linear(x, X.layer, act="silu") for x in xs]

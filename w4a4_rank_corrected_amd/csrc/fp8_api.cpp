@@ -127,8 +127,9 @@ int svdq_fp8_quantize_weights(const void* W, int w_dtype, int experts, int m, in
   REQUIRE(W && qw && wscale, SVDQ_ERR_INVALID_ARG, "W, qw and wscale must not be NULL");
   REQUIRE(element_aligned(W, w_dtype), SVDQ_ERR_ALIGNMENT, "W must be element-aligned");
   REQUIRE(aligned16(qw), SVDQ_ERR_ALIGNMENT, "qw must be 16-byte aligned");
-  // (2^24 workgroups of 16 KB of codes are 256 GB)
-  REQUIRE(experts <= SVDQ_MAX_DIM && (long long)fp8_blocks(m) * fp8_blocks(n) <= (1LL << 24) / experts,
+  // a workgroup of 256 threads for each block of 16 KB of codes
+  REQUIRE(experts <= SVDQ_MAX_DIM &&
+              launch_fits(std::min((long long)fp8_blocks(m) * fp8_blocks(n), 1LL << 30) * experts, 256),
           SVDQ_ERR_UNSUPPORTED, "too many weights (experts=%d, m=%d, n=%d)", experts, m, n);
   return hip_status(launch_fp8_weights(W, w_dtype, experts, m, n, transposed != 0, qw, wscale, stream),
                     "fp8_quantize_weights");
