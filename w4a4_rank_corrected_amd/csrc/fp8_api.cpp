@@ -184,7 +184,7 @@ int svdq_fp8_linear(const uint16_t* x, const svdq_fp8_layer* layer, const svdq_e
   uint8_t* ws = (uint8_t*)workspace;
   // few blocks of x: every workgroup of the product quantizes them itself, unless y is
   // written where x may still be read
-  if (plan.rb == 1 && (long long)fp8_blocks(layer->m) * b <= kFp8FusedBlocks && apart_from_x(x, b, layer->m, ep, layer->n, y_dtype))
+  if (plan.rb == 1 && b <= 16 && fp8_blocks(layer->m) * b <= kFp8FusedBlocks && apart_from_x(x, b, layer->m, ep, layer->n, y_dtype))
     return hip_status(launch_fp8_rows_x(product_args(ws, ws + w.as_off, *layer, b, ep), x, layer->m, plan, y_dtype, stream),
                       "fp8_gemm");
   st = hip_status(launch_fp8_act(x, b, layer->m, ws, ws + w.as_off, stream), "fp8_quantize_act");

@@ -334,7 +334,7 @@ int launch_fp8_rows(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* st
 }
 
 int launch_fp8_rows_x(const Fp8Args& a, const uint16_t* x, int m, const Fp8Plan& plan, int y_dtype, void* stream) {
-  if (plan.rb != 1 || a.groups.offsets || (long long)a.G * a.b > kFp8FusedBlocks) return (int)hipErrorInvalidValue;
+  if (plan.rb != 1 || a.b > 16 || a.groups.offsets || a.G * a.b > kFp8FusedBlocks) return (int)hipErrorInvalidValue;
   Fp8Args f = a;
   f.qx = reinterpret_cast<const uint8_t*>(x);
   return y_dtype == SVDQ_OUT_BF16 ? launch_fp8_rows_typed<1, true, false, true>(f, plan.split, (hipStream_t)stream, m)

@@ -285,7 +285,7 @@ int launch_fp8_weights(const void* w, int dtype, int experts, int m, int n, bool
                        uint8_t* wscale, void* stream);
 int launch_fp8_rows(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* stream);
 int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& plan, int y_dtype, void* ws, void* stream);
-// The row kernel on x itself: rb 1, one layer, at most kFp8FusedBlocks blocks of x (four
+// The row kernel on x itself: up to 16 rows of one layer, at most kFp8FusedBlocks blocks (four
 // or fewer for each 16 lanes of a workgroup, 8 KB of LDS).
 constexpr int kFp8FusedBlocks = 64;
 int launch_fp8_rows_x(const Fp8Args& a, const uint16_t* x, int m, const Fp8Plan& plan, int y_dtype, void* stream);

@@ -137,13 +137,14 @@ double fp8_tiles_us(long long tiles, int G, int k, bool exact) {
 }
 
 // The same by the row kernel, for `steps` of 16 rb rows x 16 columns x 128 channels:
-//   one layer: 1 row, 1152 -> 6912 5.8; 16 rows, 8192 -> 8192 19.3; 32: 25.7; 64: 42.7;
-//   100, 2048 -> 2048 8.6; 333, 1000 -> 1500 11.4; 256, 4608 -> 1152 25.6;
+//   one layer, us for rb 1 / 2 / 4: 64 rows, 2048 -> 2048 7.5 / 7.3 / 8.5; 179, 1344 -> 256
+//   4.6 / 5.3 / 7.0; 333, 1000 -> 1500 11.8 / 11.9 / 11.4; 100, 2048 -> 2048 11.5 / 9.2 / 8.6;
+//   64, 8192 -> 8192 62 / 48 / 43; 16 rows of it 19.3 with rb 1;
 //   64 experts, 2048 -> 1408, mean rows 1: 21.7 (tiles 15.1), 8: 52.9 (21.9), 32: 110 (37);
 //   8 experts, 4096 -> 1152, mean 1: 9.3 (18.9), 8: 16.1 (23.6), 16: 19.3 (23.5), 32: 27.4 (24.1)
 double fp8_rows_us(double steps, int rb, bool grouped) {
   if (grouped) return 3.5 + (rb == 1 ? 0.00035 : 0.0006) * steps;
-  return rb == 1 ? 3.5 + 0.0005 * steps : (rb == 2 ? 4.0 + 0.0007 * steps : 4.5 + 0.0014 * steps);
+  return rb == 1 ? 3.5 + 0.0005 * steps : (rb == 2 ? 4.0 + 0.0007 * steps : 6.3 + 0.0011 * steps);
 }
 
 }  // namespace
@@ -188,12 +189,17 @@ Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
     const double us = fp8_tiles_us(tiles, G, k, exact);
     if (us < best) best = us, p.pieces = k;
   }
-  const int rb = mean <= 16 ? 1 : (mean <= 32 ? 2 : 4);
-  const long long blocks = grouped ? grouped_row_blocks(b, experts, 16 * rb) : (b + 16 * rb - 1) / (16 * rb);
-  if (fp8_rows_us((double)blocks * (double)((n + 15) / 16) * G, rb, grouped) < best) {
+  for (int rb : {1, 2, 4}) {
+    if (grouped && rb != (mean <= 16 ? 1 : (mean <= 32 ? 2 : 4))) continue;
+    const long long blocks = grouped ? grouped_row_blocks(b, experts, 16 * rb) : (b + 16 * rb - 1) / (16 * rb);
+    const double us = fp8_rows_us((double)blocks * (double)((n + 15) / 16) * G, rb, grouped);
+    if (us >= best) continue;
+    best = us;
     p.rb = rb;
-    p.pieces = 1;
     p.split = rows_split(blocks, n, 2 * G, rb);
+  }
+  if (p.rb) {
+    p.pieces = 1;
     p.threads = 64 * p.split.nwk * p.split.nwc;
     return p;
   }
