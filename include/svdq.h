@@ -727,7 +727,9 @@ int svdq_combine_rows_grad(const void* dy, int t, int n, int dtype, const int32_
  * Scaling by powers of two is exact, and sums are held in fp32.  How the products
  * of a block are added depends on y's type:
  *   fp32 y, and bf16 y of few rows: the scaled codes as bf16 (exact) through the
- *     bf16 matrix instruction, which adds exact products in fp32;
+ *     bf16 matrix instruction, which adds exact products in fp32.  At the ends of
+ *     bf16's range that rounds: a weight below 2^-126 to a multiple of 2^-133, and
+ *     a value from 31/16 2^127 on, whose code stands for 2^128, to an infinity;
  *   bf16 y of many rows: the 8-bit matrix instruction, which adds the products of
  *     eight neighbouring channels at the exponent of the largest and keeps 13 bits
  *     below it (and adds those sums in fp32).  For v's sum that is an error of some

@@ -350,6 +350,29 @@ def test_extreme_scales(S, rows, out):
     close(S.svdq_fp8_linear(dev_bf16(x), lay, out_dtype=dtype_of(out)), *R.epilogue(v, dv, out=out))
 
 
+@pytest.mark.parametrize("rows,out", [(4, "f32"), (6, "bf16"), (100, "f32"), (2100, "bf16")])
+def test_ends_of_the_range(S, rows, out):
+    """The least scales of W (weights down to 2^-135) beside the largest of X.  As bf16 a weight is off by half a
+    step of 2^-133 at most."""
+    m, n = 384, 300
+    rng = np.random.default_rng(17)
+    w = rng.standard_normal((n, m)) * 2.0 ** -120 * np.exp2(-16.0 * rng.random((n, m)))
+    w[:, :128] = rng.integers(-20, 20, (n, 128)) * 2.0 ** -135
+    w = w.astype(np.float32).astype(np.float64)
+    x = rng.standard_normal((6, m)) * 2.0 ** 124
+    x[3] = rng.uniform(-1.9, 1.9, m) * 2.0 ** 127
+    x = R.bf16(x)
+    x = np.tile(x, (-(-rows // 6), 1))[:rows]
+    lay = S.DeviceLayerFp8(torch.from_numpy(w).float().cuda(), transposed=True)
+    xq, wq = F.quantize(x, 1), F.quantize(w, 128)
+    assert wq[1].min() == -126 and xq[1].max() == 120
+    v, dv = R.product_values(xq[2], wq[2], m)
+    dv = dv + 2.0 ** -134 * np.abs(xq[2]).sum(1, keepdims=True)
+    if out == "bf16":
+        dv = dv + F.aligned(xq, wq)
+    close(S.svdq_fp8_linear(dev_bf16(x), lay, out_dtype=dtype_of(out)), *R.epilogue(v, dv, out=out))
+
+
 # ---------------------------------------------------------------------------
 # grouped by expert
 # ---------------------------------------------------------------------------

@@ -35,7 +35,8 @@ __device__ __forceinline__ f32x4 mfma_scaled(const i32x8& a, const i32x8& b, con
 }
 
 // Eight codes times their block's scale (a power of two, as a float) in bf16, which
-// holds them exactly: four significant bits.
+// holds them exactly (four significant bits) inside its range: below 2^-126 to the
+// multiples of 2^-133, at 2^128 to infinity.
 __device__ __forceinline__ bf16x8 decode8(uint32_t lo, uint32_t hi, float scale) {
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
   const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);

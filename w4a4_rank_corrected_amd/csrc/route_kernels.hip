@@ -164,6 +164,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
         index[s] = key[i] < experts ? row : -1 - row;
         row_index[row] = s / k;
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (the next 64 slots see the moved rows)
     }
     s0 += 64 * kKeys;
     if (s0 < w1) load_keys(s0);
