@@ -27,13 +27,13 @@ void plan(int b, int n, int m, int experts, int dtype) {
   CHECK(grid >= 1 && p.threads >= 64 && p.threads <= 1024);
   if (p.rb) {
     CHECK(p.rb == 1 || p.rb == 2 || p.rb == 4);
-    CHECK(!p.big && p.pieces == 1 && p.ws_bytes == 0);
+    CHECK(!p.big && !p.small && p.pieces == 1 && p.ws_bytes == 0);
     CHECK(p.threads == 64 * p.split.nwk * p.split.nwc && p.threads <= (p.rb == 4 ? 512 : 1024));
     CHECK(p.split.nwk * p.split.nwc * p.rb <= 32);  // KB of LDS, beside the codes of few blocks
     const long long blocks = experts ? grouped_row_blocks(b, experts, 16 * p.rb) : (b + 16LL * p.rb - 1) / (16 * p.rb);
     CHECK(grid == blocks * ((n + 16LL * p.split.nwc - 1) / (16 * p.split.nwc)));
   } else if (p.big) {
-    CHECK(dtype == SVDQ_OUT_BF16 && p.threads == 512 && p.ws_bytes == 0);
+    CHECK(dtype == SVDQ_OUT_BF16 && !p.small && p.threads == 512 && p.ws_bytes == 0);
     if (experts) {
       CHECK(grid == t256);
     } else {
@@ -41,6 +41,9 @@ void plan(int b, int n, int m, int experts, int dtype) {
       CHECK(p.full >= 1 && p.full <= t256 && grid == p.full + (t256 - p.full) * p.parts);
       CHECK(p.parts > 1 || p.full == t256);
     }
+  } else if (p.small) {
+    CHECK(!experts && p.threads == 256 && p.pieces == 1 && p.ws_bytes == 0);
+    CHECK(grid == ((b + 63LL) / 64) * ((n + 127LL) / 128));
   } else {
     CHECK(p.threads == 256 && p.pieces >= 1 && p.pieces <= G && grid == t128 * p.pieces);
     CHECK(!experts || p.pieces == 1);

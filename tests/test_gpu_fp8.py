@@ -205,11 +205,11 @@ def test_transposed_layer_has_the_same_values(S):
 # products
 # ---------------------------------------------------------------------------
 
-# one row and a few (quantized in the product's kernel or before it), the row kernel, whole and split tiles of 128 x 128,
-# tiles of 256 x 256 with a last round whole, in halves and in quarters
+# one row and a few (quantized in the product's kernel or before it), the row kernel, tiles of 64 x 128, whole and split
+# ones of 128 x 128, tiles of 256 x 256 with a last round whole, in halves and in quarters
 SHAPES = [(1, 1, 1), (1, 8192, 40), (1, 8193, 40), (4, 2048, 33), (9, 900, 20), (16, 512, 70), (17, 128, 50), (40, 100, 90), (1, 128, 16), (1, 1152, 700), (2, 130, 33), (7, 1000, 513), (16, 256, 128), (17, 384, 130), (33, 700, 64),
           (64, 2048, 96), (65, 129, 257), (130, 640, 300), (257, 1152, 200), (300, 4200, 72), (512, 300, 520),
-          (2048, 130, 257), (2300, 400, 513), (2500, 1100, 300),
+          (333, 1000, 1500), (450, 1900, 900), (2100, 640, 900), (2048, 130, 257), (2300, 400, 513), (2500, 1100, 300),
           (300, 4608, 700), (400, 4700, 1100), (129, 8192, 1000), (4100, 140, 2300), (4608, 130, 4800), (4350, 260, 4150), (4096, 128, 4096)]
 
 
@@ -260,6 +260,11 @@ def test_epilogue(S, b, act, n, begin):
         S.svdq_fp8_linear(dev_bf16(x), X.layer, act=act, act_begin=begin, gate=dev_bf16(gate), gate_rows=rows, residual=own, y=own)
         assert torch.equal(own, got)
         assert (wres[:, :2] == 7).all() and (wres[:, 2 + n:] == 7).all()
+
+
+@pytest.mark.parametrize("act,n,begin", [("gelu_tanh", 512, 0), ("silu", 450, 200), ("relu", 512, 128)])
+def test_epilogue_of_larger_tiles(S, act, n, begin):
+    test_epilogue(S, 4200, act, n, begin)
 
 
 @pytest.mark.parametrize("b", [1, 5, 64, 300])

@@ -43,6 +43,17 @@ __device__ __forceinline__ void load_whole(const void* row, int j, float (&v)[W]
     for (int e = 0; e < 4; ++e) v[e] = w[e];
   }
 }
+// The same where the row may end in them (n >= 1 columns): an element at a time, the last
+// one for those behind it, so that all of the loads are under way together.
+template <int W, bool BF16>
+__device__ __forceinline__ void load_ragged(const void* row, int j, int n, float (&v)[W]) {
+  if (j + W <= n) return load_whole<W, BF16>(row, j, v);
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    const int at = min(j + e, n - 1);
+    v[e] = BF16 ? bf16_lo(reinterpret_cast<const uint16_t*>(row)[at]) : reinterpret_cast<const float*>(row)[at];
+  }
+}
 template <int W, bool BF16>
 __device__ __forceinline__ void store_whole(void* to, const float (&v)[W]) {
   if constexpr (BF16)
@@ -78,9 +89,24 @@ __device__ __forceinline__ void finish_rows(const f32x4 (&acc)[4][QB], int row0,
     auto finish = [&](auto A, auto MORE) {
       uint8_t* y = reinterpret_cast<uint8_t*>(row_of<OUT_BF16>(ep.y, row0 + r, ep.ldy)) + (jw + W * c) * (OUT_BF16 ? 2 : 4);
       const size_t next = (size_t)16 * ep.ldy * (OUT_BF16 ? 2 : 4);
+      // The gate and the residual of a block of rows are loaded before the block before it
+      // is stored (the compiler would wait for each: the residual may be y).
+      float gv[2][UNITS][W], rv[2][UNITS][W];
+      auto load_more = [&](int q) {
+        const int i = min(row0 + 16 * q + r, row_end - 1);
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const int j = jw + W * c + 4 * W * u;
+          if (ep.gate) load_whole<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, gv[q & 1][u]);
+          if (ep.residual) load_whole<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, rv[q & 1][u]);
+        }
+      };
+      if constexpr (decltype(MORE)::value) load_more(0);
 #pragma unroll
       for (int q = 0; q < QB; ++q, y += next) {
         const int i = row0 + 16 * q + r;
+        if constexpr (decltype(MORE)::value)
+          if (q + 1 < QB) load_more(q + 1);
         if (i >= row_end) break;
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
@@ -88,18 +114,13 @@ __device__ __forceinline__ void finish_rows(const f32x4 (&acc)[4][QB], int row0,
 #pragma unroll
           for (int e = 0; e < W; ++e) v[e] = act_value<decltype(A)::value>(acc[W / 4 * u + e / 4][q][e & 3]);
           if constexpr (decltype(MORE)::value) {
-            const int j = jw + W * c + 4 * W * u;
             if (ep.gate) {
-              float gv[W];
-              load_whole<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, gv);
 #pragma unroll
-              for (int e = 0; e < W; ++e) v[e] *= gv[e];
+              for (int e = 0; e < W; ++e) v[e] *= gv[q & 1][u][e];
             }
             if (ep.residual) {
-              float rv[W];
-              load_whole<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, rv);
 #pragma unroll
-              for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
+              for (int e = 0; e < W; ++e) v[e] = rv[q & 1][u][e] + v[e];
             }
           }
           store_whole<W, OUT_BF16>(y + 64 * u, v);
@@ -139,37 +160,46 @@ __device__ __forceinline__ void finish_rows(const f32x4 (&acc)[4][QB], int row0,
     // other lanes' results: LDS accesses of one wave complete in order
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    constexpr int kRows = 64 / LANES, U = QB == 1 || OUT_BF16 ? 2 : 4;  // rows at a time, times U with their loads together
 #pragma unroll 1
-    for (int k = rr; k < (QB > 1 ? 32 : 16); k += 64 / LANES) {
-      const int i = row0 + 32 * p + k;
-      if (i < row_end && j < n) {
-        float v[W];
+    for (int k0 = rr; k0 < (QB > 1 ? 32 : 16); k0 += U * kRows) {
+      float gv[U][W], rv[U][W];
 #pragma unroll
-        for (int e = 0; e < W; e += 4) {
-          const f32x4 t = *reinterpret_cast<const f32x4*>(part + k * kPitch + (W * cc + e) * 4);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) v[e + x] = t[x];
+      for (int u = 0; u < U; ++u) {
+        const int i = row0 + 32 * p + k0 + u * kRows;
+        if (i < row_end && j < n) {
+          if (ep.gate) load_ragged<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, gv[u]);
+          if (ep.residual) load_ragged<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, rv[u]);
         }
-        with_act(ep.act, [&](auto A) {
+      }
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const float t = act_value<decltype(A)::value>(v[e]);
-            v[e] = j + e >= ep.act_begin ? t : v[e];
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * kRows, i = row0 + 32 * p + k;
+        if (i < row_end && j < n) {
+          float v[W];
+#pragma unroll
+          for (int e = 0; e < W; e += 4) {
+            const f32x4 t = *reinterpret_cast<const f32x4*>(part + k * kPitch + (W * cc + e) * 4);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[e + x] = t[x];
           }
-        });
-        if (ep.gate) {
-          float gv[W];
-          load_cols<W, true>(row_of<true>(ep.gate, i / ep.gate_rows, n), j, n, gv);
+          with_act(ep.act, [&](auto A) {
 #pragma unroll
-          for (int e = 0; e < W; ++e) v[e] *= gv[e];
-        }
-        if (ep.residual) {
-          float rv[W];
-          load_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.residual, i, ep.ldr), j, n, rv);
+            for (int e = 0; e < W; ++e) {
+              const float t = act_value<decltype(A)::value>(v[e]);
+              v[e] = j + e >= ep.act_begin ? t : v[e];
+            }
+          });
+          if (ep.gate) {
 #pragma unroll
-          for (int e = 0; e < W; ++e) v[e] = rv[e] + v[e];
+            for (int e = 0; e < W; ++e) v[e] *= gv[u][e];
+          }
+          if (ep.residual) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = rv[u][e] + v[e];
+          }
+          store_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, v);
         }
-        store_cols<W, OUT_BF16>(row_of<OUT_BF16>(ep.y, i, ep.ldy), j, n, v);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -519,6 +549,22 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8Args a, int tiles_m, i
                                                 s_scale_even, s_scale_odd, sums);
 }
 
+// Tiles of 64 x 128, three workgroups a CU, where those of 128 x 128 leave CUs idle: half
+// the multiplications in a step's chain (333 rows, 1000 -> 1500 in fp32: 9.9 us, where
+// 36 tiles of 128 x 128 take 13.5).
+template <bool EXACT>
+__global__ __launch_bounds__(256) void fp8_small_kernel(Fp8Args a, int tiles_m, int tiles_n) {
+  typedef TileShape<2, 2, 2> Shape;
+  __shared__ __align__(16) uint8_t s_even[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_odd[Shape::kBuffer];
+  __shared__ __align__(16) uint8_t s_scale_even[Shape::kScales];
+  __shared__ __align__(16) uint8_t s_scale_odd[Shape::kScales];
+  int ti, tj;
+  tile_at(xcd_range((int)blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
+  tile<2, 2, 2, EXACT, !EXACT, false, false>(a, a.qx, a.ascale, a.qw, a.wscale, a.bias, a.G, ti * 64, tj * 128, a.b,
+                                             s_even, s_odd, s_scale_even, s_scale_odd, nullptr);
+}
+
 // The pieces' sums of a tile added in their order, the bias, and the rest.  A workgroup
 // takes the blocks q of 16 rows of the tile's four waves.
 template <bool OUT_BF16>
@@ -558,6 +604,10 @@ int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& p, int y_dtype, void* ws, 
     return p.parts == 1 ? go(fp8_big_kernel<1>) : p.parts == 2 ? go(fp8_big_kernel<2>) : go(fp8_big_kernel<4>);
   }
   const int tm = (a.b + 127) / 128, tn = (a.n + 127) / 128;
+  if (p.small) {
+    auto go = [&](auto kernel) { return launch_checked(kernel, p.split.grid, 256, st, a, (a.b + 63) / 64, tn); };
+    return exact ? go(fp8_small_kernel<true>) : go(fp8_small_kernel<false>);
+  }
   f32x4* sums = reinterpret_cast<f32x4*>(ws);
   auto go = [&](auto kernel) { return launch_checked(kernel, p.split.grid, 256, st, a, tm, tn, p.pieces, sums); };
   if (a.groups.offsets) return exact ? go(fp8_tile_kernel<true, true, false>) : go(fp8_tile_kernel<false, true, false>);

@@ -272,10 +272,10 @@ struct Fp8Args {
 };
 // The kernel of a product (experts 0: one layer) and its largest launch: the row
 // kernel with rb 16-row blocks a workgroup; or (rb 0) tiles of 128 x 128, in `pieces`
-// along the channels; or (big) the first `full` tiles of 256 x 256 and the others in
+// along the channels; or (small) of 64 x 128; or (big) the first `full` tiles of 256 x 256 and the others in
 // `parts` (1: there are no others).
 struct Fp8Plan {
-  int rb, big, full, parts, pieces, threads;
+  int rb, big, small, full, parts, pieces, threads;
   RowsSplit split;
   size_t ws_bytes;
 };

@@ -136,6 +136,17 @@ double fp8_tiles_us(long long tiles, int G, int k, bool exact) {
   return (4.0 + ((G + k - 1) / k) * step) * rounds + (k > 1 ? 1.5 + 0.35 * k + 0.026 * units : 0.0);
 }
 
+// The same by tiles of 64 x 128, whole (128 x 128, in the best pieces, against it):
+//   fp32: 333 rows, 1000 -> 1500 13.5, 9.9; 512, 1152 -> 1152 12.6, 10.4; 1000, 2048 -> 2048
+//   20.7, 16.1; 256, 1152 -> 6912 14.4, 11.0; 1000, 4608 -> 1152 22.9, 30.0; 2048, 2048 ->
+//   2048 22.6, 23.6;  bf16: 333, 1000 -> 1500 9.7, 7.8; 512, 2048 -> 2048 11.7, 10.5;
+//   1000, 2048 -> 2048 11.8, 10.8; 256, 4608 -> 4608 18.2, 21.5; 2048, 2048 -> 2048 13.0, 14.8
+double fp8_small_us(long long tiles, int G, bool exact) {
+  const double units = (double)tiles;
+  const double step = units <= kMaxCUs ? (exact ? 0.71 : 0.48) : (exact ? 1.2 : 0.66);
+  return (4.0 + G * step) * std::max(1.0, units / (2 * kMaxCUs));
+}
+
 // The same by the row kernel, for `steps` of 16 rb rows x 16 columns x 128 channels:
 //   one layer, us for rb 1 / 2 / 4: 64 rows, 2048 -> 2048 7.5 / 7.3 / 8.5; 179, 1344 -> 256
 //   4.6 / 5.3 / 7.0; 333, 1000 -> 1500 11.8 / 11.9 / 11.4; 100, 2048 -> 2048 11.5 / 9.2 / 8.6;
@@ -159,12 +170,13 @@ double fp8_rows_us(double steps, int rb, bool grouped) {
 //   * the same for experts of 1024 rows on average and more (8 experts, 4096 -> 4096,
 //     mean 2048: 314 by 128 x 128, 252; 1024: 150, 143; 512: 82, 95; 1152 -> 4608, mean
 //     1024: 59.5, 56.7): below, half-empty last row blocks cost more;
-//   * otherwise tiles of 128 x 128, one layer's in the pieces that are quickest, or the
-//     row kernel, whichever the estimates above say is quicker.
+//   * otherwise tiles of 128 x 128, one layer's in the pieces that are quickest, for one
+//     layer tiles of 64 x 128, or the row kernel, whichever the estimates above say is
+//     quickest.
 Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
   const int G = fp8_blocks(m);
   const bool exact = y_dtype == SVDQ_OUT_F32, grouped = experts > 0;
-  Fp8Plan p{0, 0, 0, 1, 1, 256, {1, 1, 0}, 0};
+  Fp8Plan p{0, 0, 0, 0, 1, 1, 256, {1, 1, 0}, 0};
   const long long big = (long long)((b + 255) / 256) * ((n + 255) / 256);
   if (!grouped && !exact && big > 128) {
     p.big = 1;
@@ -189,6 +201,11 @@ Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
     const double us = fp8_tiles_us(tiles, G, k, exact);
     if (us < best) best = us, p.pieces = k;
   }
+  const long long small = (long long)((b + 63) / 64) * ((n + 127) / 128);
+  if (!grouped) {
+    const double us = fp8_small_us(small, G, exact);
+    if (us < best) best = us, p.small = 1;
+  }
   for (int rb : {1, 2, 4}) {
     if (grouped && rb != (mean <= 16 ? 1 : (mean <= 32 ? 2 : 4))) continue;
     const long long blocks = grouped ? grouped_row_blocks(b, experts, 16 * rb) : (b + 16 * rb - 1) / (16 * rb);
@@ -200,7 +217,13 @@ Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
   }
   if (p.rb) {
     p.pieces = 1;
+    p.small = 0;
     p.threads = 64 * p.split.nwk * p.split.nwc;
+    return p;
+  }
+  if (p.small) {
+    p.pieces = 1;
+    p.split.grid = small;
     return p;
   }
   p.split.grid = tiles * p.pieces;
