@@ -438,7 +438,10 @@ __device__ __forceinline__ void tile_at(int u, int tiles_m, int tiles_n, int& ti
 
 // Tiles of 256 x 256, one workgroup a CU, for whole rounds of the CUs; the tiles left
 // over are cut into PARTS of 256 x 128 or 128 x 128, so that the last round takes every
-// CU for the time of a part.
+// CU for the time of a part.  A step takes 2870 cycles, 2048 of them its multiplications'
+// (LDS reads and the barrier the rest); before the first step and behind the last one
+// nothing multiplies, 3000 and 4000 cycles: 8192 x 8192 -> 8192 380-400 us (2.75-2.9
+// PFLOP/s), 4608 x 4608 -> 12288 202 (2.6), 4096 x 1152 -> 4608 29 (1.5).
 template <int PARTS>
 __global__ __launch_bounds__(512) void fp8_big_kernel(Fp8Args a, int tiles_m, int tiles_n, int full) {
   typedef TileShape<8, 2, 4> Shape;
@@ -492,7 +495,8 @@ __device__ __forceinline__ bool grouped_tile(const Fp8Args& a, int tiles_n, Grou
   return true;
 }
 
-// 256 x 256 for experts of many rows.
+// 256 x 256 for experts of many rows (8 experts, 2048 rows each of 4096 -> 4096 252 us,
+// 2.2 PFLOP/s).
 __global__ __launch_bounds__(512) void fp8_big_grouped_kernel(Fp8Args a, int tiles_n) {
   typedef TileShape<8, 2, 4> Shape;
   __shared__ __align__(16) uint8_t s_even[Shape::kBuffer];
@@ -505,7 +509,9 @@ __global__ __launch_bounds__(512) void fp8_big_grouped_kernel(Fp8Args a, int til
                                           s_odd, s_scale_even, s_scale_odd, nullptr);
 }
 
-// Tiles of 128 x 128, two workgroups a CU: experts' rows, fp32 results, and few tiles,
+// Tiles of 128 x 128, two workgroups a CU (of which one ends while the other multiplies):
+// experts' rows (64 experts, 18006 rows of 2048 -> 1408 in all 100 us: 1.04 PFLOP/s, 1.3 of
+// whole tiles; the L2s' 16 TB/s of records bound it), fp32 results, and few tiles,
 // which may be split along the channels (PIECES: piece p of tile u takes every block
 // from p G / pieces to (p + 1) G / pieces and leaves its sums in slot u pieces + p).
 template <bool EXACT, bool GROUPED, bool PIECES>
