@@ -724,17 +724,11 @@ int svdq_combine_rows_grad(const void* dy, int t, int n, int dtype, const int32_
  *           a NaN has e = 0 and the NaN code 0x7F everywhere, so that its row (or
  *           its columns) of Y is NaN.
  *   v[i,j] = sum_g 2^(ex[g,i] + ew[g,j/128]) sum_{k in g} cx[i,k] cw[k,j] + bias[j]
- * Scaling by powers of two is exact, and sums are held in fp32.  How the products
- * of a block are added depends on y's type:
- *   fp32 y, and bf16 y of few rows: the scaled codes as bf16 (exact) through the
- *     bf16 matrix instruction, which adds exact products in fp32.  At the ends of
- *     bf16's range that rounds: a weight below 2^-126 to a multiple of 2^-133, and
- *     a value from 31/16 2^127 on, whose code stands for 2^128, to an infinity;
- *   bf16 y of many rows: the 8-bit matrix instruction, which adds the products of
- *     eight neighbouring channels at the exponent of the largest and keeps 13 bits
- *     below it (and adds those sums in fp32).  For v's sum that is an error of some
- *     10^-5 of the sum of the products' magnitudes, where y's rounding is 2^-8 of y;
- *     fp32 results of the same would show it.
+ * Scaling by powers of two is exact, and sums are held in fp32: the scaled codes go
+ * as bf16 (exact) through the bf16 matrix instruction, which adds exact products in
+ * fp32.  At the ends of bf16's range that rounds: a weight below 2^-126 to a multiple
+ * of 2^-133, and a value from 31/16 2^127 on, whose code stands for 2^128, to an
+ * infinity.
  * Layouts, G = ceil(m / 128):
  *   codes of X   [G][rows][128]: byte t of a record is channel 128 g + t's code,
  *                zero behind channel m - 1 (X: of any value in a block of NaN);
@@ -743,6 +737,18 @@ int svdq_combine_rows_grad(const void* dy, int t, int n, int dtype, const int32_
  * m and n are any dimensions here (1 .. SVDQ_MAX_DIM).
  * ========================================================================= */
 #define SVDQ_FP8_BLOCK 128
+
+/* A caller's choice, or-ed to y_dtype SVDQ_OUT_BF16 of the products below (with fp32
+ * y it is refused): many rows may go through the 8-bit matrix instruction, which is
+ * up to twice as quick and keeps fewer bits.  It adds the products of eight
+ * neighbouring channels at the exponent of the largest with 13 bits below it, and
+ * those sums in fp32.  Each of the eight is off by up to 2^-13 of the largest, so v by
+ * up to 2^-10 of the sum, over the eights, of their largest product's magnitude (a
+ * factor below 2^(e-6), e its block's exponent, counted as that).  This goes by the
+ * products, not by |v|: where they cancel, or v and the residual do, it can be more
+ * than y's rounding, and small products beside a large one of the same eight can be
+ * lost altogether.  Which calls take that instruction depends on the shape. */
+#define SVDQ_FP8_FAST_SUMS 0x100
 
 /* A layer on the device: qw and wscale as above (svdq_fp8_quantize_weights makes
  * them), bias bf16 [n] or NULL (element alignment).  wscale: any alignment. */
@@ -777,10 +783,9 @@ int svdq_fp8_quantize_weights(const void* W, int w_dtype, int experts, int m, in
 int svdq_fp8_quantize_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t* ascale, void* stream);
 
 /* DEVICE: the product with an epilogue (epi NULL: none) of svdq_*_epi's kind.
- * The order of the fp32 sums depends only on the shape and y's type.  Workspace:
- * 16-byte aligned, >= svdq_fp8_gemm_workspace_size(b, n, m) bytes (0 where no tile
- * is split for either type of y), one for each of the calls that overlap in
- * time. */
+ * The order of the sums depends only on the shape and y_dtype.  Workspace: 16-byte
+ * aligned, >= svdq_fp8_gemm_workspace_size(b, n, m) bytes (0 where no tile is split
+ * for any y_dtype), one for each of the calls that overlap in time. */
 size_t svdq_fp8_gemm_workspace_size(int b, int n, int m);
 int svdq_fp8_gemm(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer* layer, const svdq_epilogue* epi, int b,
                   void* y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);

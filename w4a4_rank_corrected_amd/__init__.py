@@ -23,6 +23,7 @@ from ._binding import (  # noqa: F401
     svdq_grouped_gemm_w4a4_lowrank_up, svdq_grouped_linear_workspace_size, svdq_grouped_linear,
     svdq_combine_rows,
     svdq_sort_rows_workspace_size, svdq_sort_rows, svdq_dispatch_rows, svdq_combine_rows_grad, SVDQ_FP8_BLOCK,
+    SVDQ_FP8_FAST_SUMS,
     DeviceLayerFp8, GroupedDeviceLayerFp8, svdq_fp8_quantize_weights, svdq_fp8_quantize_act,
     svdq_fp8_gemm_workspace_size, svdq_fp8_gemm, svdq_fp8_linear_workspace_size, svdq_fp8_linear,
     svdq_fp8_grouped_gemm, svdq_fp8_grouped_linear_workspace_size, svdq_fp8_grouped_linear)
@@ -47,7 +48,7 @@ __all__ = [
     "svdq_grouped_gemm_w4a4_lowrank_up", "svdq_grouped_linear_workspace_size", "svdq_grouped_linear",
     "svdq_combine_rows",
     "svdq_sort_rows_workspace_size", "svdq_sort_rows", "svdq_dispatch_rows", "svdq_combine_rows_grad",
-    "SVDQ_FP8_BLOCK", "DeviceLayerFp8", "GroupedDeviceLayerFp8", "svdq_fp8_quantize_weights",
+    "SVDQ_FP8_BLOCK", "SVDQ_FP8_FAST_SUMS", "DeviceLayerFp8", "GroupedDeviceLayerFp8", "svdq_fp8_quantize_weights",
     "svdq_fp8_quantize_act", "svdq_fp8_gemm_workspace_size", "svdq_fp8_gemm",
     "svdq_fp8_linear_workspace_size", "svdq_fp8_linear", "svdq_fp8_grouped_gemm",
     "svdq_fp8_grouped_linear_workspace_size", "svdq_fp8_grouped_linear",

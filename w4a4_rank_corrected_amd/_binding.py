@@ -30,6 +30,7 @@ SVDQ_MAX_DIM = 1 << 22
 SVDQ_W8A8_MAX_M = 131072
 SVDQ_MAX_EXPERTS = 1024
 SVDQ_FP8_BLOCK = 128
+SVDQ_FP8_FAST_SUMS = 0x100
 ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "gelu_erf": 2, "silu": 3, "relu": 4}  # SVDQ_ACT_*
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsvdq.so")
@@ -1479,13 +1480,26 @@ def svdq_fp8_gemm_workspace_size(b: int, n: int, m: int) -> int:
     return int(lib().svdq_fp8_gemm_workspace_size(b, n, m))
 
 
+def _fp8_code(code: int, fast_sums: bool) -> int:
+    """A product's y_dtype for the C ABI."""
+    if not fast_sums:
+        return code
+    if code != SVDQ_OUT_BF16:
+        raise ValueError("fast_sums is for bfloat16 results")
+    return code | SVDQ_FP8_FAST_SUMS
+
+
 def svdq_fp8_gemm(qx, ascale, layer: DeviceLayerFp8, act: str = "none", act_begin: int = 0, gate=None,
-                  gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None, stream=None):
+                  gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None, stream=None,
+                  fast_sums: bool = False):
     """The product of svdq_fp8_quantize_act's codes with a layer, with the epilogue
-    of svdq_gemm_w4a4_lowrank_up_epi."""
+    of svdq_gemm_w4a4_lowrank_up_epi.  Sums are held in 32 bits; fast_sums (bf16
+    results only): many rows may take the 8-bit matrix instruction, up to twice as
+    quick, whose sums of eight products keep 13 bits below the largest."""
     b, device, n = _fp8_operands(qx, ascale, layer), qx.device, layer.n
     with _On(device, stream) as handle:
         y, code, epi = _epilogue(b, n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
+        code = _fp8_code(code, fast_sums)
         need = svdq_fp8_gemm_workspace_size(b, n, layer.m) if workspace is None else 0
         workspace, wsb = _workspace(workspace, need, device)
         _check(lib().svdq_fp8_gemm(_ptr(qx), _ptr(ascale), ctypes.byref(layer.struct), ctypes.byref(epi), b,
@@ -1498,9 +1512,11 @@ def svdq_fp8_linear_workspace_size(b: int, m: int, n: int) -> int:
 
 
 def svdq_fp8_linear(x, layer: DeviceLayerFp8, act: str = "none", act_begin: int = 0, gate=None,
-                    gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None, stream=None):
+                    gate_rows: Optional[int] = None, residual=None, out_dtype=None, y=None, workspace=None, stream=None,
+                    fast_sums: bool = False):
     """y = residual + gate * act(x W + bias) of a layer in 8-bit floating point (the
-    arguments of svdq_linear_epi; workspace: svdq_fp8_linear_workspace_size bytes)."""
+    arguments of svdq_linear_epi; workspace: svdq_fp8_linear_workspace_size bytes;
+    fast_sums: see svdq_fp8_gemm)."""
     b, m = _input(x)
     device = layer.qw.device
     _dev(x, "x", device=device)
@@ -1508,6 +1524,7 @@ def svdq_fp8_linear(x, layer: DeviceLayerFp8, act: str = "none", act_begin: int 
         raise ValueError(f"x has {m} channels, the layer {layer.m}")
     with _On(device, stream) as handle:
         y, code, epi = _epilogue(b, layer.n, device, y, out_dtype, act, act_begin, gate, gate_rows, residual)
+        code = _fp8_code(code, fast_sums)
         need = svdq_fp8_linear_workspace_size(b, m, layer.n) if workspace is None else 0
         workspace, wsb = _workspace(workspace, need, device)
         _check(lib().svdq_fp8_linear(x.data_ptr(), ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code,
@@ -1516,15 +1533,16 @@ def svdq_fp8_linear(x, layer: DeviceLayerFp8, act: str = "none", act_begin: int 
 
 
 def svdq_fp8_grouped_gemm(qx, ascale, offsets, layer: GroupedDeviceLayerFp8, row_index=None, act: str = "none",
-                          act_begin: int = 0, out_dtype=None, y=None, stream=None):
+                          act_begin: int = 0, out_dtype=None, y=None, stream=None, fast_sums: bool = False):
     """The product of rows sorted by expert with their experts' layers: row i takes
     row row_index[i] (None: i) of the codes, which svdq_fp8_quantize_act made of the
-    tokens.  Rows without an expert are not written."""
+    tokens.  Rows without an expert are not written.  fast_sums: see svdq_fp8_gemm."""
     import torch
     x_rows, dev = _fp8_operands(qx, ascale, layer), qx.device
     b = _fp8_rows(offsets, layer, row_index, x_rows, dev)
     with _On(dev, stream) as handle:
         y, code, epi = _epilogue(b, layer.n, dev, y, out_dtype, act, act_begin)
+        code = _fp8_code(code, fast_sums)
         _check(lib().svdq_fp8_grouped_gemm(_ptr(qx), _ptr(ascale), x_rows, _ptr(row_index), _ptr(offsets),
                                            ctypes.byref(layer.struct), ctypes.byref(epi), b, y.data_ptr(), code, handle))
     return y
@@ -1549,10 +1567,11 @@ def svdq_fp8_grouped_linear_workspace_size(b: int, x_rows: int, experts: int, m:
 
 
 def svdq_fp8_grouped_linear(x, offsets, layer: GroupedDeviceLayerFp8, row_index=None, act: str = "none",
-                            act_begin: int = 0, out_dtype=None, y=None, workspace=None, stream=None):
+                            act_begin: int = 0, out_dtype=None, y=None, workspace=None, stream=None,
+                            fast_sums: bool = False):
     """svdq_grouped_linear in the 8-bit floating-point setting: act(x[row_index[i]]
     W_e + bias_e) for row i of expert e; the rows without an expert are not
-    written."""
+    written.  fast_sums: see svdq_fp8_gemm."""
     x_rows, m = _input(x)
     dev = layer.qw.device
     _dev(x, "x", device=dev)
@@ -1561,6 +1580,7 @@ def svdq_fp8_grouped_linear(x, offsets, layer: GroupedDeviceLayerFp8, row_index=
     b = _fp8_rows(offsets, layer, row_index, x_rows, dev)
     with _On(dev, stream) as handle:
         y, code, epi = _epilogue(b, layer.n, dev, y, out_dtype, act, act_begin)
+        code = _fp8_code(code, fast_sums)
         need = 0
         if workspace is None:
             need = svdq_fp8_grouped_linear_workspace_size(b, x_rows, layer.experts, m, layer.n)

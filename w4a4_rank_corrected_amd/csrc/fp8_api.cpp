@@ -9,6 +9,9 @@ using namespace svdq;
 
 namespace {
 
+// y's type without the choice of its sums (any other value as it is: check_y refuses it).
+int y_type(int y_dtype) { return y_dtype == (SVDQ_OUT_BF16 | SVDQ_FP8_FAST_SUMS) ? SVDQ_OUT_BF16 : y_dtype; }
+
 int check_dims(int m, int n) {
   REQUIRE(m >= 1 && n >= 1, SVDQ_ERR_INVALID_ARG, "m and n must be >= 1 (got m=%d n=%d)", m, n);
   REQUIRE(m <= SVDQ_MAX_DIM && n <= SVDQ_MAX_DIM, SVDQ_ERR_UNSUPPORTED, "m and n must be <= %d (got m=%d n=%d)",
@@ -42,8 +45,8 @@ int check_product(const svdq_fp8_layer* L, const svdq_epilogue* epi, int b, void
   REQUIRE(L != nullptr, SVDQ_ERR_INVALID_ARG, "layer is NULL");
   int st = check_dims(L->m, L->n);
   if (!st) st = check_rows(b);
-  if (!st) st = check_y(y, y_dtype, b);
-  if (!st) st = check_epilogue(epi, b, L->n, y, y_dtype, ep);
+  if (!st) st = check_y(y, y_type(y_dtype), b);
+  if (!st) st = check_epilogue(epi, b, L->n, y, y_type(y_dtype), ep);
   if (st || b == 0) return st;
   st = check_weights(L->qw, L->wscale, L->bias);
   if (st) return st;
@@ -61,10 +64,10 @@ int check_grouped_product(const svdq_fp8_grouped_layer* L, const svdq_epilogue* 
           L->experts);
   int st = check_dims(L->m, L->n);
   if (!st) st = check_rows(b);
-  if (!st) st = check_y(y, y_dtype, b);
+  if (!st) st = check_y(y, y_type(y_dtype), b);
   REQUIRE(st || !epi || (!epi->gate && !epi->residual), SVDQ_ERR_UNSUPPORTED,
           "a grouped product takes no gate and no residual");
-  if (!st) st = check_epilogue(epi, b, L->n, y, y_dtype, ep);
+  if (!st) st = check_epilogue(epi, b, L->n, y, y_type(y_dtype), ep);
   if (st || b == 0) return st;
   REQUIRE(offsets != nullptr, SVDQ_ERR_INVALID_ARG, "offsets must not be NULL");
   REQUIRE(((uintptr_t)offsets & 3u) == 0 && ((uintptr_t)row_index & 3u) == 0, SVDQ_ERR_ALIGNMENT,
@@ -80,9 +83,10 @@ int check_grouped_product(const svdq_fp8_grouped_layer* L, const svdq_epilogue* 
   return SVDQ_OK;
 }
 
-// The product's workspace, whatever its output's type.
+// The product's workspace, whatever its output's type and sums.
 size_t fp8_gemm_ws_bytes(int b, int n, int m) {
-  return std::max(fp8_plan(b, n, m, 0, SVDQ_OUT_BF16).ws_bytes, fp8_plan(b, n, m, 0, SVDQ_OUT_F32).ws_bytes);
+  return std::max(fp8_plan(b, n, m, 0, SVDQ_OUT_BF16).ws_bytes,
+                  fp8_plan(b, n, m, 0, SVDQ_OUT_BF16 | SVDQ_FP8_FAST_SUMS).ws_bytes);
 }
 
 // Codes, scales and the product's share of a whole layer's workspace.
@@ -161,7 +165,7 @@ int svdq_fp8_gemm(const uint8_t* qx, const uint8_t* ascale, const svdq_fp8_layer
   const Fp8Plan plan = fp8_plan(b, layer->n, layer->m, 0, y_dtype);
   if (!st) st = check_workspace(workspace, workspace_bytes, fp8_gemm_ws_bytes(b, layer->n, layer->m), 16);
   if (st) return st;
-  return hip_status(launch_fp8_gemm(product_args(qx, ascale, *layer, b, ep), plan, y_dtype, workspace, stream),
+  return hip_status(launch_fp8_gemm(product_args(qx, ascale, *layer, b, ep), plan, y_type(y_dtype), workspace, stream),
                     "fp8_gemm");
 }
 
@@ -182,14 +186,15 @@ int svdq_fp8_linear(const uint16_t* x, const svdq_fp8_layer* layer, const svdq_e
   if (!st) st = check_workspace(workspace, workspace_bytes, w.total, kAlign);
   if (st) return st;
   uint8_t* ws = (uint8_t*)workspace;
+  const int type = y_type(y_dtype);
   // few blocks of x: every workgroup of the product quantizes them itself, unless y is
   // written where x may still be read
-  if (plan.rb == 1 && b <= 16 && fp8_blocks(layer->m) * b <= kFp8FusedBlocks && apart_from_x(x, b, layer->m, ep, layer->n, y_dtype))
-    return hip_status(launch_fp8_rows_x(product_args(ws, ws + w.as_off, *layer, b, ep), x, layer->m, plan, y_dtype, stream),
+  if (plan.rb == 1 && b <= 16 && fp8_blocks(layer->m) * b <= kFp8FusedBlocks && apart_from_x(x, b, layer->m, ep, layer->n, type))
+    return hip_status(launch_fp8_rows_x(product_args(ws, ws + w.as_off, *layer, b, ep), x, layer->m, plan, type, stream),
                       "fp8_gemm");
   st = hip_status(launch_fp8_act(x, b, layer->m, ws, ws + w.as_off, stream), "fp8_quantize_act");
   if (st) return st;
-  return hip_status(launch_fp8_gemm(product_args(ws, ws + w.as_off, *layer, b, ep), plan, y_dtype, ws + w.gemm_off, stream),
+  return hip_status(launch_fp8_gemm(product_args(ws, ws + w.as_off, *layer, b, ep), plan, type, ws + w.gemm_off, stream),
                     "fp8_gemm");
 }
 
@@ -203,7 +208,8 @@ int svdq_fp8_grouped_gemm(const uint8_t* qx, const uint8_t* ascale, int x_rows, 
   st = check_codes(qx, ascale);
   if (st) return st;
   return hip_status(launch_fp8_gemm(grouped_args(qx, ascale, x_rows, row_index, offsets, *layer, b, ep),
-                                    fp8_plan(b, layer->n, layer->m, layer->experts, y_dtype), y_dtype, nullptr, stream),
+                                    fp8_plan(b, layer->n, layer->m, layer->experts, y_dtype), y_type(y_dtype), nullptr,
+                                    stream),
                     "fp8_grouped_gemm");
 }
 
@@ -229,7 +235,8 @@ int svdq_fp8_grouped_linear(const uint16_t* x, int x_rows, const int32_t* row_in
   st = hip_status(launch_fp8_act(x, x_rows, layer->m, ws, ws + w.as_off, stream), "fp8_quantize_act");
   if (st) return st;
   return hip_status(launch_fp8_gemm(grouped_args(ws, ws + w.as_off, x_rows, row_index, offsets, *layer, b, ep),
-                                    fp8_plan(b, layer->n, layer->m, layer->experts, y_dtype), y_dtype, nullptr, stream),
+                                    fp8_plan(b, layer->n, layer->m, layer->experts, y_dtype), y_type(y_dtype), nullptr,
+                                    stream),
                     "fp8_grouped_gemm");
 }
 

@@ -436,7 +436,7 @@ __device__ __forceinline__ void tile_at(int u, int tiles_m, int tiles_n, int& ti
   ti = band * 8 + in - tj * high;
 }
 
-// Tiles of 256 x 256, one workgroup a CU, for whole rounds of the CUs; the tiles left
+// Tiles of 256 x 256 by the 8-bit instruction (fast sums), one workgroup a CU, for whole rounds of the CUs; the tiles left
 // over are cut into PARTS of 256 x 128 or 128 x 128, so that the last round takes every
 // CU for the time of a part.  A step takes 2870 cycles, 2048 of them its multiplications'
 // (LDS reads and the barrier the rest); before the first step and behind the last one
@@ -514,7 +514,7 @@ __global__ __launch_bounds__(512) void fp8_big_grouped_kernel(Fp8Args a, int til
 // whole tiles; the L2s' 16 TB/s of records bound it), fp32 results, and few tiles,
 // which may be split along the channels (PIECES: piece p of tile u takes every block
 // from p G / pieces to (p + 1) G / pieces and leaves its sums in slot u pieces + p).
-template <bool EXACT, bool GROUPED, bool PIECES>
+template <bool EXACT, bool OUT_BF16, bool GROUPED, bool PIECES>
 __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8Args a, int tiles_m, int tiles_n, int pieces, f32x4* sums) {
   typedef TileShape<4, 2, 2> Shape;
   __shared__ __align__(16) uint8_t s_even[Shape::kBuffer];
@@ -551,14 +551,14 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8Args a, int tiles_m, i
       sums += (size_t)u * (128 * 128 / 4);
     }
   }
-  tile<4, 2, 2, EXACT, !EXACT, GROUPED, PIECES>(a, qx, ascale, qw, wscale, bias, G, i0, j0, row_end, s_even, s_odd,
+  tile<4, 2, 2, EXACT, OUT_BF16, GROUPED, PIECES>(a, qx, ascale, qw, wscale, bias, G, i0, j0, row_end, s_even, s_odd,
                                                 s_scale_even, s_scale_odd, sums);
 }
 
 // Tiles of 64 x 128, three workgroups a CU, where those of 128 x 128 leave CUs idle: half
 // the multiplications in a step's chain (333 rows, 1000 -> 1500 in fp32: 9.9 us, where
 // 36 tiles of 128 x 128 take 13.5).
-template <bool EXACT>
+template <bool EXACT, bool OUT_BF16>
 __global__ __launch_bounds__(256) void fp8_small_kernel(Fp8Args a, int tiles_m, int tiles_n) {
   typedef TileShape<2, 2, 2> Shape;
   __shared__ __align__(16) uint8_t s_even[Shape::kBuffer];
@@ -567,7 +567,7 @@ __global__ __launch_bounds__(256) void fp8_small_kernel(Fp8Args a, int tiles_m, 
   __shared__ __align__(16) uint8_t s_scale_odd[Shape::kScales];
   int ti, tj;
   tile_at(xcd_range((int)blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
-  tile<2, 2, 2, EXACT, !EXACT, false, false>(a, a.qx, a.ascale, a.qw, a.wscale, a.bias, a.G, ti * 64, tj * 128, a.b,
+  tile<2, 2, 2, EXACT, OUT_BF16, false, false>(a, a.qx, a.ascale, a.qw, a.wscale, a.bias, a.G, ti * 64, tj * 128, a.b,
                                              s_even, s_odd, s_scale_even, s_scale_odd, nullptr);
 }
 
@@ -602,7 +602,7 @@ __global__ __launch_bounds__(256) void fp8_pieces_kernel(Fp8Args a, int tiles_m,
 
 int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& p, int y_dtype, void* ws, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const bool exact = y_dtype == SVDQ_OUT_F32;
+  const bool bf = y_dtype == SVDQ_OUT_BF16;
   if (p.big) {
     const int tm = (a.b + 255) / 256, tn = (a.n + 255) / 256;
     if (a.groups.offsets) return launch_checked(fp8_big_grouped_kernel, p.split.grid, 512, st, a, tn);
@@ -612,18 +612,25 @@ int launch_fp8_tiles(const Fp8Args& a, const Fp8Plan& p, int y_dtype, void* ws, 
   const int tm = (a.b + 127) / 128, tn = (a.n + 127) / 128;
   if (p.small) {
     auto go = [&](auto kernel) { return launch_checked(kernel, p.split.grid, 256, st, a, (a.b + 63) / 64, tn); };
-    return exact ? go(fp8_small_kernel<true>) : go(fp8_small_kernel<false>);
+    if (p.fast) return go(fp8_small_kernel<false, true>);
+    return bf ? go(fp8_small_kernel<true, true>) : go(fp8_small_kernel<true, false>);
   }
   f32x4* sums = reinterpret_cast<f32x4*>(ws);
   auto go = [&](auto kernel) { return launch_checked(kernel, p.split.grid, 256, st, a, tm, tn, p.pieces, sums); };
-  if (a.groups.offsets) return exact ? go(fp8_tile_kernel<true, true, false>) : go(fp8_tile_kernel<false, true, false>);
-  if (p.pieces == 1) return exact ? go(fp8_tile_kernel<true, false, false>) : go(fp8_tile_kernel<false, false, false>);
-  const int status = exact ? go(fp8_tile_kernel<true, false, true>) : go(fp8_tile_kernel<false, false, true>);
+  // (the kinds of sums and of y that there are)
+  auto pick = [&](auto GROUPED, auto PIECES) {
+    constexpr bool g = decltype(GROUPED)::value, k = decltype(PIECES)::value;
+    if (p.fast) return go(fp8_tile_kernel<false, true, g, k>);
+    return bf ? go(fp8_tile_kernel<true, true, g, k>) : go(fp8_tile_kernel<true, false, g, k>);
+  };
+  if (a.groups.offsets) return pick(std::true_type{}, std::false_type{});
+  if (p.pieces == 1) return pick(std::false_type{}, std::false_type{});
+  const int status = pick(std::false_type{}, std::true_type{});
   if (status != 0) return status;
   auto join = [&](auto kernel) {
     return launch_checked(kernel, (long long)tm * tn * 4, 256, st, a, tm, tn, p.pieces, (const f32x4*)sums);
   };
-  return exact ? join(fp8_pieces_kernel<false>) : join(fp8_pieces_kernel<true>);
+  return bf ? join(fp8_pieces_kernel<true>) : join(fp8_pieces_kernel<false>);
 }
 
 }  // namespace svdq

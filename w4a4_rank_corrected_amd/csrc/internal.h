@@ -274,10 +274,14 @@ struct Fp8Args {
 // kernel with rb 16-row blocks a workgroup; or (rb 0) tiles of 128 x 128, in `pieces`
 // along the channels; or (small) of 64 x 128; or (big) the first `full` tiles of 256 x 256 and the others in
 // `parts` (1: there are no others).
+// fast: tiles by the 8-bit matrix instruction (SVDQ_FP8_FAST_SUMS asked for), otherwise by
+// the bf16 one.  y_dtype as the C ABI takes it, flag and all; y_dtype of the launchers
+// without the flag.
 struct Fp8Plan {
   int rb, big, small, full, parts, pieces, threads;
   RowsSplit split;
   size_t ws_bytes;
+  bool fast;
 };
 Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype);
 int launch_fp8_act(const uint16_t* x, int b, int m, uint8_t* qx, uint8_t* ascale, void* stream);

@@ -124,11 +124,11 @@ namespace {
 
 // Microseconds of an 8-bit floating-point product by tiles of 128 x 128 in k pieces, as
 // measured: a launch and a tile's ends 4, a step 0.6 with one workgroup on a CU and 0.96
-// for both of two (results in fp32: 0.96 and 1.65); for pieces a second launch, and the
+// for both of two (exact, by the bf16 matrix instruction: 0.96 and 1.65); for pieces a second launch, and the
 // sums, 64 KB a piece, written and read.
-//   tiles x pieces, steps of all pieces, bf16: 72 x 1, 36: 26.7; 72 x 2: 20.7; 72 x 4: 20.3;
+//   tiles x pieces, steps of all pieces, fast: 72 x 1, 36: 26.7; 72 x 2: 20.7; 72 x 4: 20.3;
 //   18 x 1, 36: 21.0; x 2: 15.4; x 4: 12.5; x 8: 15.0;  80 x 1, 16: 11.7; x 2: 15.5;
-//   128 x 1, 64: 43.7; x 2: 30.9; x 4: 27.7;  fp32: 72 x 1, 36: 39.5; x 2: 26.4; x 4: 25.8
+//   128 x 1, 64: 43.7; x 2: 30.9; x 4: 27.7;  exact: 72 x 1, 36: 39.5; x 2: 26.4; x 4: 25.8
 double fp8_tiles_us(long long tiles, int G, int k, bool exact) {
   const double units = (double)(tiles * k);
   const double step = units <= kMaxCUs ? (exact ? 0.96 : 0.6) : (exact ? 1.65 : 0.96);
@@ -137,9 +137,9 @@ double fp8_tiles_us(long long tiles, int G, int k, bool exact) {
 }
 
 // The same by tiles of 64 x 128, whole (128 x 128, in the best pieces, against it):
-//   fp32: 333 rows, 1000 -> 1500 13.5, 9.9; 512, 1152 -> 1152 12.6, 10.4; 1000, 2048 -> 2048
+//   exact: 333 rows, 1000 -> 1500 13.5, 9.9; 512, 1152 -> 1152 12.6, 10.4; 1000, 2048 -> 2048
 //   20.7, 16.1; 256, 1152 -> 6912 14.4, 11.0; 1000, 4608 -> 1152 22.9, 30.0; 2048, 2048 ->
-//   2048 22.6, 23.6;  bf16: 333, 1000 -> 1500 9.7, 7.8; 512, 2048 -> 2048 11.7, 10.5;
+//   2048 22.6, 23.6;  fast: 333, 1000 -> 1500 9.7, 7.8; 512, 2048 -> 2048 11.7, 10.5;
 //   1000, 2048 -> 2048 11.8, 10.8; 256, 4608 -> 4608 18.2, 21.5; 2048, 2048 -> 2048 13.0, 14.8
 double fp8_small_us(long long tiles, int G, bool exact) {
   const double units = (double)tiles;
@@ -161,7 +161,7 @@ double fp8_rows_us(double steps, int rb, bool grouped) {
 }  // namespace
 
 // The 8-bit floating-point product of one layer (experts 0) or of experts' rows:
-//   * bf16 results of one layer with more than 128 tiles of 256 x 256: those tiles, which
+//   * fast sums of one layer with more than 128 tiles of 256 x 256: those tiles, which
 //     take half the records from the L2s that 128 x 128 ones do (16 TB/s of them were that
 //     kernel's limit: 8192 x 8192 -> 8192 487 us against 377); their last round is cut
 //     smaller where the tiles left over are few: 4608 x 4608 -> 12288 (96 of 864 left)
@@ -175,8 +175,8 @@ double fp8_rows_us(double steps, int rb, bool grouped) {
 //     quickest.
 Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
   const int G = fp8_blocks(m);
-  const bool exact = y_dtype == SVDQ_OUT_F32, grouped = experts > 0;
-  Fp8Plan p{0, 0, 0, 0, 1, 1, 256, {1, 1, 0}, 0};
+  const bool exact = y_dtype != (SVDQ_OUT_BF16 | SVDQ_FP8_FAST_SUMS), grouped = experts > 0;
+  Fp8Plan p{0, 0, 0, 0, 1, 1, 256, {1, 1, 0}, 0, !exact};
   const long long big = (long long)((b + 255) / 256) * ((n + 255) / 256);
   if (!grouped && !exact && big > 128) {
     p.big = 1;
