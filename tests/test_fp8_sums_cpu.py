@@ -60,3 +60,21 @@ def test_exact_sums_unless_asked_for():
                 for E in (0, 8):
                     assert not kernel(b, n, m, E, "bf16").startswith("big"), (b, n, m, E)
                     assert kernel(b, n, m, E, "bf16") == kernel(b, n, m, E, "f32")
+
+
+# weights of some MB to 500 MB: up-projections, output layers
+WIDE = [(1152, 6912), (1152, 32768), (128, 33024), (4096, 14336), (4096, 32769), (4096, 128256), (8192, 8192), (8192, 28672),
+        (16384, 7168), (2048, 32000), (2048, 65536), (8192, 65536)]
+
+
+@pytest.mark.parametrize("m,n", WIDE)
+@pytest.mark.parametrize("out", ["bf16", "f32", "fast"])
+def test_one_row_of_a_wide_layer_takes_the_row_kernel(m, n, out):
+    """It reads the weights at memory's rate; tiles of 64 rows and more leave all but one of them empty."""
+    assert kernel(1, n, m, 0, out) == "rows 1"
+
+
+@pytest.mark.parametrize("m,n", WIDE)
+def test_few_rows_take_no_tiles_of_256_rows(m, n):
+    for b in (1, 16, 64, 128):
+        assert not kernel(b, n, m, 0, "fast").startswith("big")

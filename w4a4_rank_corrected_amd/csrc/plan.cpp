@@ -153,16 +153,23 @@ double fp8_small_us(long long tiles, int G, bool exact) {
 //   64, 8192 -> 8192 62 / 48 / 43; 16 rows of it 19.3 with rb 1;
 //   64 experts, 2048 -> 1408, mean rows 1: 21.7 (tiles 15.1), 8: 52.9 (21.9), 32: 110 (37);
 //   8 experts, 4096 -> 1152, mean 1: 9.3 (18.9), 8: 16.1 (23.6), 16: 19.3 (23.5), 32: 27.4 (24.1)
-double fp8_rows_us(double steps, int rb, bool grouped) {
+// of one layer with weights from memory, rows 1 / 4 / 8 / 16: 8192 -> 28672 47.6 / 48.0 / 53.4 / 64.0 (tiles
+//   of 64 x 128 59-60); 4096 -> 14336 16.7 / 16.2 / 17.6 / 20.3; 4096 -> 128256 92 / 94 / 104 / 126 (102-103)
+double fp8_rows_us(double steps, int rb, int b, bool grouped) {
   if (grouped) return 3.5 + (rb == 1 ? 0.00035 : 0.0006) * steps;
-  return rb == 1 ? 3.5 + 0.0005 * steps : (rb == 2 ? 4.0 + 0.0007 * steps : 6.3 + 0.0011 * steps);
+  if (rb == 1) return 3.5 + (0.00036 + 0.00014 * std::min(b, 16) / 16) * steps;
+  return rb == 2 ? 4.0 + 0.0007 * steps : 6.3 + 0.0011 * steps;
 }
+
+// No tiles of one layer are quicker than a launch and the weights from memory (5.1 TB/s).
+double fp8_memory_us(int n, int m) { return 4.0 + (double)n * m / 5.1e6; }
 
 }  // namespace
 
 // The 8-bit floating-point product of one layer (experts 0) or of experts' rows:
-//   * fast sums of one layer with more than 128 tiles of 256 x 256: those tiles, which
-//     take half the records from the L2s that 128 x 128 ones do (16 TB/s of them were that
+//   * fast sums of more than 128 rows of one layer with more than 128 tiles of 256 x 256 (fewer
+//     rows leave half of each tile empty: 4096 -> 128256, 128 rows 125 against 111 by 128 x 128,
+//     129 rows 123 against 158): those tiles, which take half the records from the L2s that 128 x 128 ones do (16 TB/s of them were that
 //     kernel's limit: 8192 x 8192 -> 8192 487 us against 377); their last round is cut
 //     smaller where the tiles left over are few: 4608 x 4608 -> 12288 (96 of 864 left)
 //     212 whole, 204 in halves, 216 in quarters; 4096 x 1152 -> 4608 (32 of 288) 36.5,
@@ -178,7 +185,7 @@ Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
   const bool exact = y_dtype != (SVDQ_OUT_BF16 | SVDQ_FP8_FAST_SUMS), grouped = experts > 0;
   Fp8Plan p{0, 0, 0, 0, 1, 1, 256, {1, 1, 0}, 0, !exact};
   const long long big = (long long)((b + 255) / 256) * ((n + 255) / 256);
-  if (!grouped && !exact && big > 128) {
+  if (!grouped && !exact && b > 128 && big > 128) {
     p.big = 1;
     const long long full = big / kMaxCUs * kMaxCUs, left = big - full;
     p.parts = left == 0 || left > 128 ? 1 : (left > 64 ? 2 : 4);
@@ -195,21 +202,22 @@ Fp8Plan fp8_plan(int b, int n, int m, int experts, int y_dtype) {
     return p;
   }
   const long long tiles = (grouped ? grouped_row_blocks(b, experts, 128) : (b + 127) / 128) * ((n + 127) / 128);
-  double best = fp8_tiles_us(tiles, G, 1, exact);
+  const double least = grouped ? 0.0 : fp8_memory_us(n, m);
+  double best = std::max(fp8_tiles_us(tiles, G, 1, exact), least);
   for (int k : {2, 3, 4, 6, 8}) {
     if (grouped || G < 2 * k) break;
-    const double us = fp8_tiles_us(tiles, G, k, exact);
+    const double us = std::max(fp8_tiles_us(tiles, G, k, exact), least);
     if (us < best) best = us, p.pieces = k;
   }
   const long long small = (long long)((b + 63) / 64) * ((n + 127) / 128);
   if (!grouped) {
-    const double us = fp8_small_us(small, G, exact);
+    const double us = std::max(fp8_small_us(small, G, exact), least);
     if (us < best) best = us, p.small = 1;
   }
   for (int rb : {1, 2, 4}) {
     if (grouped && rb != (mean <= 16 ? 1 : (mean <= 32 ? 2 : 4))) continue;
     const long long blocks = grouped ? grouped_row_blocks(b, experts, 16 * rb) : (b + 16 * rb - 1) / (16 * rb);
-    const double us = fp8_rows_us((double)blocks * (double)((n + 15) / 16) * G, rb, grouped);
+    const double us = fp8_rows_us((double)blocks * (double)((n + 15) / 16) * G, rb, b, grouped);
     if (us >= best) continue;
     best = us;
     p.rb = rb;
