@@ -680,7 +680,8 @@ int svdq_sort_rows(const int32_t* expert, int t, int k, int experts, int32_t* of
                    int32_t* index, void* workspace, size_t workspace_bytes, void* stream);
 
 /* DEVICE: the tokens' rows in the order that `index` gives (the transpose of
- * svdq_combine_rows):
+ * svdq_combine_rows where each row is named once, as by svdq_sort_rows; of any
+ * index it is svdq_combine_rows_grad without dweight):
  *     rows[index[t,q], j] = weight[t,q] x[t,j]
  * one product in fp32, rounded once.
  *   x [t][n] in dtype (SVDQ_OUT_BF16 or SVDQ_OUT_F32); weight fp32 [t][k] or NULL
@@ -692,18 +693,22 @@ int svdq_sort_rows(const int32_t* expert, int t, int k, int experts, int32_t* of
 int svdq_dispatch_rows(const void* x, int t, int n, int dtype, const int32_t* index, const float* weight, int k, int R,
                        void* rows, void* stream);
 
-/* DEVICE: the gradient of svdq_combine_rows.  For dy = d loss / d y:
- *     drows[index[t,q], j] = weight[t,q] dy[t,j]     (as svdq_dispatch_rows)
- *     dweight[t,q] = sum_j dy[t,j] rows[index[t,q], j]    (fp32, a fixed order)
- * and dweight 0 for an index outside [0, R).  The residual's gradient is dy.
+/* DEVICE: the gradient of svdq_combine_rows, for every index that it takes.  For
+ * dy = d loss / d y:
+ *     drows[r,j] = sum over the (t,q) with index[t,q] = r of weight[t,q] dy[t,j]
+ *     dweight[t,q] = sum_j dy[t,j] rows[index[t,q], j]
+ * summed in fp32 in a fixed order (drows: that of the slots) and, drows, rounded
+ * once.  A row that no slot names gets 0; an index outside [0, R), also svdq_sort_rows'
+ * -1 - r, names no row, and its dweight is 0.  The residual's gradient is dy.
  *   dy [t][n], rows [R][n], drows [R][n] in dtype; dweight fp32 [t][k].  drows
  *   or dweight may be NULL (not wanted; without dweight rows is not used).
- *   weight NULL: ones.  index: each row named once at the most, as
- *   svdq_sort_rows writes it; of a row that several slots name drows gets one
- *   slot's part, in pieces, not the sum (dweight is right all the same).
- *   drows and dweight are apart from each other and from the inputs, except that
- *   drows may be rows when each row is named once at the most.  Element
- *   alignment.  1 <= k <= SVDQ_MAX_EXPERTS.
+ *   weight NULL: ones.  drows and dweight are apart from each other and from the
+ *   inputs, except that drows may be rows.  Element alignment.
+ *   1 <= k <= SVDQ_MAX_EXPERTS.  t = 0: nothing is written (drows of no tokens is
+ *   the caller's to clear).
+ * Rows that very many slots name (more than 64, or thousands of slots beyond the first
+ * among neighbouring rows) cost a reading of the index for every 512 (fp32: 256)
+ * columns.
  * The gradient of a grouped layer's gather (row_index) is svdq_combine_rows of
  * the rows' gradients without weights. */
 int svdq_combine_rows_grad(const void* dy, int t, int n, int dtype, const int32_t* index, const float* weight, int k,

@@ -1314,7 +1314,8 @@ def _scatter_operands(x, name, index, weight):
 def svdq_dispatch_rows(x, index, weight=None, rows=None, stream=None):
     """rows[index[t, q]] = weight[t, q] x[t] (weight None: copies), index int32
     [t][k] as svdq_sort_rows gives it: a dropped slot's row (-1 - index) becomes
-    zero.  rows: [R][n] of x's dtype; allocated here, it has t k rows."""
+    zero.  rows: [R][n] of x's dtype; allocated here, it has t k rows, each of
+    which svdq_sort_rows' index names (a row that no slot names is not written)."""
     import torch
     t, n, k = _scatter_operands(x, "x", index, weight)
     dev = x.device
@@ -1330,13 +1331,13 @@ def svdq_dispatch_rows(x, index, weight=None, rows=None, stream=None):
 
 
 def svdq_combine_rows_grad(dy, index, weight=None, rows=None, drows=None, dweight=None, stream=None):
-    """The gradient of svdq_combine_rows(rows, index, weight): (drows, dweight) with
-    drows[index[t, q]] = weight[t, q] dy[t] and dweight[t, q] = dy[t] . rows[index[t, q]]
-    (0 for a dropped slot).  The residual's gradient is dy.
+    """The gradient of svdq_combine_rows(rows, index, weight), for every index that
+    it takes: (drows, dweight) with drows[r] the sum of weight[t, q] dy[t] over the
+    slots that name r (0 where none does) and dweight[t, q] = dy[t] . rows[index[t, q]]
+    (0 for an index outside the rows).  The residual's gradient is dy.
 
     rows: [R][n] of dy's dtype; without it only drows (t k rows, unless given) is
-    computed and dweight is None.  index: each row named once at the most, as
-    svdq_sort_rows gives it."""
+    computed and dweight is None.  drows may be rows."""
     import torch
     t, n, k = _scatter_operands(dy, "dy", index, weight)
     dev = dy.device
@@ -1354,6 +1355,8 @@ def svdq_combine_rows_grad(dy, index, weight=None, rows=None, drows=None, dweigh
         _dev(rows, "rows", dy.dtype, (R, n), dev)
         _dev(drows, "drows", dy.dtype, (R, n), dev)
         _dev(dweight, "dweight", torch.float32, (t, k), dev)
+        if t == 0:
+            drows.zero_()
         _check(lib().svdq_combine_rows_grad(_ptr(dy), t, n, _out_code(dy.dtype), _ptr(index), _ptr(weight), k,
                                             _ptr(rows), R, _ptr(drows), _ptr(dweight), handle))
     return drows, dweight

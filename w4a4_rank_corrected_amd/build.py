@@ -20,11 +20,11 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsvdq.so")
 
-HOST_SOURCES = ["api.cpp", "epi_api.cpp", "fp8_api.cpp", "route_api.cpp", "prep.cpp", "bundle.cpp", "plan.cpp"]
+HOST_SOURCES = ["api.cpp", "epi_api.cpp", "fp8_api.cpp", "route_api.cpp", "grad_api.cpp", "prep.cpp", "bundle.cpp", "plan.cpp"]
 HIP_SOURCES = ["act_kernels.hip", "gemm_kernels.hip", "epi_kernels.hip", "rows_kernels.hip", "group_kernels.hip",
                "fp8_kernels.hip", "fp8_tiles.hip", "route_kernels.hip", "scratch.hip"]
 HEADERS = ["internal.h", "checks.h", "device_common.h", "quant.h", "epilogue.h", "grouped.h", "gemm_body.h", "launch.h",
-           "fp8.h"]
+           "fp8.h", "route_checks.h"]
 
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")

@@ -247,8 +247,16 @@ struct SortPlan {
 SortPlan sort_plan(int b);
 int launch_sort_rows(const int32_t* expert, int b, int k, int experts, int32_t* offsets, int32_t* row_index,
                      int32_t* index, void* ws, void* stream);
-// drows NULL: the weights' gradient only; dweight NULL: the rows only.
+// The dispatch of rows x to drows (rows, dweight NULL), or the weights' gradient alone (drows NULL).
 int launch_scatter_rows(const void* x, int t, int n, int dtype, const int32_t* index, const float* weight, int k,
+                        const void* rows, int R, void* drows, float* dweight, void* stream);
+// Workgroups of the rows' gradient, `per` rows each.
+struct GradPlan {
+  int per, blocks;
+};
+GradPlan grad_plan(int R);
+// drows NULL: the weights' gradient only; dweight NULL: the rows' only.
+int launch_combine_grad(const void* dy, int t, int n, int dtype, const int32_t* index, const float* weight, int k,
                         const void* rows, int R, void* drows, float* dweight, void* stream);
 
 // ---- the 8-bit floating-point setting --------------------------------------------

@@ -120,6 +120,15 @@ SortPlan sort_plan(int b) {
   return p;
 }
 
+// The rows' gradient of the combination: two workgroups a CU, each reading the whole
+// index once; 4096 rows at the most (8 bytes each in LDS, beside 16 KB of lists).
+GradPlan grad_plan(int R) {
+  GradPlan p;
+  p.per = std::min(std::max((R + 2 * kMaxCUs - 1) / (2 * kMaxCUs), 1), 4096);
+  p.blocks = (R + p.per - 1) / p.per;
+  return p;
+}
+
 namespace {
 
 // Microseconds of an 8-bit floating-point product by tiles of 128 x 128 in k pieces, as

@@ -173,14 +173,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
 }
 
 // ---------------------------------------------------------------------------
-// Dispatch, and the gradient of the combination:
-//     drows[index[t,q]] = weight[t,q] x[t],   dweight[t,q] = x[t] . rows[index[t,q]]
+// Dispatch, and the weights' gradient of the combination, driven by the tokens:
+//     rows[index[t,q]] = weight[t,q] x[t],   dweight[t,q] = x[t] . rows[index[t,q]]
 // nw waves take a token, each every nw-th chunk of 64 W columns (16 bytes a lane),
-// its rows eight at a time, all loads of a chunk together.  x is read once for
-// eight rows; a row's elements are read before they are written (drows may be
-// rows).  Sums: a lane's own products in order, then the lanes by halves, then
-// the waves in order, all in fp32.  Memory bounds both: 4096 x 6 rows of 2048 in bf16,
-// dispatch 20.6 us, 5.7 TB/s, gradient 45.5 us, 4.8 TB/s.
+// its rows eight at a time, all loads of a chunk together; x is read once for eight
+// rows.  Sums: a lane's own products in order, then the lanes by halves, then the
+// waves in order, all in fp32.  Memory bounds it: 4096 x 6 rows of 2048 in bf16,
+// dispatch 20.6 us, 5.7 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kRouteBatch = 8;
 
@@ -229,21 +228,23 @@ struct RowVector {
   }
 };
 
-template <bool BF16, bool DOT, bool WRITE>
-__global__ __launch_bounds__(256) void scatter_rows_kernel(const void* __restrict__ x, int t_count, int n,
-                                                           const int32_t* __restrict__ index,
-                                                           const float* __restrict__ weight, int k, const void* rows,
-                                                           int R, void* drows, float* __restrict__ dweight, int nw) {
+// The tokens of workgroup `block` of kWaves waves.  WRITE: dispatch; otherwise the weights' gradient.
+template <bool BF16, bool WRITE, int kWaves>
+__device__ __forceinline__ void token_part(const void* __restrict__ x, int t_count, int n,
+                                           const int32_t* __restrict__ index, const float* __restrict__ weight, int k,
+                                           const void* rows, int R, void* out, float* __restrict__ dweight, int nw,
+                                           long long block) {
   typedef RowVector<BF16> V;
   constexpr int W = V::W;
-  __shared__ float s_dot[4][kRouteBatch];
+  constexpr bool DOT = !WRITE;
+  __shared__ float s_dot[kWaves][kRouteBatch];
   const int lane = (int)(threadIdx.x & 63);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int part = wave % nw;
-  const long long t = (long long)blockIdx.x * (4 / nw) + wave / nw;
+  const long long t = block * (kWaves / nw) + wave / nw;
   const bool live = t < t_count;
   for (int q0 = 0; q0 < k; q0 += kRouteBatch) {
-    int row[kRouteBatch];  // the slot's row: >= 0 used, -1 - r to be cleared, below -R not there
+    int row[kRouteBatch];  // the slot's row: >= 0 used, -1 - r to be cleared (dispatch), below -R not there
     float w[kRouteBatch], dot[kRouteBatch];
 #pragma unroll
     for (int q = 0; q < kRouteBatch; ++q) {
@@ -292,7 +293,7 @@ __global__ __launch_bounds__(256) void scatter_rows_kernel(const void* __restric
                 o = xv;
               }
             }
-            V::put(drows, row[q] >= 0 ? row[q] : -1 - row[q], n, j, o);
+            V::put(out, row[q] >= 0 ? row[q] : -1 - row[q], n, j, o);
           }
         }
       }
@@ -312,6 +313,197 @@ __global__ __launch_bounds__(256) void scatter_rows_kernel(const void* __restric
       __syncthreads();
     }
   }
+}
+
+template <bool BF16, bool WRITE>
+__global__ __launch_bounds__(256) void scatter_rows_kernel(const void* __restrict__ x, int t_count, int n,
+                                                           const int32_t* __restrict__ index,
+                                                           const float* __restrict__ weight, int k, const void* rows,
+                                                           int R, void* drows, float* __restrict__ dweight, int nw) {
+  token_part<BF16, WRITE, 4>(x, t_count, n, index, weight, k, rows, R, drows, dweight, nw, blockIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// The rows' gradient of the combination, driven by the rows:
+//     drows[r] = sum over the slots (t,q) that name r, in their order, of weight[t,q] dy[t]
+// so that a row that no slot names becomes zero, one that several name gets their sum
+// in a fixed order, and a slot that names none touches nothing.  A workgroup takes
+// `per` neighbouring rows.  It reads the whole index (all loads of a round together)
+// and keeps in LDS the slots that name its rows: one in the row's own entry, further
+// ones in a list behind it, which is put into the slots' order; then its waves take
+// four chunks of 64 W columns of a row at a time.  Lists longer than kListMost or
+// beyond the workgroup's kLinks links are given up: such a row's slots are found by
+// reading the index again for each of its chunks.
+// ---------------------------------------------------------------------------
+constexpr int kGradThreads = 512, kGradWaves = kGradThreads / 64;
+constexpr int kLinks = 2048, kListMost = 64;
+constexpr uint32_t kNone = ~0u, kEnd = ~0u - 1, kMany = ~0u - 2;  // Namer::next: no slot, the list's end, given up
+struct Namer {
+  uint32_t slot, next;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void rows_part(const void* __restrict__ dy, int t_count, int n,
+                                          const int32_t* __restrict__ index, const float* __restrict__ weight, int k,
+                                          int R, void* drows, int per, int block, Namer* named) {
+  typedef RowVector<BF16> V;
+  constexpr int W = V::W;
+  Namer* links = named + per;
+  __shared__ uint32_t s_links;
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r0 = block * per, count = min(per, R - r0);
+  const size_t total = (size_t)t_count * k;  // at most 2^32 slots: 0 .. 2^32 - 1
+  for (int i = tid; i < count; i += kGradThreads) named[i].next = kNone;
+  if (tid == 0) s_links = 0;
+  __syncthreads();
+  auto name = [&](uint32_t row, uint32_t slot) {
+    Namer& at = named[row];
+    if (atomicCAS(&at.next, kNone, kEnd) == kNone) {
+      at.slot = slot;
+      return;
+    }
+    const uint32_t e = atomicAdd(&s_links, 1u);
+    if (e < (uint32_t)kLinks) {
+      links[e].slot = slot;
+      links[e].next = atomicExch(&at.next, e);
+    } else {
+      atomicExch(&at.next, kMany);  // (links put before it later end in it)
+    }
+  };
+  constexpr int B = 4;  // vectors of four slots a thread has under way
+  for (size_t s0 = 0; s0 < total; s0 += 4 * B * kGradThreads) {
+    u32x4 v[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const size_t s = s0 + 4 * ((size_t)i * kGradThreads + tid);
+      v[i] = u32x4{~0u, ~0u, ~0u, ~0u};
+      if (s + 4 <= total) {
+        v[i] = *reinterpret_cast<const u32x4_at4*>(index + s);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (s + e < total) v[i][e] = (uint32_t)index[s + e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // (what lies outside the R rows lies outside these; a filled-up place is -1)
+        const uint32_t row = v[i][e] - (uint32_t)r0;
+        if (row < (uint32_t)count) name(row, (uint32_t)(s0 + 4 * ((size_t)i * kGradThreads + tid) + e));
+      }
+  }
+  __syncthreads();
+  // lists into the slots' order: the least of the rest to each place
+  for (int i = tid; i < count; i += kGradThreads) {
+    uint32_t first = named[i].next;
+    if (first >= kMany) continue;
+    int length = 1;
+    for (uint32_t e = first; e < kMany && length <= kListMost; e = links[e].next) {
+      ++length;
+      if (links[e].next == kMany) length = kListMost + 1;
+    }
+    if (length > kListMost) {
+      named[i].next = kMany;
+      continue;
+    }
+    for (Namer* p = &named[i]; p->next != kEnd; p = &links[p->next]) {
+      Namer* least = p;
+      for (uint32_t e = p->next; e != kEnd; e = links[e].next)
+        if (links[e].slot < least->slot) least = &links[e];
+      const uint32_t t = p->slot;
+      p->slot = least->slot;
+      least->slot = t;
+    }
+  }
+  __syncthreads();
+  constexpr int C = 4;  // chunks of a row a wave takes at a time
+  const int groups = (n + C * 64 * W - 1) / (C * 64 * W);
+  for (long long u = wave; u < (long long)count * groups; u += kGradWaves) {
+    const int i = (int)(u / groups), j0 = (int)(u - (long long)i * groups) * C * 64 * W + lane * W;
+    const uint32_t slot = __builtin_amdgcn_readfirstlane(named[i].slot);
+    const uint32_t next = __builtin_amdgcn_readfirstlane(named[i].next);
+    const long long row = r0 + i;
+    if (next == kNone || next == kEnd) {
+      u32x4 o[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        o[c] = u32x4{0u, 0u, 0u, 0u};
+        const int j = j0 + c * 64 * W;
+        if (next == kEnd && j < n) o[c] = V::template get<false>(dy, slot / (uint32_t)k, n, j);
+      }
+      if (weight && next == kEnd) {
+        const float w = weight[slot];
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (BF16)
+              o[c][e] = pack_bf16x2(w * bf16_lo(o[c][e]), w * bf16_hi(o[c][e]));
+            else
+              o[c][e] = __float_as_uint(w * __uint_as_float(o[c][e]));
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int j = j0 + c * 64 * W;
+        if (j < n) V::put(drows, row, n, j, o[c]);
+      }
+      continue;
+    }
+#pragma unroll 1
+    for (int c = 0; c < C; ++c) {
+      const int j = j0 + c * 64 * W;
+      float sum[W];
+      bool any = false;
+      auto add = [&](uint32_t s) {
+        const u32x4 v = j < n ? V::template get<false>(dy, s / (uint32_t)k, n, j) : u32x4{0u, 0u, 0u, 0u};
+        const float w = weight ? weight[s] : 1.0f;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float p = w * V::value(v, e);
+          sum[e] = any ? sum[e] + p : p;
+        }
+        any = true;
+      };
+      if (next != kMany) {
+        add(slot);
+        for (uint32_t e = next; e != kEnd; e = __builtin_amdgcn_readfirstlane(links[e].next))
+          add(__builtin_amdgcn_readfirstlane(links[e].slot));
+      } else {
+        for (size_t s0 = 0; s0 < total; s0 += 64) {
+          uint64_t hits = __ballot(s0 + lane < total && index[s0 + lane] == (int32_t)row);
+          for (; hits; hits &= hits - 1) add((uint32_t)(s0 + __builtin_ctzll(hits)));
+        }
+      }
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = BF16 ? pack_bf16x2(sum[2 * e % W], sum[(2 * e + 1) % W]) : __float_as_uint(sum[e]);
+      if (j < n) V::put(drows, row, n, j, o);
+    }
+  }
+}
+
+// The gradient in one launch: the first row_blocks workgroups take rows, the others tokens'
+// weights (none where dweight is NULL).  4096 x 6 rows of 2048 in bf16: 54.7 us, where
+// the rows alone take 32.9 (dy read once for each row that it reaches, by the caches) and
+// the weights 21.7; tokens' rows written by the tokens' waves, with the rows of no or
+// several slots in a launch before them, 54.8.
+template <bool BF16>
+__global__ __launch_bounds__(kGradThreads) void combine_grad_kernel(const void* __restrict__ dy, int t_count, int n,
+                                                                    const int32_t* __restrict__ index,
+                                                                    const float* __restrict__ weight, int k,
+                                                                    const void* rows, int R, void* drows,
+                                                                    float* __restrict__ dweight, int nw, int per,
+                                                                    int row_blocks) {
+  extern __shared__ __align__(16) Namer grad_lds[];
+  if ((int)blockIdx.x < row_blocks)
+    rows_part<BF16>(dy, t_count, n, index, weight, k, R, drows, per, (int)blockIdx.x, grad_lds);
+  else
+    token_part<BF16, false, kGradWaves>(dy, t_count, n, index, weight, k, rows, R, nullptr, dweight, nw,
+                                        (long long)blockIdx.x - row_blocks);
 }
 
 }  // namespace
@@ -337,25 +529,55 @@ int launch_sort_rows(const int32_t* expert, int b, int k, int experts, int32_t* 
   return (int)hipGetLastError();
 }
 
+namespace {
+
+// Waves of a token: a whole chunk each, or a part where tokens alone do not fill the
+// chip (4096 tokens x 6 rows of 2048, other rows every call: gradient bf16 57 us with
+// one, 60 with two, 50 with four, fp32 105, 108, 91; 4096 x 2 rows of 1001 bf16:
+// dispatch 7.9 with one, 8.8 with two; 300 x 6 rows of 4608 bf16: 18.9, 12.5, 9.8).
+int token_waves(int t, int n, bool bf) {
+  const int chunk = bf ? 512 : 256, whole = n / chunk, units = (n + chunk - 1) / chunk;
+  int nw = 1;
+  while (nw < 4 && (2 * nw <= whole || (2 * nw <= units && (long long)t * nw < 8 * kMaxCUs))) nw *= 2;
+  return nw;
+}
+
+}  // namespace
+
 int launch_scatter_rows(const void* x, int t, int n, int dtype, const int32_t* index, const float* weight, int k,
                         const void* rows, int R, void* drows, float* dweight, void* stream) {
   const bool bf = dtype == SVDQ_OUT_BF16;
-  const int units = (n + (bf ? 512 : 256) - 1) / (bf ? 512 : 256);  // a wave's chunks in a row
-  // Waves of a token: a whole chunk each, or a part where tokens alone do not fill the
-  // chip (4096 tokens x 6 rows of 2048, other rows every call: gradient bf16 57 us with
-  // one, 60 with two, 50 with four, fp32 105, 108, 91; 4096 x 2 rows of 1001 bf16:
-  // dispatch 7.9 with one, 8.8 with two; 300 x 6 rows of 4608 bf16: 18.9, 12.5, 9.8).
-  const int whole = n / (bf ? 512 : 256);
-  int nw = 1;
-  while (nw < 4 && (2 * nw <= whole || (2 * nw <= units && (long long)t * nw < 8 * kMaxCUs))) nw *= 2;
-  const int grid = (int)(((long long)t * nw + 3) / 4);
+  const int nw = token_waves(t, n, bf);
   auto go = [&](auto kernel) {
-    return launch_checked(kernel, grid, 256, (hipStream_t)stream, x, t, n, index, weight, k, rows, R, drows, dweight,
-                          nw);
+    return launch_checked(kernel, ((long long)t * nw + 3) / 4, 256, (hipStream_t)stream, x, t, n, index, weight, k, rows, R,
+                          drows, dweight, nw);
   };
-  if (dweight && drows) return bf ? go(scatter_rows_kernel<true, true, true>) : go(scatter_rows_kernel<false, true, true>);
-  if (dweight) return bf ? go(scatter_rows_kernel<true, true, false>) : go(scatter_rows_kernel<false, true, false>);
-  return bf ? go(scatter_rows_kernel<true, false, true>) : go(scatter_rows_kernel<false, false, true>);
+  if (dweight) return bf ? go(scatter_rows_kernel<true, false>) : go(scatter_rows_kernel<false, false>);
+  return bf ? go(scatter_rows_kernel<true, true>) : go(scatter_rows_kernel<false, true>);
+}
+
+int launch_combine_grad(const void* dy, int t, int n, int dtype, const int32_t* index, const float* weight, int k,
+                        const void* rows, int R, void* drows, float* dweight, void* stream) {
+  const bool bf = dtype == SVDQ_OUT_BF16;
+  const int nw = token_waves(t, n, bf);
+  if (!drows || R == 0) return launch_scatter_rows(dy, t, n, dtype, index, weight, k, rows, R, nullptr, dweight, stream);
+  long long tokens = dweight ? ((long long)t * nw + kGradWaves - 1) / kGradWaves : 0;
+  if (dweight && drows == rows) {  // all rows are read before any is written
+    const int status = launch_scatter_rows(dy, t, n, dtype, index, weight, k, rows, R, nullptr, dweight, stream);
+    if (status != 0) return status;
+    tokens = 0;
+  }
+  const GradPlan p = grad_plan(R);
+  auto go = [&](auto kernel) {
+    if (!launch_fits(p.blocks + tokens, kGradThreads)) return (int)hipErrorInvalidConfiguration;
+    const int ok = scratch_free(reinterpret_cast<const void*>(kernel));
+    if (ok != 0) return ok;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.blocks + tokens)), dim3(kGradThreads),
+                       (size_t)(p.per + kLinks) * sizeof(Namer), (hipStream_t)stream, dy, t, n, index, weight, k, rows, R,
+                       drows, dweight, nw, p.per, p.blocks);
+    return (int)hipGetLastError();
+  };
+  return bf ? go(combine_grad_kernel<true>) : go(combine_grad_kernel<false>);
 }
 
 }  // namespace svdq
