@@ -212,3 +212,36 @@ def test_most_rows(S, Rn):
     index = rng.integers(-1, Rn, (200000, 4))
     index[1000] = index[1001]
     check(S, index, Rn, 2, "f32", True, 5)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_rows_past_32_bit_offsets(S, out):
+    """Rows of more than 4 GB: the gradients and the dispatch of the first and the last ones."""
+    n, t, k = 4096, 40, 3
+    Rn = 300000 if out == "f32" else 600000
+    rng = np.random.default_rng(3)
+    at = np.concatenate([rng.choice(50, 60, replace=True), Rn - 1 - rng.choice(50, 60, replace=True)])
+    index = rng.permutation(at).reshape(t, k)
+    rows = torch.zeros(Rn, n, dtype=dt(out), device="cuda")
+    used = np.unique(index)
+    some, sd = data(rng, (len(used), n), out)
+    rows[torch.from_numpy(used).cuda()] = sd
+    dy, dyd = data(rng, (t, n), out)
+    idx = torch.from_numpy(index.astype(np.int32)).cuda()
+    place = np.searchsorted(used, index)
+    d, size, terms, dw, ds = reference(dy, some, place, None)
+    drows, dweight = S.svdq_combine_rows_grad(dyd, idx, None, rows, drows=torch.full_like(rows, float("nan")))
+    got = drows[torch.from_numpy(used).cuda()].float().cpu().numpy().astype(np.float64)
+    half = 2.0 ** -8 if out == "bf16" else 0.0
+    assert (np.abs(got - d) <= terms[:, None] * R.U * 1.01 * size + np.abs(d) * half * 1.01).all()
+    assert (np.abs(dweight.cpu().numpy() - dw) <= (n + 8) * R.U * ds).all()
+    drows[torch.from_numpy(used).cuda()] = 0
+    for lo in range(0, Rn, 50000):
+        assert (drows[lo: lo + 50000] == 0).all()  # all the others were made zero
+    once, first = np.unique(index, return_index=True)
+    single = np.full((t, k), Rn, np.int64)  # each row once: what dispatch takes
+    single.reshape(-1)[first] = once
+    drows.fill_(7)
+    S.svdq_dispatch_rows(dyd, torch.from_numpy(single.astype(np.int32)).cuda(), rows=drows)
+    assert torch.equal(drows[torch.from_numpy(once).cuda()], dyd[torch.from_numpy(first // k).cuda()])
+    assert (drows[Rn // 2 - 100: Rn // 2 + 100] == 7).all()
