@@ -708,7 +708,8 @@ int svdq_dispatch_rows(const void* x, int t, int n, int dtype, const int32_t* in
  *   the caller's to clear).
  * Rows that very many slots name (more than 64, or thousands of slots beyond the first
  * among neighbouring rows) cost a reading of the index for every 512 (fp32: 256)
- * columns.
+ * columns and their additions one after another: 24576 slots on one row of 2048 take
+ * 20 ms.
  * The gradient of a grouped layer's gather (row_index) is svdq_combine_rows of
  * the rows' gradients without weights. */
 int svdq_combine_rows_grad(const void* dy, int t, int n, int dtype, const int32_t* index, const float* weight, int k,

@@ -440,8 +440,9 @@ __device__ __forceinline__ void tile_at(int u, int tiles_m, int tiles_n, int& ti
 // over are cut into PARTS of 256 x 128 or 128 x 128, so that the last round takes every
 // CU for the time of a part.  A step takes 2870 cycles, 2048 of them its multiplications'
 // (LDS reads and the barrier the rest); before the first step and behind the last one
-// nothing multiplies, 3000 and 4000 cycles: 8192 x 8192 -> 8192 380-400 us (2.75-2.9
-// PFLOP/s), 4608 x 4608 -> 12288 202 (2.6), 4096 x 1152 -> 4608 29 (1.5).
+// nothing multiplies, 3000 and 4000 cycles without an activation: 8192 x 8192 -> 8192
+// 380-400 us (2.75-2.9 PFLOP/s), 4608 x 4608 -> 12288 202 (2.6), with GELU from column
+// 4608 on 225-238; 4096 x 1152 -> 4608 29 (1.5), with GELU 35.
 template <int PARTS>
 __global__ __launch_bounds__(512) void fp8_big_kernel(Fp8Args a, int tiles_m, int tiles_n, int full) {
   typedef TileShape<8, 2, 4> Shape;
@@ -510,8 +511,11 @@ __global__ __launch_bounds__(512) void fp8_big_grouped_kernel(Fp8Args a, int til
 }
 
 // Tiles of 128 x 128, two workgroups a CU (of which one ends while the other multiplies):
-// experts' rows (64 experts, 18006 rows of 2048 -> 1408 in all 100 us: 1.04 PFLOP/s, 1.3 of
-// whole tiles; the L2s' 16 TB/s of records bound it), fp32 results, and few tiles,
+// every product of many rows with exact sums (the bf16 instruction: 8192 x 8192 -> 8192
+// 885 us, 1.24 PFLOP/s, where a library's bf16 product reaches 1.3-1.37; 4608 x 4608 ->
+// 12288 with GELU 453; 4096 x 1152 -> 4608 with GELU 55, its 1152 tiles 2.25 rounds of the
+// CUs), experts' rows (64 experts, 18006 rows of 2048 -> 1408 135 us, fast sums 101; a
+// quarter of the tiles' rows are no expert's: fast sums 73 at even counts), and few tiles,
 // which may be split along the channels (PIECES: piece p of tile u takes every block
 // from p G / pieces to (p + 1) G / pieces and leaves its sums in slot u pieces + p).
 template <bool EXACT, bool OUT_BF16, bool GROUPED, bool PIECES>

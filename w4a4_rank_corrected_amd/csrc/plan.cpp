@@ -162,6 +162,8 @@ double fp8_small_us(long long tiles, int G, bool exact) {
 //   64, 8192 -> 8192 62 / 48 / 43; 16 rows of it 19.3 with rb 1;
 //   64 experts, 2048 -> 1408, mean rows 1: 21.7 (tiles 15.1), 8: 52.9 (21.9), 32: 110 (37);
 //   8 experts, 4096 -> 1152, mean 1: 9.3 (18.9), 8: 16.1 (23.6), 16: 19.3 (23.5), 32: 27.4 (24.1)
+//   (tiles with fast sums; exact ones: 64 experts, mean 2: 34.9 (43.9), 8: 52 (48), 16: 72 (48);
+//   8 experts, mean 8: 15.4 (32.8), 32: 25.9 (33.3), 64: 41.2 (33.5), taken 41.6)
 // of one layer with weights from memory, rows 1 / 4 / 8 / 16: 8192 -> 28672 47.6 / 48.0 / 53.4 / 64.0 (tiles
 //   of 64 x 128 59-60); 4096 -> 14336 16.7 / 16.2 / 17.6 / 20.3; 4096 -> 128256 92 / 94 / 104 / 126 (102-103)
 double fp8_rows_us(double steps, int rb, int b, bool grouped) {
@@ -178,11 +180,12 @@ double fp8_memory_us(int n, int m) { return 4.0 + (double)n * m / 5.1e6; }
 // The 8-bit floating-point product of one layer (experts 0) or of experts' rows:
 //   * fast sums of more than 128 rows of one layer with more than 128 tiles of 256 x 256 (fewer
 //     rows leave half of each tile empty: 4096 -> 128256, 128 rows 125 against 111 by 128 x 128,
-//     129 rows 123 against 158): those tiles, which take half the records from the L2s that 128 x 128 ones do (16 TB/s of them were that
-//     kernel's limit: 8192 x 8192 -> 8192 487 us against 377); their last round is cut
-//     smaller where the tiles left over are few: 4608 x 4608 -> 12288 (96 of 864 left)
-//     212 whole, 204 in halves, 216 in quarters; 4096 x 1152 -> 4608 (32 of 288) 36.5,
-//     31.5, 29.1; 4608 x 3072 -> 9216 (136 of 648) 112, 125, 132;
+//     129 rows 123 against 158): those tiles, which take half the records from the L2s that
+//     128 x 128 ones do (8192 x 8192 -> 8192 487 us against 377; these times without an
+//     activation); their last round is cut smaller where the tiles left over are few:
+//     4608 x 4608 -> 12288 (96 of 864 left) 212 whole, 204 in halves, 216 in quarters;
+//     4096 x 1152 -> 4608 (32 of 288) 36.5, 31.5, 29.1; 4608 x 3072 -> 9216 (136 of 648)
+//     112, 125, 132;
 //   * the same for experts of 1024 rows on average and more (8 experts, 4096 -> 4096,
 //     mean 2048: 314 by 128 x 128, 252; 1024: 150, 143; 512: 82, 95; 1152 -> 4608, mean
 //     1024: 59.5, 56.7): below, half-empty last row blocks cost more;
