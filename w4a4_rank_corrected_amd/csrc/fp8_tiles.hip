@@ -436,8 +436,9 @@ __device__ __forceinline__ void tile_at(int u, int tiles_m, int tiles_n, int& ti
   ti = band * 8 + in - tj * high;
 }
 
-// Tiles of 256 x 256 by the 8-bit instruction (fast sums), one workgroup a CU, for whole rounds of the CUs; the tiles left
-// over are cut into PARTS of 256 x 128 or 128 x 128, so that the last round takes every
+// Tiles of 256 x 256 by the 8-bit instruction (fast sums; the decoded operands of exact
+// ones have no registers left), one workgroup a CU, for whole rounds of the CUs; the tiles
+// left over are cut into PARTS of 256 x 128 or 128 x 128, so that the last round takes every
 // CU for the time of a part.  A step takes 2870 cycles, 2048 of them its multiplications'
 // (LDS reads and the barrier the rest); before the first step and behind the last one
 // nothing multiplies, 3000 and 4000 cycles without an activation: 8192 x 8192 -> 8192
@@ -556,7 +557,7 @@ __global__ __launch_bounds__(256) void fp8_tile_kernel(Fp8Args a, int tiles_m, i
     }
   }
   tile<4, 2, 2, EXACT, OUT_BF16, GROUPED, PIECES>(a, qx, ascale, qw, wscale, bias, G, i0, j0, row_end, s_even, s_odd,
-                                                s_scale_even, s_scale_odd, sums);
+                                                  s_scale_even, s_scale_odd, sums);
 }
 
 // Tiles of 64 x 128, three workgroups a CU, where those of 128 x 128 leave CUs idle: half
@@ -572,7 +573,7 @@ __global__ __launch_bounds__(256) void fp8_small_kernel(Fp8Args a, int tiles_m, 
   int ti, tj;
   tile_at(xcd_range((int)blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, ti, tj);
   tile<2, 2, 2, EXACT, OUT_BF16, false, false>(a, a.qx, a.ascale, a.qw, a.wscale, a.bias, a.G, ti * 64, tj * 128, a.b,
-                                             s_even, s_odd, s_scale_even, s_scale_odd, nullptr);
+                                               s_even, s_odd, s_scale_even, s_scale_odd, nullptr);
 }
 
 // The pieces' sums of a tile added in their order, the bias, and the rest.  A workgroup
